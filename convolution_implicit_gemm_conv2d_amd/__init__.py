@@ -5,7 +5,9 @@ kernels of ``libconvmi.so``.  PyTorch provides device memory and the current
 stream.  The low-level functions carry the C names and arguments;
 ``conv2d``, ``conv2d_input_grad``, ``conv2d_weight_grad``, ``conv1d`` and
 ``conv2d_transposed`` derive the sizes from tensor shapes and allocate the
-output (and the weight gradient's workspace, when none is given).
+output (and the weight gradient's workspace, when none is given).  The
+operators around a convolution (gated feed-forward, block norms, gradient
+clipping) are in ``block`` and exported here.
 """
 from __future__ import annotations
 
@@ -440,3 +442,9 @@ def conv2d_weight_grad(x, dy, w_shape, stride=1, padding=0, dilation=1, groups=1
     conv_bwd_dw_ex(x, dy, out, workspace, workspace.numel() * workspace.element_size(), N, C, H, W,
                    C_out, KH, KW, sh, sw, ph, pw, dh, dw_, groups, lay, dt, code, stream)
     return out
+
+
+from .block import *  # noqa: E402,F401,F403  (uses the helpers above)
+from .block import __all__ as _block_all  # noqa: E402
+
+__all__ += _block_all

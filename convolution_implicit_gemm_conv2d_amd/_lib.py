@@ -12,6 +12,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)),
                         else "libconvmi.so")
 
 _I = ctypes.c_int
+_L = ctypes.c_longlong
 _P = ctypes.c_void_p
 
 # Name -> (restype, argtypes), mirroring include/convmi.h.
@@ -34,6 +35,18 @@ SIGNATURES = {
     "conv_bwd_dw_ex": (_I, [_P, _P, _P, _P, ctypes.c_size_t] + _GEOM + [_I, _P]),
     "conv_bwd_dw_workspace_size": (_I, _GEOM + [_I, ctypes.POINTER(ctypes.c_size_t)]),
     "conv_bwd_dw_noalloc": (_I, [_P, _P, _P] + _GEOM + [_P]),
+    # x w_gate w_up b_gate b_up h saved, rows C F act dtype
+    "conv_gated_fwd": (_I, [_P] * 7 + [_L, _I, _I, _I, _I, _P]),
+    "conv_gated_bwd": (_I, [_P] * 13 + [ctypes.c_size_t, _L, _I, _I, _I, _I, _P]),
+    "conv_gated_bwd_workspace_size": (_I, [_L, _I, _I, _I, ctypes.POINTER(ctypes.c_size_t)]),
+    # ..., rows C gate_rows post pre act eps dtype
+    "conv_block_norm_fwd": (_I, [_P] * 10 + [_L, _I, _L, _I, _I, _I, ctypes.c_float, _I, _P]),
+    "conv_block_norm_bwd": (_I, [_P] * 19 + [ctypes.c_size_t, _L, _I, _L, _I, _I, _I, ctypes.c_float, _I, _P]),
+    "conv_block_norm_bwd_workspace_size": (_I, [_L, _I, _L, ctypes.POINTER(ctypes.c_size_t)]),
+    # host arrays: pointers, element counts, dtypes
+    "conv_grad_norm": (_I, [_P, _P, _P, _I, _P, _P, ctypes.c_size_t, _P]),
+    "conv_grad_clip": (_I, [_P, _P, _P, _P, _I, ctypes.c_float, ctypes.c_float, _P, _P, ctypes.c_size_t, _P]),
+    "conv_grad_workspace_size": (_I, [_I, ctypes.POINTER(ctypes.c_size_t)]),
     "conv_path_name": (ctypes.c_char_p, [_I]),
     "conv_last_error": (ctypes.c_char_p, []),
     "conv_arm_launch_events": (_I, [_P, _P]),

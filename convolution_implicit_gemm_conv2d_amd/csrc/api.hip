@@ -44,6 +44,9 @@ namespace {
 
 thread_local std::string t_last_error;
 
+}  // namespace
+
+namespace convmi {
 int fail(int code, const char* fmt, ...)
 {
     char buf[512];
@@ -54,6 +57,11 @@ int fail(int code, const char* fmt, ...)
     t_last_error = buf;
     return code;
 }
+}  // namespace convmi
+
+namespace {
+
+using convmi::fail;
 
 int64_t extent(int64_t in, int64_t k, int64_t stride, int64_t pad, int64_t dil)
 {

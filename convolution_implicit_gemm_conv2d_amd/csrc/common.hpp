@@ -156,6 +156,41 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((float2_t{lo, hi}), bf16x2_t));
 }
 
+// Sixteen bytes at any element alignment: the target's global accesses take
+// unaligned addresses, so rows of odd length and odd offsets still load and
+// store whole vectors.
+typedef uint32_t uint32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+__device__ __forceinline__ uint4 load16_any(const void* p)
+{
+    const uint32x4_any v = *static_cast<const uint32x4_any*>(p);
+    return make_uint4(v.x, v.y, v.z, v.w);
+}
+__device__ __forceinline__ void store16_any(void* p, uint4 v)
+{
+    uint32x4_any t;
+    t.x = v.x; t.y = v.y; t.z = v.z; t.w = v.w;
+    *static_cast<uint32x4_any*>(p) = t;
+}
+
+// Sum over the 64 lanes of a wave, the same in every lane.  Row shifts leave
+// each 16-lane row's sum in its last lane, two broadcasts carry it across
+// the rows to lane 63; the order is fixed, so the result is too.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_shift(float v)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xf, true));
+}
+__device__ __forceinline__ float wave_sum(float v)
+{
+    v += dpp_shift<0x111, 0xf>(v);
+    v += dpp_shift<0x112, 0xf>(v);
+    v += dpp_shift<0x114, 0xf>(v);
+    v += dpp_shift<0x118, 0xf>(v);
+    v += dpp_shift<0x142, 0xa>(v);
+    v += dpp_shift<0x143, 0xc>(v);
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
+
 // Division by a runtime constant d >= 1 for dividends below 2^31, as a
 // multiply-high, an add and a shift (Granlund and Montgomery, "Division by
 // invariant integers using multiplication", 1994: with l = ceil(log2 d) and

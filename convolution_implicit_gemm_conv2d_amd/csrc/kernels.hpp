@@ -9,6 +9,9 @@ namespace convmi {
 // Compute units of the current device (queried once per device).
 int device_cu_count();
 
+// Records the message of a failed call on this thread; returns `code`.
+int fail(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+
 // Generic direct forward, any geometry, layout and dtype (dtype 0 fp32, 1 bf16).
 hipError_t launch_fwd_direct(const void* x, const void* w, const void* bias, void* y,
                              const Geom& g, int dtype, hipStream_t s);
@@ -79,5 +82,60 @@ hipError_t launch_dx_igemm(const void* dy, const void* w, const void* bias, void
 bool can_dx_band(const Geom& g, int dtype);
 hipError_t launch_dx_band(const void* dy, const void* w, const void* bias, void* dx,
                           const Geom& g, hipStream_t s);
+
+// Sums `pieces` rows of fp32 partials in row order (fixed-order tree), column
+// by column, and rounds once: column q * q_pitch + c goes to out[q][c] (a null
+// out[q] is skipped).  `pitch` is the row length of `part` in values.  With
+// no pieces the outputs become zero.
+constexpr int kSumOutputs = 6;
+struct SumArgs {
+    const float* part;
+    int64_t pitch;
+    int pieces;
+    int cols;
+    int dtype;
+    int q_pitch;          // distance of two q blocks within a row of `part`, in values
+    void* out[kSumOutputs];
+};
+hipError_t launch_column_sums(const SumArgs& a, int nq, hipStream_t s);
+
+// Norms before and after a block with gate and residual scale (see
+// conv_block_norm_fwd / conv_block_norm_bwd in include/convmi.h).
+struct NormArgs {
+    const void *dy, *da;                          // backward only
+    const void *x, *f, *z, *s;                    // stream, branch, gate, scale
+    const void *post_w, *post_b, *pre_w, *pre_b;
+    void *y, *a;                                  // forward
+    void *dx, *df, *dz, *ds, *dpost_w, *dpost_b, *dpre_w, *dpre_b;
+    float* part;                                  // fp32 partial sums
+    int64_t rows, gate_rows;                      // gate_rows: rows that share one gate row
+    int C;
+    int post, pre, act;
+    float eps;
+};
+hipError_t launch_norm_fwd(const NormArgs& a, int dtype, hipStream_t s);
+hipError_t launch_norm_bwd(const NormArgs& a, int dtype, hipStream_t s);
+size_t norm_bwd_workspace(int64_t rows, int64_t gate_rows, int C, int has_gate);
+
+// Gated feed-forward layer (see conv_gated_fwd / conv_gated_bwd).
+struct GatedArgs {
+    const void *dh, *x, *wg, *wu, *bg, *bu;
+    float* saved;
+    void *h, *dx, *dwg, *dwu, *dbg, *dbu;
+    void* workspace;
+    int64_t rows;
+    int C, F, act;
+};
+hipError_t launch_gated_fwd(const GatedArgs& a, int dtype, hipStream_t s);
+hipError_t launch_gated_bwd(const GatedArgs& a, int dtype, hipStream_t s);
+size_t gated_bwd_workspace(int64_t rows, int C, int F, int dtype);
+
+// Global norm of a list of gradients and clipping by it.
+constexpr int kClipMaxBlocks = 2048;   // partials of one list of up to kClipTensors tensors
+constexpr int kClipTensors = 128;      // tensors one launch takes (its table is a kernel argument)
+size_t clip_workspace(int n);
+// `dst` null: the norm only.
+hipError_t launch_clip(const void* const* src, void* const* dst, const size_t* counts, const int* dtypes, int n,
+                       float max_norm, float eps, float* norm, void* workspace, hipStream_t s);
 
 }  // namespace convmi

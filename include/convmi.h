@@ -347,6 +347,158 @@ const char *conv_path_name(int path);
  */
 int conv_arm_launch_events(void *start, void *stop);
 
+/* ------------------------------------------------------------------------
+ * Operators around a convolution: the gated feed-forward layer, the norms
+ * before and after a block, and the gradients' global norm.  They work on
+ * channels-last rows: an NHWC image batch is N*H*W rows of C channels, an NLC
+ * sequence batch N*L rows, a batch of tokens one row each.  Ownership,
+ * execution and error reporting are as above; `rows` may be 0 (nothing is
+ * read, parameter gradients become zero).  Tensors are dense; pointers need
+ * the alignment of their elements only, and 16-byte alignment with row
+ * lengths that are multiples of 8 (bf16) is the fast case.  Accumulation,
+ * statistics and activations are in fp32 (the squares of conv_grad_norm in
+ * fp64); each output is rounded once.
+ */
+
+/* Activations: t, 1/(1+exp(-t)), t/(1+exp(-t)), t Phi(t) with Phi the normal
+ * distribution function, its tanh form 0.5 t (1 + tanh(sqrt(2/pi) (t +
+ * 0.044715 t^3))), max(t, 0) (derivative 0 at 0), tanh(t). */
+typedef enum conv_act {
+    CONV_ACT_NONE = 0,
+    CONV_ACT_SIGMOID = 1,
+    CONV_ACT_SILU = 2,
+    CONV_ACT_GELU = 3,
+    CONV_ACT_GELU_TANH = 4,
+    CONV_ACT_RELU = 5,
+    CONV_ACT_TANH = 6
+} conv_act_t;
+
+typedef enum conv_norm { CONV_NORM_NONE = 0, CONV_NORM_RMS = 1, CONV_NORM_LAYER = 2 } conv_norm_t;
+
+/*
+ * Gated feed-forward layer: two 1x1 convolutions of the same input, one
+ * through an activation, multiplied, in one kernel:
+ *   g = x w_gate^T + b_gate,  u = x w_up^T + b_up,  h = act(g) * u.
+ *   x [rows, C], w_gate and w_up [F, C] (a 1x1 OHWI weight), b_gate and b_up
+ *   [F] or NULL (both or neither), h [rows, F].
+ *   saved : fp32 [rows, 2F] that receives g (first F of a row) and u, for
+ *           conv_gated_bwd; NULL to keep nothing.
+ * C, F >= 1; dtype CONV_F32 or CONV_BF16 for every tensor but `saved`.
+ * Errors: CONV_ERR_INVALID_ARG (a null or misaligned pointer, a size or enum
+ * out of range), CONV_ERR_OVERFLOW (C or F above 2^20, or rows above 2^31 - 1),
+ * CONV_ERR_HIP.
+ */
+int conv_gated_fwd(const void *x, const void *w_gate, const void *w_up,
+                   const void *b_gate, const void *b_up, void *h,
+                   float *saved, long long rows, int C, int F, int act,
+                   int dtype, void *stream);
+
+/*
+ * Gradient of conv_gated_fwd from dh [rows, F]:
+ *   dg = dh u act'(g), du = dh act(g);  dx = dg w_gate + du w_up;
+ *   dw_gate = dg^T x, dw_up = du^T x;  db_gate, db_up: column sums of dg, du.
+ * g and u come from `saved` (as conv_gated_fwd wrote it) or, when that is
+ * NULL, are computed again.  dg and du are rounded to dtype once, as operands
+ * of the products.  Any output may be NULL; b_gate and b_up as in the forward
+ * call (unused with `saved`).
+ *   workspace : 16-byte aligned, at least conv_gated_bwd_workspace_size bytes.
+ * Errors as conv_gated_fwd, and CONV_ERR_INVALID_ARG for the workspace.
+ */
+int conv_gated_bwd(const void *dh, const void *x, const void *w_gate,
+                   const void *w_up, const void *b_gate, const void *b_up,
+                   const float *saved, void *dx, void *dw_gate, void *dw_up,
+                   void *db_gate, void *db_up, void *workspace,
+                   size_t workspace_bytes, long long rows, int C, int F,
+                   int act, int dtype, void *stream);
+
+/* Workspace bytes of conv_gated_bwd for these sizes.  Host only. */
+int conv_gated_bwd_workspace_size(long long rows, int C, int F, int dtype,
+                                  size_t *bytes);
+
+/*
+ * Norms around a block with its gate and residual scale, in one pass:
+ *   n = post(branch),  y = x + scale * act(gate) * n,  a = pre(y),
+ *   rms:   v / sqrt(mean(v^2) + eps) * w
+ *   layer: (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) * w + b
+ * over the C channels of each row: `post` is the norm after the block that
+ * made `branch`, `pre` the norm before the next one.
+ *   x, branch, y, a [rows, C].  branch NULL: y = x (a norm alone).
+ *   gate : [rows / gate_rows, C], each row shared by gate_rows consecutive
+ *          rows (1: a gate for every element; H*W: one for each image);
+ *          gate_rows divides rows.  NULL: no gate.
+ *   scale, pre_w, post_w [C]: NULL for ones.  pre_b, post_b [C]: NULL for
+ *   zeros, and only with a layer norm.
+ *   y or a may be NULL, not both; a needs pre other than CONV_NORM_NONE.
+ * Errors: CONV_ERR_INVALID_ARG (a null or misaligned pointer; a size, enum or
+ * eps <= 0 out of range; a gate, scale or post norm without a branch),
+ * CONV_ERR_OVERFLOW (C above 2^20 or rows above 2^31 - 1), CONV_ERR_HIP.
+ */
+int conv_block_norm_fwd(const void *x, const void *branch, const void *gate,
+                        const void *scale, const void *post_w,
+                        const void *post_b, const void *pre_w,
+                        const void *pre_b, void *y, void *a, long long rows,
+                        int C, long long gate_rows, int post, int pre,
+                        int act, float eps, int dtype, void *stream);
+
+/*
+ * Gradient of conv_block_norm_fwd from dy and da [rows, C] (the gradients of
+ * y and a; either may be NULL for zeros, not both; da needs a pre norm).
+ * Works from the forward inputs; y and the statistics are computed again.
+ *   dx, dbranch [rows, C], dgate (the gate's shape, summed over the rows that
+ *   share a gate row), dscale, dpost_w, dpost_b, dpre_w, dpre_b [C]: any may
+ *   be NULL.
+ *   workspace : 16-byte aligned, at least conv_block_norm_bwd_workspace_size
+ *   bytes.
+ * Errors as conv_block_norm_fwd, and CONV_ERR_INVALID_ARG for the workspace.
+ */
+int conv_block_norm_bwd(const void *dy, const void *da, const void *x,
+                        const void *branch, const void *gate,
+                        const void *scale, const void *post_w,
+                        const void *post_b, const void *pre_w,
+                        const void *pre_b, void *dx, void *dbranch,
+                        void *dgate, void *dscale, void *dpost_w,
+                        void *dpost_b, void *dpre_w, void *dpre_b,
+                        void *workspace, size_t workspace_bytes,
+                        long long rows, int C, long long gate_rows, int post,
+                        int pre, int act, float eps, int dtype, void *stream);
+
+/* Workspace bytes of conv_block_norm_bwd.  gate_rows as in the call, 0 for no
+ * gate.  Host only. */
+int conv_block_norm_bwd_workspace_size(long long rows, int C,
+                                       long long gate_rows, size_t *bytes);
+
+/*
+ * Global norm of a list of gradients: norm = sqrt(sum over tensors of the sum
+ * of g^2), one fp32 value on the device.
+ *   grads, counts, dtypes : host arrays of n device pointers, element counts
+ *   (a count of 0 is skipped) and conv_dtype_t values; read before the call
+ *   returns.  n >= 0.
+ *   workspace : 16-byte aligned, at least conv_grad_workspace_size(n) bytes.
+ * Errors: CONV_ERR_INVALID_ARG (a null or misaligned pointer, n < 0, a bad
+ * dtype, the workspace), CONV_ERR_OVERFLOW (a count of 2^46 or more),
+ * CONV_ERR_HIP.
+ */
+int conv_grad_norm(const void *const *grads, const size_t *counts,
+                   const int *dtypes, int n, float *norm, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
+/*
+ * Clipping by the global norm: c = min(1, max_norm / (norm + eps)) and
+ * outs[i] = c * grads[i] (outs[i] may be grads[i]; it must not overlap
+ * another gradient).  The norm before clipping goes to `norm` unless that is
+ * NULL; nothing is read back to the host.  A norm that is not finite gives c
+ * by the same formula (0 or NaN).  max_norm >= 0, eps >= 0.
+ * Errors as conv_grad_norm.
+ */
+int conv_grad_clip(const void *const *grads, void *const *outs,
+                   const size_t *counts, const int *dtypes, int n,
+                   float max_norm, float eps, float *norm, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of conv_grad_norm and conv_grad_clip for n tensors.  Host
+ * only. */
+int conv_grad_workspace_size(int n, size_t *bytes);
+
 /* Message describing the last failure on the calling thread ("" if none). */
 const char *conv_last_error(void);
 
