@@ -67,6 +67,13 @@ __device__ __forceinline__ void wait_vm()
     __builtin_amdgcn_s_waitcnt((VM & 15) | (0x7 << 4) | (0xf << 8) | ((VM >> 4) << 14));
 }
 
+// The same, and every LDS access of the wave done.
+template <int VM>
+__device__ __forceinline__ void wait_vm_lds()
+{
+    __builtin_amdgcn_s_waitcnt((VM & 15) | (0x7 << 4) | ((VM >> 4) << 14));
+}
+
 // 16-byte buffer-to-LDS load: lane i of the wave writes the 16 bytes at
 // buffer byte `voffset` (zeros at or past the buffer's end) to LDS address
 // lds_base + 16 i.  It is issued as inline assembly so that the compiler does

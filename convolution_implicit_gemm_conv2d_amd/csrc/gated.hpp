@@ -1,0 +1,41 @@
+// Shared by the gated feed-forward layer's bf16 and fp32 kernels: the plan of
+// the gradient's workspace and the entry points of either type.
+#pragma once
+
+#include "act.hpp"
+#include "kernels.hpp"
+
+namespace convmi {
+
+// The gradient's workspace: dg and du as rows [2 * Fp] of the type (Fp: F
+// rounded up so that a K tile never holds both), partial column sums of dg and
+// du, and fp32 partials of the weight gradients when their sum over the rows
+// is cut into pieces.
+struct GatedPlan {
+    int Fp;
+    int sum_rows;          // partial rows of the column sums, [2][Fp] each
+    int pieces;            // of the weight gradients' sum; 1: no partials
+    int64_t per;           // rows of a piece
+    size_t d_bytes, sum_bytes, part_bytes;
+    size_t total() const { return d_bytes + sum_bytes + part_bytes; }
+};
+inline size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+hipError_t gated_fwd_bf16(const GatedArgs& a, hipStream_t s);
+hipError_t gated_bwd_bf16(const GatedArgs& a, hipStream_t s);
+GatedPlan gated_plan_bf16(int64_t rows, int C, int F);
+hipError_t gated_fwd_f32(const GatedArgs& a, hipStream_t s);
+hipError_t gated_bwd_f32(const GatedArgs& a, hipStream_t s);
+GatedPlan gated_plan_f32(int64_t rows, int C, int F);
+
+// dg and du from kept projections: d[row] = [dg | du], with partial column
+// sums of `chunk` rows each when sums is not null.
+hipError_t launch_gated_kept(const GatedArgs& a, void* d, float* sums, int Fp, int chunks, int64_t chunk, int dtype,
+                             hipStream_t s);
+int gated_kept_chunks(int64_t rows, int Fp, int64_t* chunk);
+// The bias gradients from partial column sums.
+hipError_t launch_gated_bias_sums(const GatedArgs& a, const float* sums, int rows, int Fp, int dtype, hipStream_t s);
+// The weight gradients from `pieces` partials [2F][C].
+hipError_t launch_gated_weight_sums(const GatedArgs& a, const float* part, int pieces, int dtype, hipStream_t s);
+
+}  // namespace convmi

@@ -92,9 +92,9 @@ struct SumArgs {
     const float* part;
     int64_t pitch;
     int pieces;
-    int cols;
+    int64_t cols;
     int dtype;
-    int q_pitch;          // distance of two q blocks within a row of `part`, in values
+    int64_t q_pitch;      // distance of two q blocks within a row of `part`, in values
     void* out[kSumOutputs];
 };
 hipError_t launch_column_sums(const SumArgs& a, int nq, hipStream_t s);

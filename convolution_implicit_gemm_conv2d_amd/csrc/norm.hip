@@ -619,7 +619,7 @@ __global__ __launch_bounds__(kSumThreads) void column_sums_kernel(SumArgs a)
 {
     __shared__ float sums[kSumThreads / 64][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int c = blockIdx.x * 64 + lane;
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 64 + lane;
     T* out = static_cast<T*>(a.out[blockIdx.y]);
     if (!out) return;
     float acc = 0.f;
@@ -724,7 +724,7 @@ hipError_t bwd(const NormArgs& a, hipStream_t s)
 
 hipError_t launch_column_sums(const SumArgs& a, int nq, hipStream_t s)
 {
-    const dim3 grid((a.cols + 63) / 64, nq);
+    const dim3 grid(static_cast<unsigned>((a.cols + 63) / 64), nq);
     return a.dtype ? launch(column_sums_kernel<bf16_t>, grid, dim3(kSumThreads), 0, s, a)
                    : launch(column_sums_kernel<float>, grid, dim3(kSumThreads), 0, s, a);
 }

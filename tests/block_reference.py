@@ -18,8 +18,8 @@ def half_step(dtype):
     return torch.finfo(dtype).eps / 2
 
 
-def within(name, got, ref, mag, n, extra=0.0):
-    """|got - ref| <= half a step of |ref| + (n 2^-24 + extra) mag, element by
+def within(name, got, ref, mag, n, also=0.0):
+    """|got - ref| <= half a step of |ref| + n 2^-24 mag + also, element by
     element; NaN and infinities must agree.  Half a step of the smallest
     normal covers results below it."""
     assert got.shape == ref.shape, (name, got.shape, ref.shape)
@@ -28,7 +28,7 @@ def within(name, got, ref, mag, n, extra=0.0):
     assert torch.equal(torch.isnan(g), torch.isnan(r)), f"{name}: NaN in other places"
     assert torch.equal(g[~fine & ~torch.isnan(r)], r[~fine & ~torch.isnan(r)]), f"{name}: infinities differ"
     m = mag.detach().cpu().double().expand_as(r)
-    tol = half_step(got.dtype) * r.abs() + (n * U32 + extra) * (m + r.abs()) + torch.finfo(got.dtype).tiny
+    tol = half_step(got.dtype) * r.abs() + n * U32 * (m + r.abs()) + also + torch.finfo(got.dtype).tiny
     over = ((g - r).abs() / tol)[fine]
     if over.numel():
         worst = over.max().item()
