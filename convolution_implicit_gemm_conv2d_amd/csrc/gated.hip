@@ -363,6 +363,7 @@ __global__ __launch_bounds__(S::kThreads) void gated_product_kernel(Product a)
             }
             __syncthreads();
         }
+        with_act(a.act, [&](auto kind) __attribute__((always_inline)) {
 #pragma unroll
         for (int m = 0; m < S::TQ / 2; ++m) {
             const int base = (wq * (S::TQ / 2) + m) * 32;
@@ -399,7 +400,7 @@ __global__ __launch_bounds__(S::kThreads) void gated_product_kernel(Product a)
                         }
                         float h[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) h[e] = act_value(a.act, g[e]) * u[e];
+                        for (int e = 0; e < 4; ++e) h[e] = act_value<kind()>(g[e]) * u[e];
                         *reinterpret_cast<uint2*>(at) = make_uint2(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]));
                     } else {
                         const uint2 raw = *reinterpret_cast<const uint2*>(at);
@@ -408,7 +409,7 @@ __global__ __launch_bounds__(S::kThreads) void gated_product_kernel(Product a)
                         float dg[4], du[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const ActPair p = act_pair(a.act, g[e]);
+                            const ActPair p = act_pair<kind()>(g[e]);
                             dg[e] = dh[e] * u[e] * p.d;
                             du[e] = dh[e] * p.v;
                             sg[4 * v + e] += dg[e];
@@ -432,6 +433,7 @@ __global__ __launch_bounds__(S::kThreads) void gated_product_kernel(Product a)
                 }
             }
         }
+        });
         __syncthreads();
         if constexpr (MODE == kFwd) {
             store_tile<U, S::kThreads>(ring, S::BM, a.F - q0, [&](int r) { return r < rows_left ? a.h + (p0 + r) * a.F + q0 : nullptr; });

@@ -52,6 +52,7 @@ __global__ __launch_bounds__(kThreads) void gated_kept_kernel(const T* __restric
     const int n = F - f;
     const int64_t r0 = blockIdx.y * chunk, r1 = min(rows, r0 + chunk);
     float sg[4] = {}, su[4] = {};
+    with_act(act, [&](auto kind) __attribute__((always_inline)) {
     if (f < Fp) {
 #pragma unroll 2
         for (int64_t r = r0 + wave; r < r1; r += 4) {
@@ -61,7 +62,7 @@ __global__ __launch_bounds__(kThreads) void gated_kept_kernel(const T* __restric
             load4(saved + r * 2 * F + F + f, n, u);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const ActPair p = act_pair(act, g[e]);
+                const ActPair p = act_pair<kind()>(g[e]);
                 dg[e] = e < n ? h[e] * u[e] * p.d : 0.f;
                 du[e] = e < n ? h[e] * p.v : 0.f;
                 sg[e] += dg[e];
@@ -71,6 +72,7 @@ __global__ __launch_bounds__(kThreads) void gated_kept_kernel(const T* __restric
             put4(d + r * 2 * Fp + Fp + f, du);
         }
     }
+    });
     if (!sums) return;
     joined[wave][0][lane] = make_float4(sg[0], sg[1], sg[2], sg[3]);
     joined[wave][1][lane] = make_float4(su[0], su[1], su[2], su[3]);

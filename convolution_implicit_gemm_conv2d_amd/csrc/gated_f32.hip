@@ -156,6 +156,7 @@ __global__ __launch_bounds__(kThreads) void gated_f32_kernel(Product a)
 
     // A lane holds columns 8v + 4q + {0..3} of a q tile and p row `col`.
     if constexpr (kGated) {
+        with_act(a.act, [&](auto kind) __attribute__((always_inline)) {
 #pragma unroll
         for (int v = 0; v < 4; ++v)
 #pragma unroll
@@ -170,9 +171,9 @@ __global__ __launch_bounds__(kThreads) void gated_f32_kernel(Product a)
                     if (r >= a.rows || f >= a.F) continue;
                     if (MODE == kFwd) {
                         if (a.saved) a.saved[r * 2 * a.F + f] = g, a.saved[r * 2 * a.F + a.F + f] = u;
-                        a.h[r * a.F + f] = act_value(a.act, g) * u;
+                        a.h[r * a.F + f] = act_value<kind()>(g) * u;
                     } else {
-                        const ActPair p = act_pair(a.act, g);
+                        const ActPair p = act_pair<kind()>(g);
                         const float dh = a.dh[r * a.F + f], dg = dh * u * p.d, du = dh * p.v;
                         a.d_out[r * 2 * a.Fp + f] = dg;
                         a.d_out[r * 2 * a.Fp + a.Fp + f] = du;
@@ -194,6 +195,7 @@ __global__ __launch_bounds__(kThreads) void gated_f32_kernel(Product a)
                         }
                 }
             }
+        });
     } else {
 #pragma unroll
         for (int j = 0; j < TP; ++j) {

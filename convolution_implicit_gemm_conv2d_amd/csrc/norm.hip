@@ -168,6 +168,18 @@ __device__ __forceinline__ void store_row(T* p, const Part<VPT>& part, const flo
         if (part.cnt[i] > 0) store8(p + part.at[i], part.cnt[i], v[i]);
 }
 
+// v *= act(z).
+template <int VPT>
+__device__ __forceinline__ void times_act(int act, const float (&z)[VPT][kVec], float (&v)[VPT][kVec])
+{
+    with_act(act, [&](auto kind) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) v[i][e] *= act_value<kind()>(z[i][e]);
+    });
+}
+
 // Normalises a row in place and returns r; channels past the row stay 0.
 template <bool ONE, int VPT>
 __device__ __forceinline__ float normalise(int kind, const Part<VPT>& part, float inv_c, float eps, RowSum& rs,
@@ -227,10 +239,7 @@ __global__ __launch_bounds__(ONE ? 256 : 512) void norm_fwd_kernel(NormArgs k)
             }
             if (z) {
                 load_row(z + r / k.gate_rows * k.C, part, w);
-#pragma unroll
-                for (int i = 0; i < VPT; ++i)
-#pragma unroll
-                    for (int e = 0; e < kVec; ++e) n[i][e] *= act_value(k.act, w[i][e]);
+                times_act(k.act, w, n);
             }
             load_param(static_cast<const T*>(k.s), part, 1.f, w);
 #pragma unroll
@@ -356,10 +365,7 @@ __global__ __launch_bounds__(ONE ? 256 : 512) void norm_bwd_kernel(NormArgs k, P
                 load_param(static_cast<const T*>(k.s), part, 1.f, g);
                 if (z) {
                     load_row(z + r / k.gate_rows * k.C, part, w);
-#pragma unroll
-                    for (int i = 0; i < VPT; ++i)
-#pragma unroll
-                        for (int e = 0; e < kVec; ++e) g[i][e] *= act_value(k.act, w[i][e]);
+                    times_act(k.act, w, g);
                 }
                 float b[VPT][kVec];
                 load_param(static_cast<const T*>(k.post_w), part, 1.f, w);
@@ -412,15 +418,17 @@ __global__ __launch_bounds__(ONE ? 256 : 512) void norm_bwd_kernel(NormArgs k, P
                 float t[VPT][kVec], s[VPT][kVec];
                 load_row(z + r / k.gate_rows * k.C, part, t);
                 load_param(static_cast<const T*>(k.s), part, 1.f, s);
+                with_act(k.act, [&](auto kind) __attribute__((always_inline)) {
 #pragma unroll
                 for (int i = 0; i < VPT; ++i)
 #pragma unroll
                     for (int e = 0; e < kVec; ++e) {
-                        const ActPair p = act_pair(k.act, t[i][e]);
+                        const ActPair p = act_pair<kind()>(t[i][e]);
                         if (shared) sum[FULL ? kSumGate : 0][i][e] += v[i][e] * s[i][e] * p.d;
                         else t[i][e] = v[i][e] * s[i][e] * p.d;
                         sum[kSumScale][i][e] += v[i][e] * p.v;
                     }
+                });
                 if (!shared && dz) store_row(dz + r * k.C, part, t);
             } else {
 #pragma unroll
