@@ -39,7 +39,8 @@ typedef __attribute__((address_space(3))) bf16x8 lds_bf16x8;
 
 enum Mode { kFwd, kAgain, kDx, kDw };
 
-// WP x WQ waves, each TP x TQ tiles of 32x32; BK contraction values a stage.
+// WP x WQ waves, each TP x TQ tiles of 32x32; BK contraction values a stage,
+// NS stages in the ring.
 template <int WP_, int WQ_, int TP_, int TQ_, int BK_, int NS_>
 struct Shape {
     static constexpr int WP = WP_, WQ = WQ_, TP = TP_, TQ = TQ_, BK = BK_, NS = NS_;
@@ -48,7 +49,10 @@ struct Shape {
     static constexpr int kLds = NS * kStage;
     static constexpr int kPLoads = BM * BK / 8 / kThreads, kQLoads = BN * BK / 8 / kThreads;
     static constexpr int kLoads = kPLoads + kQLoads;
-    static_assert(BM * BN * 2 <= kLds, "an output tile fits in the ring");
+    static constexpr int kWaveLds = kStage / (WP * WQ);  // a wave's part of a stage
+    static constexpr int kPerCu = 163840 / kLds < 8 / (WP * WQ) ? 163840 / kLds : 8 / (WP * WQ);  // workgroups
+    static_assert(kWaveLds >= 4096, "a wave's output passes through its part of a stage");
+    static_assert(kPLoads > 0 && kQLoads > 0 && TQ % 2 == 0 && NS >= 2, "");
 };
 
 struct Product {
@@ -59,7 +63,7 @@ struct Product {
     float *saved, *sums, *part;
     int64_t rows, per;    // per: rows of a piece (dW)
     int C, F, Fp, act;
-    int p_tiles, q_tiles;
+    int p_tiles, q_tiles, tiles;  // tiles: of all pieces
 };
 
 // Where a 16-byte unit of a staged row sits.  Rows of BK values: 8 (or, with
@@ -69,66 +73,76 @@ template <int BK>
 __device__ __forceinline__ int swz_row(int r) { return BK == 64 ? (r & 7) : ((r >> 2) & 3); }
 __device__ __forceinline__ int swz_k(int k) { return ((k & 3) << 2) ^ (k & 2); }
 
+// The first n >= 1 of eight values, zeros after them.
 __device__ __forceinline__ uint4 guarded16(const bf16_t* p, int n)
 {
     if (n >= 8) return load16_any(p);
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (e < n) w[e >> 1] |= static_cast<uint32_t>(p[e]) << (16 * (e & 1));
+    for (int e = 0; e < 8; ++e) {
+        const uint32_t v = p[min(e, n - 1)];
+        w[e >> 1] |= (e < n ? v : 0u) << (16 * (e & 1));
+    }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Stages R rows of K-contiguous data: units of row r from base + r * ld.  Two
-// sources alternate every 32 rows when GATED.
-template <typename S, int R, bool GATED, bool FAST>
-struct RowStage {
-    static constexpr int kUnits = S::BK / 8, kN = R * kUnits / S::kThreads;
-    const bf16_t *src0, *src1;
-    int valid;            // rows of a source
-    int ld, K;
-    __device__ __forceinline__ void issue(int kt, char* lds, int i) const
+// Eight values at byte `off` of a buffer at any element alignment, none where
+// it is kOutside.  `ragged` (uniform: the last unit of some row is cut): the
+// first n of them by elements.  No branches but the uniform one.
+constexpr uint32_t kAll = 0x7ffffffcu;
+__device__ __forceinline__ uint4 unit_load(rsrc_t r, uint32_t off, bool ragged, int n)
+{
+    if (!ragged) return buffer_load16(r, off);
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        w[e >> 1] |= static_cast<uint32_t>(__builtin_amdgcn_raw_buffer_load_b16(r, e < n ? off + 2 * e : kOutside, 0, 0)) << (16 * (e & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Addresses of one operand's units for a thread: `off` within a tile (kOutside
+// where the tile's row or column does not exist) and the unit's contraction
+// offset.  ROWS: R rows of contraction values; otherwise BK rows of a
+// contraction index with R columns each.
+template <typename S, int R, bool ROWS>
+struct Units {
+    static constexpr int kN = R * S::BK / 8 / S::kThreads, kRow = ROWS ? S::BK / 8 : R / 8;
+    uint32_t off[kN];
+    // contraction offset (within a stage) of unit i of this thread
+    static __device__ __forceinline__ int k(int i)
     {
-        const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-        const int idx = i * S::kThreads + tid;
-        const int r = idx / kUnits, unit = (idx % kUnits) ^ swz_row<S::BK>(r);
-        const int k = kt * S::BK + unit * 8;
-        const int first = (i * S::kThreads + wave * 64) / kUnits;  // the wave's first row: one source a wave
-        const int which = GATED ? (first >> 5) & 1 : 0;
-        const int row = GATED ? (r >> 6) * 32 + (r & 31) : r;
-        const bf16_t* src = GATED && which ? src1 : src0;
-        if constexpr (FAST) {
-            const uint32_t bytes = (static_cast<uint32_t>(valid) * ld - kt * S::BK) * 2;
-            const uint32x4_t rs = dma_rsrc(src + kt * S::BK, valid > 0 ? bytes : 0u);
-            const uint32_t off = (static_cast<uint32_t>(row) * ld + unit * 8) * 2;
-            dma16(rs, k < K && row < valid ? off : kOutside, lds_addr(lds + (i * S::kThreads + wave * 64) * 16));
-        } else {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (row < valid && k < K) v = guarded16(src + static_cast<int64_t>(row) * ld + k, K - k);
-            *reinterpret_cast<uint4*>(lds + idx * 16) = v;
+        const int idx = i * S::kThreads + threadIdx.x, r = idx / kRow;
+        return ROWS ? ((idx % kRow) ^ swz_row<S::BK>(r)) * 8 : r;
+    }
+    // `valid` rows (ROWS) or columns of the tile exist.  GATED: two sources
+    // alternate every 32 rows.
+    template <bool GATED>
+    __device__ __forceinline__ void set(int valid, int ld)
+    {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const int idx = i * S::kThreads + threadIdx.x, r = idx / kRow;
+            if (ROWS) {
+                const int row = GATED ? (r >> 6) * 32 + (r & 31) : r;
+                off[i] = row < valid ? (static_cast<uint32_t>(row) * ld + k(i)) * 2u : kOutside;
+            } else {
+                const int c = ((idx % kRow) ^ swz_k(r)) * 8;
+                off[i] = c < valid ? (static_cast<uint32_t>(r) * ld + c) * 2u : kOutside;
+            }
         }
     }
-};
-
-// Stages BK rows of a contraction index, R columns from `src`; `cols` of them
-// exist, and `valid(kt)` rows.
-template <typename S, int R, bool FAST>
-struct ColStage {
-    static constexpr int kUnits = R / 8, kN = R * S::BK / 8 / S::kThreads;
-    __device__ __forceinline__ static void issue(const bf16_t* src, int valid, int ld, int cols, char* lds, int i)
+    // GATED: whether unit i of this wave comes from the second source.
+    static __device__ __forceinline__ int second(int i)
     {
-        const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-        const int idx = i * S::kThreads + tid;
-        const int k = idx / kUnits, unit = (idx % kUnits) ^ swz_k(k);
-        if constexpr (FAST) {
-            const uint32x4_t rs = dma_rsrc(src, valid > 0 ? (static_cast<uint32_t>(valid - 1) * ld + cols) * 2u : 0u);
-            const uint32_t off = (static_cast<uint32_t>(k) * ld + unit * 8) * 2;
-            dma16(rs, k < valid && unit * 8 < cols ? off : kOutside, lds_addr(lds + (i * S::kThreads + wave * 64) * 16));
-        } else {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (k < valid && unit * 8 < cols) v = guarded16(src + static_cast<int64_t>(k) * ld + unit * 8, cols - unit * 8);
-            *reinterpret_cast<uint4*>(lds + idx * 16) = v;
-        }
+        return (((i * S::kThreads + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 64) / kRow) >> 5) & 1;
+    }
+    // Values of unit i that exist, for the guarded loads.
+    __device__ __forceinline__ int count(int i, int k_left, int valid) const
+    {
+        if (off[i] == kOutside) return 0;
+        if (ROWS) return k_left - k(i);
+        const int idx = i * S::kThreads + threadIdx.x, r = idx / kRow;
+        return r < k_left ? valid - ((idx % kRow) ^ swz_k(r)) * 8 : 0;
     }
 };
 
@@ -172,61 +186,91 @@ struct ColFrag {
     }
 };
 
-// Writes a bf16 tile of `U` units a row from LDS to memory, whole units where
-// they fit.  `row(r)` gives the address of row r, or null.
-template <int U, int kThreads, typename F>
-__device__ __forceinline__ void store_tile(const char* lds, int rows, int cols, F row)
+// A wave's 32 output rows on their way from the accumulators' layout (a lane
+// holds columns 8v + 4q + {0..3} of row `lane & 31`) to rows in memory: through
+// the wave's own part of LDS, U units of 16 bytes a row, so that a store
+// instruction writes whole lines.  LDS serves a wave in order; only the
+// compiler has to keep the order too.
+__device__ __forceinline__ void wave_order()
 {
-    for (int idx = threadIdx.x; idx < rows * U; idx += kThreads) {
-        const int r = idx / U, unit = (idx % U) ^ (r & 7);
-        bf16_t* p = row(r);
-        const int n = cols - unit * 8;
-        if (!p || n <= 0) continue;
-        const uint4 v = *reinterpret_cast<const uint4*>(lds + idx * 16);
-        p += unit * 8;
-        if (n >= 8) {
-            store16_any(p, v);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+}
+template <int U>
+__device__ __forceinline__ int turn_at(int r, int unit) { return (r * U + (unit ^ ((r >> (U == 8 ? 1 : 2)) & (U - 1)))) * 16; }
+
+// `cols` columns of T exist from `p` (uniform) on, `rows` rows of pitch ld.
+template <int U, typename T>
+__device__ __forceinline__ void turn_out(const char* lds, T* p, uint32_t ld, int rows, int cols)
+{
+    constexpr int V = 16 / sizeof(T);
+    const int lane = threadIdx.x & 63;
+    const rsrc_t out = make_rsrc(p, kAll);
+    const bool ragged = cols < U * V && cols % V != 0;
+#pragma unroll
+    for (int i = 0; i < U / 2; ++i) {
+        const int r = (i * 64 + lane) / U, unit = lane % U, n = cols - unit * V;
+        const uint4 v = *reinterpret_cast<const uint4*>(lds + turn_at<U>(r, unit));
+        const uint32_t off = r < rows && n > 0 ? (r * ld + unit * V) * static_cast<uint32_t>(sizeof(T)) : kOutside;
+        if (!ragged) {
+            buffer_store16(out, off, v);
         } else {
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (e < n) p[e] = static_cast<bf16_t>(w[e >> 1] >> (16 * (e & 1)));
+            for (int e = 0; e < V; ++e) {
+                const uint32_t at = e < n && off != kOutside ? off + e * static_cast<uint32_t>(sizeof(T)) : kOutside;
+                if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1))), out, at, 0, 0);
+                else __builtin_amdgcn_raw_buffer_store_b32(w[e], out, at, 0, 0);
+            }
         }
     }
 }
-template <int U>
-__device__ __forceinline__ int tile_byte(int r, int unit, int half) { return (r * U + (unit ^ (r & 7))) * 16 + half * 8; }
 
-__device__ __forceinline__ void bias4(const bf16_t* b, int f, int F, float* v)
+// Four biases from column f on, zeros past F; `ragged` (uniform): some are past.
+__device__ __forceinline__ void bias4(const bf16_t* b, int f, int F, bool ragged, float* v)
 {
+    const rsrc_t r = make_rsrc(b, kAll);
+    if (!ragged) {
+        const uint2 t = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r, f * 2, 0, 0));
+        v[0] = __uint_as_float(t.x << 16); v[1] = __uint_as_float(t.x & 0xffff0000u);
+        v[2] = __uint_as_float(t.y << 16); v[3] = __uint_as_float(t.y & 0xffff0000u);
+    } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = b && f + e < F ? bf16_to_f(b[f + e]) : 0.f;
-}
-
-// Sums 16 values over the 32 lanes of a half wave; lane l of a half ends with
-// value (l & 15)'s sum (in bit-reversed halves: see `which`).
-__device__ __forceinline__ float half_sum16(float (&v)[16], int lane, int& which)
-{
-    which = 0;
-#pragma unroll
-    for (int s = 16, n = 8; n >= 1; s >>= 1, n >>= 1) {
-        const bool up = lane & s;
-        which += up ? n : 0;
-#pragma unroll
-        for (int i = 0; i < n; ++i) {
-            const float send = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
-            v[i] = keep + __shfl_xor(send, s);
-        }
+        for (int e = 0; e < 4; ++e) v[e] = bf16_to_f(__builtin_amdgcn_raw_buffer_load_b16(r, f + e < F ? (f + e) * 2 : kOutside, 0, 0));
     }
-    return v[0] + __shfl_xor(v[0], 1);
 }
 
-// Tile of a workgroup.  Workgroup b runs on XCD b mod 8: each XCD takes a
-// contiguous run of tiles, ordered so that eight p tiles share their q tiles.
-__device__ __forceinline__ void pick_tile(int b, int n, int p_tiles, int q_tiles, int& pt, int& qt, int& piece)
+// Sums 16 values over the 32 lanes of a half wave: in each step a lane gives
+// half of its values to a partner and keeps the other half.  A lane ends with
+// the sum of value half_sum_of(lane).
+__device__ __forceinline__ int half_sum_of(int lane) { return lane >> 1 & 15; }
+template <int CTRL, int N>
+__device__ __forceinline__ void half_sum_step(float* v, bool up)
 {
-    const int xcd = b & 7, per = n >> 3, rem = n & 7;
-    int t = xcd * per + min(xcd, rem) + (b >> 3);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float send = up ? v[i] : v[i + N], keep = up ? v[i + N] : v[i];
+        v[i] = keep + dpp_shift<CTRL, 0xf>(send);
+    }
+}
+__device__ __forceinline__ float half_sum16(float (&v)[16], int lane)
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        // swaps the odd rows of 16 lanes of one with the even ones of the other
+        const auto t = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[i]), __float_as_uint(v[i + 8]), false, false);
+        v[i] = __uint_as_float(t[0]) + __uint_as_float(t[1]);
+    }
+    half_sum_step<0x140, 4>(v, lane & 8);  // lane 15 - i of a row
+    half_sum_step<0x141, 2>(v, lane & 4);  // 7 - i of half a row
+    half_sum_step<0x4e, 1>(v, lane & 2);   // i ^ 2
+    return v[0] + dpp_shift<0xb1, 0xf>(v[0]);  // i ^ 1
+}
+
+// Tile t of the product.  Eight p tiles share their q tiles before the next
+// eight come.
+__device__ __forceinline__ void pick_tile(int t, int p_tiles, int q_tiles, int& pt, int& qt, int& piece)
+{
     const int tiles = p_tiles * q_tiles;
     piece = t / tiles;
     t -= piece * tiles;
@@ -238,62 +282,112 @@ __device__ __forceinline__ void pick_tile(int b, int n, int p_tiles, int q_tiles
 }
 
 template <typename S, int MODE, bool FAST>
-__global__ __launch_bounds__(S::kThreads) void gated_product_kernel(Product a)
+__global__ __launch_bounds__(S::kThreads, 2) void gated_product_kernel(Product a)
 {
     extern __shared__ char ring[];
     constexpr bool kGated = MODE == kFwd || MODE == kAgain;
     constexpr bool kPRows = MODE != kDw, kQRows = kGated;
     constexpr int kQTile = kGated ? S::BN / 2 : S::BN;  // output columns of a tile
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wp = wave / S::WQ, wq = wave % S::WQ;
     const int col = lane & 31, q = lane >> 5;
-    int pt, qt, piece;
-    pick_tile(blockIdx.x, gridDim.x, a.p_tiles, a.q_tiles, pt, qt, piece);
-    const int64_t p0 = static_cast<int64_t>(pt) * S::BM;
-    const int q0 = qt * kQTile;
+    const int p_ld = kGated ? a.C : 2 * a.Fp, q_ld = a.C;
 
-    // The contraction: K values from k0 on.
-    const int64_t m0 = MODE == kDw ? piece * a.per : 0;
-    const int64_t K = kGated ? a.C : MODE == kDx ? 2 * static_cast<int64_t>(a.Fp) : min(a.per, a.rows - m0);
-    const int nk = static_cast<int>((K + S::BK - 1) / S::BK);
-    const int rows_left = MODE == kDw ? 0 : static_cast<int>(min(static_cast<int64_t>(S::BM), a.rows - p0));
+    // Workgroup b runs on XCD b mod 8; an XCD takes a contiguous run of tiles,
+    // its workgroups take them in turn.
+    const int xcd = blockIdx.x & 7, per = a.tiles >> 3, rem = a.tiles & 7, step = gridDim.x >> 3;
+    const int first = xcd * per + min(xcd, rem) + (blockIdx.x >> 3);
+    const int end = xcd * per + min(xcd, rem) + per + (xcd < rem ? 1 : 0);
 
-    auto issue = [&](int kt, char* st, int i) __attribute__((always_inline)) {
-        if (i < S::kPLoads) {
-            if constexpr (kPRows) {
-                const int ld = kGated ? a.C : 2 * a.Fp;
-                RowStage<S, S::BM, false, FAST> rs{(kGated ? a.x : a.d) + p0 * ld, nullptr, rows_left, ld, static_cast<int>(K)};
-                rs.issue(kt, st, i);
-            } else {
-                const int64_t k = static_cast<int64_t>(kt) * S::BK;
-                ColStage<S, S::BM, FAST>::issue(a.d + (m0 + k) * 2 * a.Fp + p0, static_cast<int>(min(K - k, static_cast<int64_t>(S::BK))),
-                                                2 * a.Fp, static_cast<int>(2 * a.Fp - p0), st, i);
-            }
-        } else {
-            char* qs = st + S::kPBytes;
-            i -= S::kPLoads;
-            if constexpr (kQRows) {
-                const int64_t at = static_cast<int64_t>(q0) * a.C;
-                RowStage<S, S::BN, true, FAST> rs{a.wg + at, a.wu + at, min(kQTile, a.F - q0), a.C, a.C};
-                rs.issue(kt, qs, i);
-            } else if constexpr (MODE == kDx) {
-                const int k = kt * S::BK, up = k >= a.Fp, f = k - (up ? a.Fp : 0);
-                ColStage<S, S::BN, FAST>::issue((up ? a.wu : a.wg) + static_cast<int64_t>(f) * a.C + q0, min(a.F - f, S::BK), a.C, a.C - q0, qs, i);
-            } else {
-                const int64_t k = static_cast<int64_t>(kt) * S::BK;
-                ColStage<S, S::BN, FAST>::issue(a.x + (m0 + k) * a.C + q0, static_cast<int>(min(K - k, static_cast<int64_t>(S::BK))), a.C, a.C - q0, qs, i);
-            }
+    struct Tile {
+        int64_t p0, m0;  // first p row; first contraction index (dW)
+        int q0, K, pt, piece;
+    };
+    auto tile_of = [&](int t) __attribute__((always_inline)) {
+        Tile r;
+        int qt;
+        pick_tile(t, a.p_tiles, a.q_tiles, r.pt, qt, r.piece);
+        r.p0 = static_cast<int64_t>(r.pt) * S::BM;
+        r.q0 = qt * kQTile;
+        r.m0 = MODE == kDw ? r.piece * a.per : 0;
+        r.K = kGated ? a.C : MODE == kDx ? 2 * a.Fp : static_cast<int>(min(a.per, a.rows - r.m0));
+        return r;
+    };
+    auto stages = [](int K) __attribute__((always_inline)) { return max(1, (K + S::BK - 1) / S::BK); };
+
+    // The next stage to load: stage lk of tile lt.  Loads run ahead over the
+    // ends of tiles, so a tile's first stages arrive during the epilogue of the
+    // one before.
+    Units<S, S::BM, kPRows> pu;
+    Units<S, S::BN, kQRows> qu;
+    Tile load;
+    int lt = first, lk = 0, lstages = 0, p_valid = 0, q_valid = 0;
+    auto enter = [&]() __attribute__((always_inline)) {
+        load = tile_of(lt);
+        lk = 0;
+        lstages = stages(load.K);
+        p_valid = static_cast<int>(kPRows ? min(static_cast<int64_t>(S::BM), a.rows - load.p0) : 2 * a.Fp - load.p0);
+        q_valid = kQRows ? min(kQTile, a.F - load.q0) : a.C - load.q0;
+        pu.template set<false>(p_valid, p_ld);
+        qu.template set<kQRows>(q_valid, q_ld);
+    };
+    // Source of a stage's units, and how many contraction values are left.
+    auto p_source = [&](int& left) __attribute__((always_inline)) {
+        left = load.K - lk * S::BK;
+        const int64_t k = static_cast<int64_t>(lk) * S::BK;
+        return kPRows ? (kGated ? a.x : a.d) + load.p0 * p_ld + k : a.d + (load.m0 + k) * p_ld + load.p0;
+    };
+    auto q_source = [&](int second, int& left) __attribute__((always_inline)) {
+        int k = lk * S::BK;
+        left = load.K - k;
+        if (kQRows) return (second ? a.wu : a.wg) + static_cast<int64_t>(load.q0) * q_ld + k;
+        if (MODE == kDw) return a.x + (load.m0 + k) * q_ld + load.q0;
+        const bool up = k >= a.Fp;
+        k -= up ? a.Fp : 0;
+        left = a.F - k;
+        return (up ? a.wu : a.wg) + static_cast<int64_t>(k) * q_ld + load.q0;
+    };
+    auto bytes = [&](bool by_rows, int valid, int ld, int left) __attribute__((always_inline)) {
+        const uint32_t n = by_rows ? static_cast<uint32_t>(valid) * ld - lk * S::BK : static_cast<uint32_t>(min(left, S::BK) - 1) * ld + valid;
+        return left > 0 ? n * 2u : 0u;
+    };
+    auto issue = [&](int i, char* st) __attribute__((always_inline)) {
+        const bool is_p = i < S::kPLoads;
+        const int j = is_p ? i : i - S::kPLoads;
+        int left;
+        const bf16_t* src = is_p ? p_source(left) : q_source(kQRows ? qu.second(j) : 0, left);
+        const uint32x4_t rs = dma_rsrc(src, is_p ? bytes(kPRows, p_valid, p_ld, left) : bytes(kQRows, q_valid, q_ld, left));
+        const uint32_t off = (is_p ? pu.k(j) : qu.k(j)) < left ? (is_p ? pu.off[j] : qu.off[j]) : kOutside;
+        dma16(rs, off, lds_addr(st + (is_p ? 0 : S::kPBytes) + (j * S::kThreads + wave * 64) * 16));
+    };
+    // Rows of any length and alignment pass through registers.
+    uint4 held[FAST ? 1 : S::kLoads];
+    auto fetch = [&]() __attribute__((always_inline)) {
+        int left;
+#pragma unroll
+        for (int i = 0; i < (FAST ? 0 : S::kLoads); ++i) {
+            const bool is_p = i < S::kPLoads;
+            const int j = is_p ? i : i - S::kPLoads;
+            const bf16_t* src = is_p ? p_source(left) : q_source(kQRows ? qu.second(j) : 0, left);
+            const int n = is_p ? pu.count(j, left, p_valid) : qu.count(j, left, q_valid);
+            const bool ragged = (is_p ? kPRows : kQRows) ? left < S::BK && left % 8 != 0 : (is_p ? p_valid % 8 != 0 : q_valid % 8 != 0);
+            held[i] = unit_load(make_rsrc(src, kAll), n > 0 ? (is_p ? pu.off[j] : qu.off[j]) : kOutside, ragged, n);
         }
+    };
+    auto put = [&](char* st) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < (FAST ? 0 : S::kLoads); ++i) {
+            const int j = i < S::kPLoads ? i : i - S::kPLoads;
+            *reinterpret_cast<uint4*>(st + (i < S::kPLoads ? 0 : S::kPBytes) + (j * S::kThreads + threadIdx.x) * 16) = held[i];
+        }
+    };
+    auto advance = [&]() __attribute__((always_inline)) {
+        if (++lk < lstages) return;
+        lt += step;
+        if (lt < end) enter();
     };
 
     f32x16 acc[S::TQ][S::TP];
-#pragma unroll
-    for (int i = 0; i < S::TQ; ++i)
-#pragma unroll
-        for (int j = 0; j < S::TP; ++j)
-#pragma unroll
-            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
-
     typename std::conditional<kPRows, RowFrag<S>, ColFrag<S, S::BM, S::TP>>::type pf(wp * S::TP);
     typename std::conditional<kQRows, RowFrag<S>, ColFrag<S, S::BN, S::TQ>>::type qf(wq * S::TQ);
     struct Frags {
@@ -308,16 +402,16 @@ __global__ __launch_bounds__(S::kThreads) void gated_product_kernel(Product a)
         for (int j = 0; j < S::TP; ++j) f.p[j] = pf.read(ps, wp * S::TP + j, j, kk);
     };
     constexpr int kSteps = S::BK / 16;
-    // Multiplies one stage; the loads of stage `next` go out between its steps.
-    auto compute = [&](const char* st, int next, char* nst) __attribute__((always_inline)) {
+    // Multiplies one stage; the loads of the next one go out between its steps.
+    auto compute = [&](const char* st, bool more, char* next) __attribute__((always_inline)) {
         Frags f[2];
         read(f[0], st, 0);
 #pragma unroll
         for (int kk = 0; kk < kSteps; ++kk) {
             if (kk + 1 < kSteps) read(f[(kk + 1) & 1], st, kk + 1);
-            if (next < nk) {
+            if (FAST && more) {
 #pragma unroll
-                for (int i = kk * S::kLoads / kSteps; i < (kk + 1) * S::kLoads / kSteps; ++i) issue(next, nst, i);
+                for (int i = kk * S::kLoads / kSteps; i < (kk + 1) * S::kLoads / kSteps; ++i) issue(i, next);
             }
 #pragma unroll
             for (int i = 0; i < S::TQ; ++i)
@@ -325,170 +419,241 @@ __global__ __launch_bounds__(S::kThreads) void gated_product_kernel(Product a)
                 for (int j = 0; j < S::TP; ++j)
                     acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[kk & 1].q[i], f[kk & 1].p[j], acc[i][j], 0, 0, 0);
         }
+        if (FAST && more) advance();
     };
 
-    // Stage kt has landed for every wave after its own wait and the barrier;
-    // every wave is then done with stage kt - 1, whose place is filled next.
+    if (first >= end) return;
+    enter();
+    int ahead = 0;  // stages on their way or waiting
+    if constexpr (FAST) {
+        for (; ahead < S::NS - 1 && lt < end; ++ahead) {
 #pragma unroll
-    for (int st = 0; st < S::NS - 1; ++st)
-        if (st < nk)
-            for (int i = 0; i < S::kLoads; ++i) issue(st, ring + st * S::kStage, i);
-    for (int kt = 0; kt < nk; kt += S::NS) {
-#pragma unroll
-        for (int i = 0; i < S::NS; ++i)
-            if (kt + i < nk) {
-                if constexpr (FAST) {
-                    if (kt + i + S::NS - 2 < nk) wait_vm_lds<(S::NS - 2) * S::kLoads>();
-                    else wait_vm_lds<0>();
-                    barrier_no_fence();
-                } else {
-                    __syncthreads();
-                }
-                compute(ring + i * S::kStage, kt + i + S::NS - 1, ring + (i + S::NS - 1) % S::NS * S::kStage);
-            }
-    }
-    __syncthreads();  // every wave is done with the ring
-
-    // A lane holds columns 8v + 4q + {0..3} of a q tile and p row `col`.
-    if constexpr (kGated) {
-        constexpr int U = kQTile / 8;  // units of a tile row
-        char* second = ring + S::BM * kQTile * 2;
-        if constexpr (MODE == kAgain) {
-            // dh's tile, in the places that dg will take
-            for (int idx = tid; idx < S::BM * U; idx += S::kThreads) {
-                const int r = idx / U, f = q0 + ((idx % U) ^ (r & 7)) * 8;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (r < rows_left && f < a.F) v = guarded16(a.dh + (p0 + r) * a.F + f, a.F - f);
-                *reinterpret_cast<uint4*>(ring + idx * 16) = v;
-            }
-            __syncthreads();
-        }
-        with_act(a.act, [&](auto kind) __attribute__((always_inline)) {
-#pragma unroll
-        for (int m = 0; m < S::TQ / 2; ++m) {
-            const int base = (wq * (S::TQ / 2) + m) * 32;
-            float sg[16], su[16];
-#pragma unroll
-            for (int v = 0; v < 16; ++v) sg[v] = su[v] = 0.f;
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const int f = q0 + base + 8 * v + 4 * q;
-                float bg[4], bu[4];
-                bias4(a.bg, f, a.F, bg);
-                bias4(a.bu, f, a.F, bu);
-#pragma unroll
-                for (int j = 0; j < S::TP; ++j) {
-                    const int r = (wp * S::TP + j) * 32 + col;
-                    char* at = ring + tile_byte<U>(r, base / 8 + v, q);
-                    float g[4], u[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        g[e] = acc[2 * m][j][4 * v + e] + bg[e];
-                        u[e] = acc[2 * m + 1][j][4 * v + e] + bu[e];
-                    }
-                    if constexpr (MODE == kFwd) {
-                        if (a.saved && r < rows_left) {
-                            float* sp = a.saved + (p0 + r) * 2 * a.F + f;
-                            if (f + 4 <= a.F) {
-                                store16_any(sp, make_uint4(__float_as_uint(g[0]), __float_as_uint(g[1]), __float_as_uint(g[2]), __float_as_uint(g[3])));
-                                store16_any(sp + a.F, make_uint4(__float_as_uint(u[0]), __float_as_uint(u[1]), __float_as_uint(u[2]), __float_as_uint(u[3])));
-                            } else {
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    if (f + e < a.F) sp[e] = g[e], sp[a.F + e] = u[e];
-                            }
-                        }
-                        float h[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) h[e] = act_value<kind()>(g[e]) * u[e];
-                        *reinterpret_cast<uint2*>(at) = make_uint2(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]));
-                    } else {
-                        const uint2 raw = *reinterpret_cast<const uint2*>(at);
-                        const float dh[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u),
-                                             __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xffff0000u)};
-                        float dg[4], du[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const ActPair p = act_pair<kind()>(g[e]);
-                            dg[e] = dh[e] * u[e] * p.d;
-                            du[e] = dh[e] * p.v;
-                            sg[4 * v + e] += dg[e];
-                            su[4 * v + e] += du[e];
-                        }
-                        *reinterpret_cast<uint2*>(at) = make_uint2(pack_bf16x2(dg[0], dg[1]), pack_bf16x2(dg[2], dg[3]));
-                        *reinterpret_cast<uint2*>(at + S::BM * kQTile * 2) = make_uint2(pack_bf16x2(du[0], du[1]), pack_bf16x2(du[2], du[3]));
-                    }
-                }
-            }
-            if constexpr (MODE == kAgain) {
-                if (a.sums) {
-                    int which;
-                    const float tg = half_sum16(sg, lane, which), tu = half_sum16(su, lane, which);
-                    const int f = q0 + base + 8 * (which >> 2) + 4 * q + (which & 3);
-                    if ((lane & 1) == 0 && f < a.Fp) {
-                        float* row = a.sums + static_cast<int64_t>(pt * S::WP + wp) * 2 * a.Fp;
-                        row[f] = tg;
-                        row[a.Fp + f] = tu;
-                    }
-                }
-            }
-        }
-        });
-        __syncthreads();
-        if constexpr (MODE == kFwd) {
-            store_tile<U, S::kThreads>(ring, S::BM, a.F - q0, [&](int r) { return r < rows_left ? a.h + (p0 + r) * a.F + q0 : nullptr; });
-        } else {
-            // the columns up to Fp too: their dh is 0, and so are they
-            store_tile<U, S::kThreads>(ring, S::BM, a.Fp - q0, [&](int r) { return r < rows_left ? a.d_out + (p0 + r) * 2 * a.Fp + q0 : nullptr; });
-            store_tile<U, S::kThreads>(second, S::BM, a.Fp - q0, [&](int r) { return r < rows_left ? a.d_out + (p0 + r) * 2 * a.Fp + a.Fp + q0 : nullptr; });
+            for (int i = 0; i < S::kLoads; ++i) issue(i, ring + ahead * S::kStage);
+            advance();
         }
     } else {
-        // row p0 + r of the output: a row of dx, or of dWg or dWu (none: null)
-        auto weight_row = [&](int64_t p, int64_t& f) {
-            const bool up = p >= a.Fp;
-            f = p - (up ? a.Fp : 0);
-            return f < a.F && p < 2 * a.Fp ? (up ? 1 : 0) : -1;
-        };
-        if (MODE == kDw && a.part) {
-#pragma unroll
-            for (int j = 0; j < S::TP; ++j) {
-                int64_t f;
-                const int half = weight_row(p0 + (wp * S::TP + j) * 32 + col, f);
-                if (half < 0) continue;
-                float* row = a.part + ((static_cast<int64_t>(piece) * 2 + half) * a.F + f) * a.C;
-#pragma unroll
-                for (int i = 0; i < S::TQ; ++i)
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        const int c = q0 + (wq * S::TQ + i) * 32 + 8 * v + 4 * q;
-                        if (c + 4 <= a.C)
-                            store16_any(row + c, make_uint4(__float_as_uint(acc[i][j][4 * v]), __float_as_uint(acc[i][j][4 * v + 1]),
-                                                            __float_as_uint(acc[i][j][4 * v + 2]), __float_as_uint(acc[i][j][4 * v + 3])));
-                        else
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (c + e < a.C) row[c + e] = acc[i][j][4 * v + e];
-                    }
-            }
-            return;
-        }
-        constexpr int U = S::BN / 8;
+        fetch();
+        put(ring);
+        advance();
+        if (lt < end) fetch();
+    }
+
+    int cur = 0;  // place of the stage to multiply
+    for (int t = first; t < end; t += step) {
+        const Tile o = tile_of(t);
+        const int nk = stages(o.K);
 #pragma unroll
         for (int i = 0; i < S::TQ; ++i)
 #pragma unroll
             for (int j = 0; j < S::TP; ++j)
 #pragma unroll
-                for (int v = 0; v < 4; ++v)
-                    *reinterpret_cast<uint2*>(ring + tile_byte<U>((wp * S::TP + j) * 32 + col, (wq * S::TQ + i) * 4 + v, q)) =
-                        make_uint2(pack_bf16x2(acc[i][j][4 * v], acc[i][j][4 * v + 1]), pack_bf16x2(acc[i][j][4 * v + 2], acc[i][j][4 * v + 3]));
-        __syncthreads();
-        store_tile<U, S::kThreads>(ring, S::BM, a.C - q0, [&](int r) -> bf16_t* {
-            if (MODE == kDx) return r < rows_left && a.out ? a.out + (p0 + r) * a.C + q0 : nullptr;
-            int64_t f;
-            const int half = weight_row(p0 + r, f);
-            bf16_t* w = half < 0 ? nullptr : half ? a.out2 : a.out;
-            return w ? w + f * a.C + q0 : nullptr;
-        });
+                for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+        const char* st = nullptr;
+        for (int kt = 0; kt < nk; ++kt) {
+            st = ring + cur * S::kStage;
+            const bool more = lt < end;
+            if constexpr (FAST) {
+                // This stage has landed for every wave after its own wait and the
+                // barrier; every wave is then done with the stage before it, whose
+                // place is filled next.
+                if (ahead == S::NS - 1) wait_vm_lds<(S::NS - 2) * S::kLoads>();
+                else wait_vm_lds<0>();
+                barrier_no_fence();
+                compute(st, more, ring + (cur == 0 ? S::NS - 1 : cur - 1) * S::kStage);
+                ahead += more ? 0 : -1;
+            } else {
+                __syncthreads();
+                if (more) {
+                    put(ring + (cur + 1 == S::NS ? 0 : cur + 1) * S::kStage);
+                    advance();
+                    if (lt < end) fetch();
+                }
+                compute(st, false, nullptr);
+            }
+            cur = cur + 1 == S::NS ? 0 : cur + 1;
+        }
+        // Every wave is done with the last stage, whose place the outputs pass
+        // through; it is filled again after the next barrier.
+        wait_vm_lds<63>();
+        barrier_no_fence();
+        char* turn = const_cast<char*>(st) + wave * S::kWaveLds;
+
+        // A lane holds columns 8v + 4q + {0..3} of a q tile and p row `col`.
+        if constexpr (kGated) {
+            // One step takes 32 rows and 32 columns.  A loop with one copy of its
+            // code: unrolled over the accumulators it outgrows the instruction
+            // cache.
+            constexpr int M = S::TQ / 2;
+            const int f0 = o.q0 + wq * M * 32;  // the wave's first column
+            float tg[M], tu[M];                 // column sums
+#pragma unroll
+            for (int m = 0; m < M; ++m) tg[m] = tu[m] = 0.f;
+            uint4 dh[2];
+            auto load_dh = [&](int s) __attribute__((always_inline)) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int64_t r0 = o.p0 + (wp * S::TP + s / M) * 32;
+                    const int r = i * 16 + lane / 4, fs = f0 + s % M * 32, n = a.F - fs - lane % 4 * 8;
+                    const rsrc_t in = make_rsrc(a.dh + r0 * a.F + fs, kAll);
+                    const bool on = r < a.rows - r0 && n > 0;
+                    dh[i] = unit_load(in, on ? (r * a.F + lane % 4 * 8) * 2u : kOutside, fs + 32 > a.F && a.F % 8 != 0, on ? n : 0);
+                }
+            };
+            if constexpr (MODE == kAgain) load_dh(0);
+#pragma unroll 1
+            for (int s = 0; s < S::TP * M; ++s) {
+                const int64_t r0 = o.p0 + (wp * S::TP + s / M) * 32;
+                const int rows = static_cast<int>(min(static_cast<int64_t>(32), a.rows - r0));
+                const int fs = f0 + s % M * 32;
+                // Four columns 8v + 4q + {0..3}: g and u with their biases.
+                auto take = [&](int v, float (&g)[4], float (&u)[4]) __attribute__((always_inline)) {
+                    // keeps the registers of one group from overlapping the next
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int n = 0; n < S::TP * M; ++n)
+                        if (s == n) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) g[e] = acc[n % M * 2][n / M][4 * v + e], u[e] = acc[n % M * 2 + 1][n / M][4 * v + e];
+                        }
+                    if (a.bg) {
+                        float bg[4], bu[4];
+                        bias4(a.bg, fs + 8 * v + 4 * q, a.F, fs + 32 > a.F, bg);
+                        bias4(a.bu, fs + 8 * v + 4 * q, a.F, fs + 32 > a.F, bu);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) g[e] += bg[e], u[e] += bu[e];
+                    }
+                };
+                auto place = [&](char* to, int v, const float* w) __attribute__((always_inline)) {
+                    *reinterpret_cast<uint2*>(to + turn_at<4>(col, v) + 8 * q) = make_uint2(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]));
+                };
+                if constexpr (MODE == kFwd) {
+                    if (a.saved) {
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+#pragma unroll
+                            for (int v = 0; v < 4; ++v) {
+                                float g[4], u[4];
+                                take(v, g, u);
+                                const float(&w)[4] = n ? u : g;
+                                *reinterpret_cast<float4*>(turn + turn_at<8>(col, 2 * v + q)) = make_float4(w[0], w[1], w[2], w[3]);
+                            }
+                            wave_order();
+                            turn_out<8>(turn, a.saved + r0 * 2 * a.F + (n ? a.F : 0) + fs, 2u * a.F, rows, a.F - fs);
+                            wave_order();
+                        }
+                    }
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        float g[4], u[4];
+                        take(v, g, u);
+                        with_act(a.act, [&](auto kind) __attribute__((always_inline)) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) g[e] = act_value<kind()>(g[e]) * u[e];
+                        });
+                        place(turn, v, g);
+                    }
+                    wave_order();
+                    turn_out<4>(turn, a.h + r0 * a.F + fs, a.F, rows, a.F - fs);
+                } else {
+                    char* other = turn + 2048;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) *reinterpret_cast<uint4*>(turn + turn_at<4>(i * 16 + lane / 4, lane % 4)) = dh[i];
+                    wave_order();
+                    if (s + 1 < S::TP * M) load_dh(s + 1);
+                    float sg[16], su[16];
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        float g[4], u[4];
+                        take(v, g, u);
+                        const uint2 raw = *reinterpret_cast<const uint2*>(turn + turn_at<4>(col, v) + 8 * q);
+                        const float h[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u),
+                                            __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xffff0000u)};
+                        with_act(a.act, [&](auto kind) __attribute__((always_inline)) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const ActPair p = act_pair<kind()>(g[e]);
+                                g[e] = h[e] * u[e] * p.d;
+                                u[e] = h[e] * p.v;
+                            }
+                        });
+                        place(turn, v, g);  // where this lane's dh was
+                        place(other, v, u);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sg[4 * v + e] = g[e], su[4 * v + e] = u[e];
+                    }
+                    wave_order();
+                    // the columns up to Fp too: their dh is 0, and so are they
+                    bf16_t* d = a.d_out + r0 * 2 * a.Fp + fs;
+                    turn_out<4>(turn, d, 2u * a.Fp, rows, a.Fp - fs);
+                    turn_out<4>(other, d + a.Fp, 2u * a.Fp, rows, a.Fp - fs);
+                    if (a.sums) {
+                        const float g = half_sum16(sg, lane), u = half_sum16(su, lane);
+#pragma unroll
+                        for (int m = 0; m < M; ++m)
+                            if (s % M == m) tg[m] += g, tu[m] += u;
+                    }
+                }
+                wave_order();
+            }
+            if (MODE == kAgain && a.sums) {
+#pragma unroll
+                for (int m = 0; m < M; ++m) {
+                    const int which = half_sum_of(lane);
+                    const int f = f0 + m * 32 + 8 * (which >> 2) + 4 * q + (which & 3);
+                    if ((lane & 1) == 0 && f < a.Fp) {
+                        float* row = a.sums + static_cast<int64_t>(o.pt * S::WP + wp) * 2 * a.Fp;
+                        row[f] = tg[m];
+                        row[a.Fp + f] = tu[m];
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < S::TP; ++j) {
+                // 32 rows of dx, or (Fp is a multiple of 32) of dWg or dWu
+                const int64_t r0 = o.p0 + (wp * S::TP + j) * 32;
+                const int c0 = o.q0 + wq * S::TQ * 32;
+                bf16_t* out = a.out;
+                float* part = nullptr;
+                int64_t f = r0;
+                int rows;
+                if (MODE == kDx) {
+                    rows = static_cast<int>(min(static_cast<int64_t>(32), a.rows - r0));
+                } else {
+                    const bool up = r0 >= a.Fp;
+                    f -= up ? a.Fp : 0;
+                    rows = r0 < 2 * a.Fp ? static_cast<int>(min(static_cast<int64_t>(32), a.F - f)) : 0;
+                    out = up ? a.out2 : a.out;
+                    if (a.part) part = a.part + ((static_cast<int64_t>(o.piece) * 2 + (up ? 1 : 0)) * a.F + f) * a.C;
+                }
+                if (MODE == kDw && part) {
+#pragma unroll
+                    for (int i = 0; i < S::TQ; ++i) {
+                        const f32x16& w = acc[i][j];
+#pragma unroll
+                        for (int v = 0; v < 4; ++v)
+                            *reinterpret_cast<float4*>(turn + turn_at<8>(col, 2 * v + q)) = make_float4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
+                        wave_order();
+                        turn_out<8>(turn, part + c0 + i * 32, a.C, rows, a.C - c0 - i * 32);
+                        wave_order();
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < S::TQ; i += 2) {
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            const f32x16& w = acc[i + n][j];
+#pragma unroll
+                            for (int v = 0; v < 4; ++v)
+                                *reinterpret_cast<uint2*>(turn + turn_at<8>(col, n * 4 + v) + 8 * q) = make_uint2(pack_bf16x2(w[4 * v], w[4 * v + 1]), pack_bf16x2(w[4 * v + 2], w[4 * v + 3]));
+                        }
+                        wave_order();
+                        if (out) turn_out<8>(turn, out + f * a.C + c0 + i * 32, a.C, rows, a.C - c0 - i * 32);
+                        wave_order();
+                    }
+                }
+            }
+        }
     }
 }
 
@@ -566,19 +731,20 @@ __global__ __launch_bounds__(kFewWaves * 64) void gated_few_rows_kernel(Product 
     }
 }
 
-typedef Shape<2, 4, 4, 2, 64, 2> Big;    // 256 x 256, eight waves
-typedef Shape<2, 2, 2, 2, 64, 2> Small;  // 128 x 128, four waves
+typedef Shape<2, 2, 2, 4, 32, 3> Big;    // 128 x 256
+typedef Shape<2, 2, 2, 2, 64, 2> Small;  // 128 x 128
 
 bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 int64_t tiles(int64_t n, int t) { return (n + t - 1) / t; }
 
 template <typename S, int MODE, bool FAST>
-hipError_t run(Product& k, int64_t p_tiles, int64_t q_tiles, int pieces, hipStream_t s)
+hipError_t run(Product& k, int64_t p, int64_t q, int pieces, hipStream_t s)
 {
-    k.p_tiles = static_cast<int>(p_tiles);
-    k.q_tiles = static_cast<int>(q_tiles);
-    const int64_t blocks = p_tiles * q_tiles * pieces;
-    if (blocks >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
+    const int64_t pt = tiles(p, S::BM), qt = tiles(q, S::BN), n = pt * qt * pieces;
+    if (n >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
+    k.p_tiles = static_cast<int>(pt);
+    k.q_tiles = static_cast<int>(qt);
+    k.tiles = static_cast<int>(n);
     auto kernel = gated_product_kernel<S, MODE, FAST>;
     static std::atomic<bool> ready{false};
     if (S::kLds > 65536 && !ready.load(std::memory_order_acquire)) {
@@ -586,21 +752,19 @@ hipError_t run(Product& k, int64_t p_tiles, int64_t q_tiles, int pieces, hipStre
         if (e != hipSuccess) return e;
         ready.store(true, std::memory_order_release);
     }
-    return launch(kernel, dim3(static_cast<unsigned>(blocks)), dim3(S::kThreads), S::kLds, s, k);
+    // as many workgroups as the device holds at once, the same number on each XCD
+    const int64_t hold = std::max(8, device_cu_count() * S::kPerCu / 8 * 8);
+    return launch(kernel, dim3(static_cast<unsigned>(std::min<int64_t>((n + 7) / 8 * 8, hold))), dim3(S::kThreads), S::kLds, s, k);
 }
 
-// The large tile once it gives every CU one; smaller ones below that.
-bool use_big(int64_t p, int64_t q, int pieces) { return tiles(p, Big::BM) * tiles(q, Big::BN) * pieces >= device_cu_count(); }
+// The large tile once it gives every CU two; smaller ones below that.
+bool use_big(int64_t p, int64_t q, int pieces) { return tiles(p, Big::BM) * tiles(q, Big::BN) * pieces >= Big::kPerCu * device_cu_count(); }
 
 template <int MODE>
 hipError_t run_tiles(Product& k, int64_t p, int64_t q, int pieces, bool big, bool fast, hipStream_t s)
 {
-    if (big) {
-        const int64_t pt = tiles(p, Big::BM), qt = tiles(q, Big::BN);
-        return fast ? run<Big, MODE, true>(k, pt, qt, pieces, s) : run<Big, MODE, false>(k, pt, qt, pieces, s);
-    }
-    const int64_t pt = tiles(p, Small::BM), qt = tiles(q, Small::BN);
-    return fast ? run<Small, MODE, true>(k, pt, qt, pieces, s) : run<Small, MODE, false>(k, pt, qt, pieces, s);
+    if (big) return fast ? run<Big, MODE, true>(k, p, q, pieces, s) : run<Big, MODE, false>(k, p, q, pieces, s);
+    return fast ? run<Small, MODE, true>(k, p, q, pieces, s) : run<Small, MODE, false>(k, p, q, pieces, s);
 }
 
 Product product(const GatedArgs& a)
