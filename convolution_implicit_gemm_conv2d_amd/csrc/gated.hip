@@ -46,11 +46,13 @@ struct Shape {
     static constexpr int WP = WP_, WQ = WQ_, TP = TP_, TQ = TQ_, BK = BK_, NS = NS_;
     static constexpr int BM = WP * TP * 32, BN = WQ * TQ * 32, kThreads = WP * WQ * 64;
     static constexpr int kPBytes = BM * BK * 2, kQBytes = BN * BK * 2, kStage = kPBytes + kQBytes;
-    static constexpr int kLds = NS * kStage;
+    static constexpr int kLds = NS * kStage + BN * 4;  // the ring and a tile's biases
     static constexpr int kPLoads = BM * BK / 8 / kThreads, kQLoads = BN * BK / 8 / kThreads;
     static constexpr int kLoads = kPLoads + kQLoads;
     static constexpr int kWaveLds = kStage / (WP * WQ);  // a wave's part of a stage
-    static constexpr int kPerCu = 163840 / kLds < 8 / (WP * WQ) ? 163840 / kLds : 8 / (WP * WQ);  // workgroups
+    static constexpr int kWaves = TP * TQ > 8 ? 1 : 2;  // of a SIMD: the accumulators take 16 TP TQ of its 512 registers
+    static constexpr int kPerCu = 4 * kWaves / (WP * WQ);  // workgroups
+    static_assert(kPerCu * kLds <= 163840 && BN <= kThreads, "");
     static_assert(kWaveLds >= 4096, "a wave's output passes through its part of a stage");
     static_assert(kPLoads > 0 && kQLoads > 0 && TQ % 2 == 0 && NS >= 2, "");
 };
@@ -226,20 +228,6 @@ __device__ __forceinline__ void turn_out(const char* lds, T* p, uint32_t ld, int
     }
 }
 
-// Four biases from column f on, zeros past F; `ragged` (uniform): some are past.
-__device__ __forceinline__ void bias4(const bf16_t* b, int f, int F, bool ragged, float* v)
-{
-    const rsrc_t r = make_rsrc(b, kAll);
-    if (!ragged) {
-        const uint2 t = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r, f * 2, 0, 0));
-        v[0] = __uint_as_float(t.x << 16); v[1] = __uint_as_float(t.x & 0xffff0000u);
-        v[2] = __uint_as_float(t.y << 16); v[3] = __uint_as_float(t.y & 0xffff0000u);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = bf16_to_f(__builtin_amdgcn_raw_buffer_load_b16(r, f + e < F ? (f + e) * 2 : kOutside, 0, 0));
-    }
-}
-
 // Sums 16 values over the 32 lanes of a half wave: in each step a lane gives
 // half of its values to a partner and keeps the other half.  A lane ends with
 // the sum of value half_sum_of(lane).
@@ -282,7 +270,7 @@ __device__ __forceinline__ void pick_tile(int t, int p_tiles, int q_tiles, int& 
 }
 
 template <typename S, int MODE, bool FAST>
-__global__ __launch_bounds__(S::kThreads, 2) void gated_product_kernel(Product a)
+__global__ __launch_bounds__(S::kThreads, S::kWaves) void gated_product_kernel(Product a)
 {
     extern __shared__ char ring[];
     constexpr bool kGated = MODE == kFwd || MODE == kAgain;
@@ -320,57 +308,42 @@ __global__ __launch_bounds__(S::kThreads, 2) void gated_product_kernel(Product a
     // one before.
     Units<S, S::BM, kPRows> pu;
     Units<S, S::BN, kQRows> qu;
-    Tile load;
     int lt = first, lk = 0, lstages = 0, p_valid = 0, q_valid = 0;
+    int left = 0, q_left = 0;                // contraction values from this stage on, and rows of the q source
+    const bf16_t *p_src, *q_src, *q_src2;    // the stage's; q_src2: the other weight (gated: of the same stage, dx: from Fp on)
+    const int64_t p_step = kPRows ? S::BK : static_cast<int64_t>(S::BK) * p_ld, q_step = kQRows ? S::BK : static_cast<int64_t>(S::BK) * q_ld;
     auto enter = [&]() __attribute__((always_inline)) {
-        load = tile_of(lt);
+        const Tile o = tile_of(lt);
         lk = 0;
-        lstages = stages(load.K);
-        p_valid = static_cast<int>(kPRows ? min(static_cast<int64_t>(S::BM), a.rows - load.p0) : 2 * a.Fp - load.p0);
-        q_valid = kQRows ? min(kQTile, a.F - load.q0) : a.C - load.q0;
+        lstages = stages(o.K);
+        left = o.K;
+        q_left = MODE == kDx ? a.F : o.K;
+        p_valid = static_cast<int>(kPRows ? min(static_cast<int64_t>(S::BM), a.rows - o.p0) : 2 * a.Fp - o.p0);
+        q_valid = kQRows ? min(kQTile, a.F - o.q0) : a.C - o.q0;
         pu.template set<false>(p_valid, p_ld);
         qu.template set<kQRows>(q_valid, q_ld);
-    };
-    // Source of a stage's units, and how many contraction values are left.
-    auto p_source = [&](int& left) __attribute__((always_inline)) {
-        left = load.K - lk * S::BK;
-        const int64_t k = static_cast<int64_t>(lk) * S::BK;
-        return kPRows ? (kGated ? a.x : a.d) + load.p0 * p_ld + k : a.d + (load.m0 + k) * p_ld + load.p0;
-    };
-    auto q_source = [&](int second, int& left) __attribute__((always_inline)) {
-        int k = lk * S::BK;
-        left = load.K - k;
-        if (kQRows) return (second ? a.wu : a.wg) + static_cast<int64_t>(load.q0) * q_ld + k;
-        if (MODE == kDw) return a.x + (load.m0 + k) * q_ld + load.q0;
-        const bool up = k >= a.Fp;
-        k -= up ? a.Fp : 0;
-        left = a.F - k;
-        return (up ? a.wu : a.wg) + static_cast<int64_t>(k) * q_ld + load.q0;
-    };
-    auto bytes = [&](bool by_rows, int valid, int ld, int left) __attribute__((always_inline)) {
-        const uint32_t n = by_rows ? static_cast<uint32_t>(valid) * ld - lk * S::BK : static_cast<uint32_t>(min(left, S::BK) - 1) * ld + valid;
-        return left > 0 ? n * 2u : 0u;
+        p_src = kPRows ? (kGated ? a.x : a.d) + o.p0 * p_ld : a.d + o.m0 * p_ld + o.p0;
+        const int64_t q_at = kQRows ? static_cast<int64_t>(o.q0) * q_ld : o.q0;
+        q_src = MODE == kDw ? a.x + o.m0 * q_ld + q_at : a.wg + q_at;
+        q_src2 = a.wu + q_at;
     };
     auto issue = [&](int i, char* st) __attribute__((always_inline)) {
         const bool is_p = i < S::kPLoads;
         const int j = is_p ? i : i - S::kPLoads;
-        int left;
-        const bf16_t* src = is_p ? p_source(left) : q_source(kQRows ? qu.second(j) : 0, left);
-        const uint32x4_t rs = dma_rsrc(src, is_p ? bytes(kPRows, p_valid, p_ld, left) : bytes(kQRows, q_valid, q_ld, left));
-        const uint32_t off = (is_p ? pu.k(j) : qu.k(j)) < left ? (is_p ? pu.off[j] : qu.off[j]) : kOutside;
-        dma16(rs, off, lds_addr(st + (is_p ? 0 : S::kPBytes) + (j * S::kThreads + wave * 64) * 16));
+        const bf16_t* src = is_p ? p_src : kQRows && qu.second(j) ? q_src2 : q_src;
+        const uint32_t off = (is_p ? pu.k(j) < left : qu.k(j) < q_left) ? (is_p ? pu.off[j] : qu.off[j]) : kOutside;
+        dma16(dma_rsrc(src, kAll), off, lds_addr(st + (is_p ? 0 : S::kPBytes) + (j * S::kThreads + wave * 64) * 16));
     };
     // Rows of any length and alignment pass through registers.
     uint4 held[FAST ? 1 : S::kLoads];
     auto fetch = [&]() __attribute__((always_inline)) {
-        int left;
 #pragma unroll
         for (int i = 0; i < (FAST ? 0 : S::kLoads); ++i) {
             const bool is_p = i < S::kPLoads;
-            const int j = is_p ? i : i - S::kPLoads;
-            const bf16_t* src = is_p ? p_source(left) : q_source(kQRows ? qu.second(j) : 0, left);
-            const int n = is_p ? pu.count(j, left, p_valid) : qu.count(j, left, q_valid);
-            const bool ragged = (is_p ? kPRows : kQRows) ? left < S::BK && left % 8 != 0 : (is_p ? p_valid % 8 != 0 : q_valid % 8 != 0);
+            const int j = is_p ? i : i - S::kPLoads, have = is_p ? left : q_left;
+            const bf16_t* src = is_p ? p_src : kQRows && qu.second(j) ? q_src2 : q_src;
+            const int n = is_p ? pu.count(j, have, p_valid) : qu.count(j, have, q_valid);
+            const bool ragged = (is_p ? kPRows : kQRows) ? have < S::BK && have % 8 != 0 : (is_p ? p_valid % 8 != 0 : q_valid % 8 != 0);
             held[i] = unit_load(make_rsrc(src, kAll), n > 0 ? (is_p ? pu.off[j] : qu.off[j]) : kOutside, ragged, n);
         }
     };
@@ -382,7 +355,15 @@ __global__ __launch_bounds__(S::kThreads, 2) void gated_product_kernel(Product a
         }
     };
     auto advance = [&]() __attribute__((always_inline)) {
-        if (++lk < lstages) return;
+        if (++lk < lstages) {
+            left -= S::BK;
+            q_left -= S::BK;
+            p_src += p_step;
+            q_src += q_step;
+            if (kQRows) q_src2 += q_step;
+            if (MODE == kDx && lk * S::BK == a.Fp) q_src = q_src2, q_left = a.F;  // Fp is a multiple of BK
+            return;
+        }
         lt += step;
         if (lt < end) enter();
     };
@@ -392,39 +373,20 @@ __global__ __launch_bounds__(S::kThreads, 2) void gated_product_kernel(Product a
     typename std::conditional<kQRows, RowFrag<S>, ColFrag<S, S::BN, S::TQ>>::type qf(wq * S::TQ);
     struct Frags {
         bf16x8 q[S::TQ], p[S::TP];
+    } frags[2];
+    auto read_q = [&](Frags& f, const char* st, int kk, int i) __attribute__((always_inline)) {
+        f.q[i] = qf.read((const lds_char*)st + S::kPBytes, wq * S::TQ + i, i, kk);
     };
-    auto read = [&](Frags& f, const char* st, int kk) __attribute__((always_inline)) {
-        const lds_char* ps = (const lds_char*)st;
-        const lds_char* qs = ps + S::kPBytes;
-#pragma unroll
-        for (int i = 0; i < S::TQ; ++i) f.q[i] = qf.read(qs, wq * S::TQ + i, i, kk);
-#pragma unroll
-        for (int j = 0; j < S::TP; ++j) f.p[j] = pf.read(ps, wp * S::TP + j, j, kk);
+    auto read_p = [&](Frags& f, const char* st, int kk, int j) __attribute__((always_inline)) {
+        f.p[j] = pf.read((const lds_char*)st, wp * S::TP + j, j, kk);
     };
     constexpr int kSteps = S::BK / 16;
-    // Multiplies one stage; the loads of the next one go out between its steps.
-    auto compute = [&](const char* st, bool more, char* next) __attribute__((always_inline)) {
-        Frags f[2];
-        read(f[0], st, 0);
-#pragma unroll
-        for (int kk = 0; kk < kSteps; ++kk) {
-            if (kk + 1 < kSteps) read(f[(kk + 1) & 1], st, kk + 1);
-            if (FAST && more) {
-#pragma unroll
-                for (int i = kk * S::kLoads / kSteps; i < (kk + 1) * S::kLoads / kSteps; ++i) issue(i, next);
-            }
-#pragma unroll
-            for (int i = 0; i < S::TQ; ++i)
-#pragma unroll
-                for (int j = 0; j < S::TP; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[kk & 1].q[i], f[kk & 1].p[j], acc[i][j], 0, 0, 0);
-        }
-        if (FAST && more) advance();
-    };
 
     if (first >= end) return;
     enter();
-    int ahead = 0;  // stages on their way or waiting
+    int ahead = 0;       // stages on their way or waiting
+    int cur = S::NS - 1;  // place of the stage being multiplied
+    bool more = false;   // whether the stage that fills the place before it exists
     if constexpr (FAST) {
         for (; ahead < S::NS - 1 && lt < end; ++ahead) {
 #pragma unroll
@@ -437,46 +399,89 @@ __global__ __launch_bounds__(S::kThreads, 2) void gated_product_kernel(Product a
         advance();
         if (lt < end) fetch();
     }
+    auto place = [&](int by) __attribute__((always_inline)) {
+        const int n = cur + by;
+        return ring + (n >= S::NS ? n - S::NS : n) * S::kStage;
+    };
+    // Turns to the next stage.  It has landed for every wave after its own wait
+    // and the barrier, and every wave has then read the one before into its
+    // registers, so that one's place is free.
+    auto turn_to_next = [&]() __attribute__((always_inline)) {
+        if constexpr (FAST) {
+            if (ahead == S::NS - 1) wait_vm_lds<(S::NS - 2) * S::kLoads>();
+            else wait_vm_lds<0>();
+            barrier_no_fence();
+            more = lt < end;
+            ahead += more ? 0 : -1;
+        } else {
+            __syncthreads();
+            if (lt < end) {
+                put(place(2 % S::NS));
+                advance();
+                if (lt < end) fetch();
+            }
+        }
+        cur = cur + 1 == S::NS ? 0 : cur + 1;
+    };
+    // The loads that fill the freed place go out over the steps until the next turn.
+    auto issue_part = [&](int part) __attribute__((always_inline)) {
+        if (!FAST || !more) return;
+#pragma unroll
+        for (int i = part * S::kLoads / kSteps; i < (part + 1) * S::kLoads / kSteps; ++i) issue(i, place(S::NS - 1));
+        if (part + 1 == kSteps) advance();
+    };
 
-    int cur = 0;  // place of the stage to multiply
     for (int t = first; t < end; t += step) {
         const Tile o = tile_of(t);
         const int nk = stages(o.K);
+        float bias = 0.f;  // of column threadIdx.x of the tile (both halves)
+        if (kGated && a.bg && threadIdx.x < S::BN) {
+            const int f = o.q0 + threadIdx.x % kQTile;
+            if (f < a.F) bias = bf16_to_f((threadIdx.x < kQTile ? a.bg : a.bu)[f]);
+        }
 #pragma unroll
         for (int i = 0; i < S::TQ; ++i)
 #pragma unroll
             for (int j = 0; j < S::TP; ++j)
 #pragma unroll
                 for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
-        const char* st = nullptr;
+        turn_to_next();
+        issue_part(0);
+#pragma unroll
+        for (int i = 0; i < S::TQ; ++i) read_q(frags[0], place(0), 0, i);
+#pragma unroll
+        for (int j = 0; j < S::TP; ++j) read_p(frags[0], place(0), 0, j);
         for (int kt = 0; kt < nk; ++kt) {
-            st = ring + cur * S::kStage;
-            const bool more = lt < end;
-            if constexpr (FAST) {
-                // This stage has landed for every wave after its own wait and the
-                // barrier; every wave is then done with the stage before it, whose
-                // place is filled next.
-                if (ahead == S::NS - 1) wait_vm_lds<(S::NS - 2) * S::kLoads>();
-                else wait_vm_lds<0>();
-                barrier_no_fence();
-                compute(st, more, ring + (cur == 0 ? S::NS - 1 : cur - 1) * S::kStage);
-                ahead += more ? 0 : -1;
-            } else {
-                __syncthreads();
-                if (more) {
-                    put(ring + (cur + 1 == S::NS ? 0 : cur + 1) * S::kStage);
-                    advance();
-                    if (lt < end) fetch();
+#pragma unroll
+            for (int kk = 0; kk < kSteps; ++kk) {
+                const bool last = kk + 1 == kSteps;
+                const bool next = !last || kt + 1 < nk;
+                // The last step's operands are in registers: on to the next
+                // stage, whose first operands arrive during this step.
+                if (last && next) turn_to_next();
+                Frags &f = frags[kk & 1], &n = frags[(kk + 1) & 1];
+                static_assert(kSteps % 2 == 0, "the next stage's operands take the first place again");
+#pragma unroll
+                for (int i = 0; i < S::TQ; ++i) {
+                    if (next) {
+                        read_q(n, place(0), last ? 0 : kk + 1, i);
+#pragma unroll
+                        for (int j = i * S::TP / S::TQ; j < (i + 1) * S::TP / S::TQ; ++j) read_p(n, place(0), last ? 0 : kk + 1, j);
+                        if (i == S::TQ - 1) issue_part(last ? 0 : kk + 1);
+                    }
+#pragma unroll
+                    for (int j = 0; j < S::TP; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.q[i], f.p[j], acc[i][j], 0, 0, 0);
                 }
-                compute(st, false, nullptr);
             }
-            cur = cur + 1 == S::NS ? 0 : cur + 1;
         }
         // Every wave is done with the last stage, whose place the outputs pass
-        // through; it is filled again after the next barrier.
+        // through; it is filled again after the next turn.
+        float* biases = reinterpret_cast<float*>(ring + S::NS * S::kStage);
+        if (kGated && a.bg && threadIdx.x < S::BN) biases[threadIdx.x] = bias;
         wait_vm_lds<63>();
         barrier_no_fence();
-        char* turn = const_cast<char*>(st) + wave * S::kWaveLds;
+        char* turn = place(0) + wave * S::kWaveLds;
 
         // A lane holds columns 8v + 4q + {0..3} of a q tile and p row `col`.
         if constexpr (kGated) {
@@ -516,14 +521,13 @@ __global__ __launch_bounds__(S::kThreads, 2) void gated_product_kernel(Product a
                             for (int e = 0; e < 4; ++e) g[e] = acc[n % M * 2][n / M][4 * v + e], u[e] = acc[n % M * 2 + 1][n / M][4 * v + e];
                         }
                     if (a.bg) {
-                        float bg[4], bu[4];
-                        bias4(a.bg, fs + 8 * v + 4 * q, a.F, fs + 32 > a.F, bg);
-                        bias4(a.bu, fs + 8 * v + 4 * q, a.F, fs + 32 > a.F, bu);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) g[e] += bg[e], u[e] += bu[e];
+                        const float* b = biases + wq * M * 32 + s % M * 32 + 8 * v + 4 * q;
+                        const float4 bg = *reinterpret_cast<const float4*>(b), bu = *reinterpret_cast<const float4*>(b + kQTile);
+                        g[0] += bg.x; g[1] += bg.y; g[2] += bg.z; g[3] += bg.w;
+                        u[0] += bu.x; u[1] += bu.y; u[2] += bu.z; u[3] += bu.w;
                     }
                 };
-                auto place = [&](char* to, int v, const float* w) __attribute__((always_inline)) {
+                auto lay = [&](char* to, int v, const float* w) __attribute__((always_inline)) {
                     *reinterpret_cast<uint2*>(to + turn_at<4>(col, v) + 8 * q) = make_uint2(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]));
                 };
                 if constexpr (MODE == kFwd) {
@@ -550,7 +554,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void gated_product_kernel(Product a
 #pragma unroll
                             for (int e = 0; e < 4; ++e) g[e] = act_value<kind()>(g[e]) * u[e];
                         });
-                        place(turn, v, g);
+                        lay(turn, v, g);
                     }
                     wave_order();
                     turn_out<4>(turn, a.h + r0 * a.F + fs, a.F, rows, a.F - fs);
@@ -576,8 +580,8 @@ __global__ __launch_bounds__(S::kThreads, 2) void gated_product_kernel(Product a
                                 u[e] = h[e] * p.v;
                             }
                         });
-                        place(turn, v, g);  // where this lane's dh was
-                        place(other, v, u);
+                        lay(turn, v, g);  // where this lane's dh was
+                        lay(other, v, u);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) sg[4 * v + e] = g[e], su[4 * v + e] = u[e];
                     }
@@ -629,6 +633,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void gated_product_kernel(Product a
                 if (MODE == kDw && part) {
 #pragma unroll
                     for (int i = 0; i < S::TQ; ++i) {
+                        __builtin_amdgcn_sched_barrier(0);
                         const f32x16& w = acc[i][j];
 #pragma unroll
                         for (int v = 0; v < 4; ++v)
@@ -640,6 +645,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void gated_product_kernel(Product a
                 } else {
 #pragma unroll
                     for (int i = 0; i < S::TQ; i += 2) {
+                        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                         for (int n = 0; n < 2; ++n) {
                             const f32x16& w = acc[i + n][j];
@@ -731,7 +737,8 @@ __global__ __launch_bounds__(kFewWaves * 64) void gated_few_rows_kernel(Product 
     }
 }
 
-typedef Shape<2, 2, 2, 4, 32, 3> Big;    // 128 x 256
+typedef Shape<2, 2, 4, 4, 32, 4> Wide;   // 256 x 256, one workgroup a CU
+typedef Shape<2, 2, 2, 4, 32, 3> Big;    // 128 x 256, two
 typedef Shape<2, 2, 2, 2, 64, 2> Small;  // 128 x 128
 
 bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -757,13 +764,29 @@ hipError_t run(Product& k, int64_t p, int64_t q, int pieces, hipStream_t s)
     return launch(kernel, dim3(static_cast<unsigned>(std::min<int64_t>((n + 7) / 8 * 8, hold))), dim3(S::kThreads), S::kLds, s, k);
 }
 
-// The large tile once it gives every CU two; smaller ones below that.
-bool use_big(int64_t p, int64_t q, int pieces) { return tiles(p, Big::BM) * tiles(q, Big::BN) * pieces >= Big::kPerCu * device_cu_count(); }
+// The largest tile that gives every CU its workgroups; the widest only for long
+// sums, where its loads and LDS reads (half as many for a product) count and
+// its epilogue, which nothing runs beside, does not.
+enum class Tile { kSmall, kBig, kWide };
+constexpr int64_t kLongSum = 1024;
+template <typename S>
+bool fills(int64_t p, int64_t q, int pieces) { return tiles(p, S::BM) * tiles(q, S::BN) * pieces >= S::kPerCu * device_cu_count(); }
+Tile pick(int64_t p, int64_t q, int pieces, int64_t K)
+{
+    if (K >= kLongSum && fills<Wide>(p, q, pieces)) return Tile::kWide;
+    return fills<Big>(p, q, pieces) ? Tile::kBig : Tile::kSmall;
+}
+// Partial rows of the column sums of `rows` rows: one for each wave's rows.
+int64_t sum_rows(int64_t rows, Tile t)
+{
+    return t == Tile::kWide ? tiles(rows, Wide::BM) * Wide::WP : t == Tile::kBig ? tiles(rows, Big::BM) * Big::WP : tiles(rows, Small::BM) * Small::WP;
+}
 
 template <int MODE>
-hipError_t run_tiles(Product& k, int64_t p, int64_t q, int pieces, bool big, bool fast, hipStream_t s)
+hipError_t run_tiles(Product& k, int64_t p, int64_t q, int pieces, Tile t, bool fast, hipStream_t s)
 {
-    if (big) return fast ? run<Big, MODE, true>(k, p, q, pieces, s) : run<Big, MODE, false>(k, p, q, pieces, s);
+    if (t == Tile::kWide && fast) return run<Wide, MODE, true>(k, p, q, pieces, s);
+    if (t != Tile::kSmall) return fast ? run<Big, MODE, true>(k, p, q, pieces, s) : run<Big, MODE, false>(k, p, q, pieces, s);
     return fast ? run<Small, MODE, true>(k, p, q, pieces, s) : run<Small, MODE, false>(k, p, q, pieces, s);
 }
 
@@ -791,17 +814,17 @@ GatedPlan gated_plan_bf16(int64_t rows, int C, int F)
 {
     GatedPlan p{};
     p.Fp = (F + 63) / 64 * 64;
-    // pieces of the weight gradients' sum: about one workgroup a CU, no piece
+    // pieces of the weight gradients' sum: about one workgroup a place, no piece
     // under 512 rows
-    const bool big = use_big(2 * static_cast<int64_t>(p.Fp), C, 1);
-    const int bm = big ? Big::BM : Small::BM, bn = big ? Big::BN : Small::BN;
-    const int64_t t = tiles(2 * static_cast<int64_t>(p.Fp), bm) * tiles(C, bn);
-    const int64_t want = std::max<int64_t>(1, std::min<int64_t>((big ? 1 : 2) * device_cu_count() / t, rows / 512));
+    const int64_t dp = 2 * static_cast<int64_t>(p.Fp), cus = device_cu_count();
+    const Tile t = pick(dp, C, 1, rows);
+    const int64_t n = t == Tile::kWide ? tiles(dp, Wide::BM) * tiles(C, Wide::BN) : t == Tile::kBig ? tiles(dp, Big::BM) * tiles(C, Big::BN) : tiles(dp, Small::BM) * tiles(C, Small::BN);
+    const int64_t hold = (t == Tile::kWide ? Wide::kPerCu : t == Tile::kBig ? Big::kPerCu : Small::kPerCu) * cus;
+    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(hold / n, rows / 512));
     p.per = std::max<int64_t>(64, (tiles(rows, static_cast<int>(want)) + 63) / 64 * 64);
     p.pieces = static_cast<int>(std::max<int64_t>(1, (rows + p.per - 1) / p.per));
     int64_t chunk;
-    const int64_t again = tiles(rows, Small::BM) * Small::WP;
-    p.sum_rows = static_cast<int>(std::max<int64_t>(gated_kept_chunks(rows, p.Fp, &chunk), again));
+    p.sum_rows = static_cast<int>(std::max<int64_t>(gated_kept_chunks(rows, p.Fp, &chunk), sum_rows(rows, Tile::kSmall)));
     p.d_bytes = round256(static_cast<size_t>(rows) * 2 * p.Fp * 2);
     p.sum_bytes = round256(static_cast<size_t>(p.sum_rows) * 2 * p.Fp * 4);
     p.part_bytes = p.pieces > 1 ? round256(static_cast<size_t>(p.pieces) * 2 * F * C * 4) : 0;
@@ -820,7 +843,7 @@ hipError_t gated_fwd_bf16(const GatedArgs& a, hipStream_t s)
         if (a.rows <= 32) return launch(fast ? gated_few_rows_kernel<2, true> : gated_few_rows_kernel<2, false>, grid, block, 0, s, k);
         return launch(fast ? gated_few_rows_kernel<4, true> : gated_few_rows_kernel<4, false>, grid, block, 0, s, k);
     }
-    return run_tiles<kFwd>(k, a.rows, 2 * static_cast<int64_t>(a.F), 1, use_big(a.rows, 2 * static_cast<int64_t>(a.F), 1), fast, s);
+    return run_tiles<kFwd>(k, a.rows, 2 * static_cast<int64_t>(a.F), 1, pick(a.rows, 2 * static_cast<int64_t>(a.F), 1, a.C), fast, s);
 }
 
 hipError_t gated_bwd_bf16(const GatedArgs& a, hipStream_t s)
@@ -833,21 +856,21 @@ hipError_t gated_bwd_bf16(const GatedArgs& a, hipStream_t s)
     const ArmedEvents armed = armed_events();
     armed_events() = ArmedEvents{armed.start, nullptr};
     hipError_t e = hipSuccess;
-    int sum_rows = 0;
+    int summed = 0;
     if (a.rows > 0) {
         if (a.saved) {
             int64_t chunk;
-            sum_rows = gated_kept_chunks(a.rows, p.Fp, &chunk);
-            e = launch_gated_kept(a, d, sums, p.Fp, sum_rows, chunk, 1, s);
+            summed = gated_kept_chunks(a.rows, p.Fp, &chunk);
+            e = launch_gated_kept(a, d, sums, p.Fp, summed, chunk, 1, s);
         } else {
             Product k = product(a);
             k.d_out = d;
             k.sums = sums;
             k.Fp = p.Fp;
             const bool fast = a.C % 8 == 0 && aligned(a.x) && aligned(a.wg) && aligned(a.wu);
-            const bool big = use_big(a.rows, 2 * static_cast<int64_t>(a.F), 1);
-            sum_rows = static_cast<int>(tiles(a.rows, big ? Big::BM : Small::BM)) * (big ? Big::WP : Small::WP);
-            e = run_tiles<kAgain>(k, a.rows, 2 * static_cast<int64_t>(a.F), 1, big, fast, s);
+            const Tile t = pick(a.rows, 2 * static_cast<int64_t>(a.F), 1, a.C);
+            summed = static_cast<int>(sum_rows(a.rows, fast || t != Tile::kWide ? t : Tile::kBig));
+            e = run_tiles<kAgain>(k, a.rows, 2 * static_cast<int64_t>(a.F), 1, t, fast, s);
         }
         armed_events() = ArmedEvents{nullptr, nullptr};
         if (e != hipSuccess) return e;
@@ -856,12 +879,12 @@ hipError_t gated_bwd_bf16(const GatedArgs& a, hipStream_t s)
             k.d = d;
             k.Fp = p.Fp;
             k.out = static_cast<bf16_t*>(a.dx);
-            e = run_tiles<kDx>(k, a.rows, a.C, 1, use_big(a.rows, a.C, 1), a.C % 8 == 0 && aligned(a.wg) && aligned(a.wu), s);
+            e = run_tiles<kDx>(k, a.rows, a.C, 1, pick(a.rows, a.C, 1, 2 * static_cast<int64_t>(p.Fp)), a.C % 8 == 0 && aligned(a.wg) && aligned(a.wu), s);
             if (e != hipSuccess) return e;
         }
     }
     if (sums) {
-        e = launch_gated_bias_sums(a, sums, sum_rows, p.Fp, 1, s);
+        e = launch_gated_bias_sums(a, sums, summed, p.Fp, 1, s);
         if (e != hipSuccess) return e;
     }
     if (a.dwg || a.dwu) {
@@ -873,7 +896,7 @@ hipError_t gated_bwd_bf16(const GatedArgs& a, hipStream_t s)
         k.part = p.pieces > 1 ? part : nullptr;
         k.per = p.per;
         if (p.pieces == 1) armed_events() = ArmedEvents{nullptr, armed.stop};
-        e = run_tiles<kDw>(k, 2 * static_cast<int64_t>(p.Fp), a.C, p.pieces, use_big(2 * static_cast<int64_t>(p.Fp), a.C, 1),
+        e = run_tiles<kDw>(k, 2 * static_cast<int64_t>(p.Fp), a.C, p.pieces, pick(2 * static_cast<int64_t>(p.Fp), a.C, 1, a.rows),
                            a.C % 8 == 0 && aligned(a.x), s);
         armed_events() = ArmedEvents{nullptr, p.pieces > 1 ? armed.stop : nullptr};
         if (e == hipSuccess && p.pieces > 1) e = launch_gated_weight_sums(a, part, p.pieces, 1, s);
