@@ -133,6 +133,12 @@ struct Units {
             }
         }
     }
+    // Drops the units past `left` contraction values.
+    __device__ __forceinline__ void cut(int left)
+    {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) off[i] = k(i) < left ? off[i] : kOutside;
+    }
     // GATED: whether unit i of this wave comes from the second source.
     static __device__ __forceinline__ int second(int i)
     {
@@ -312,6 +318,18 @@ __global__ __launch_bounds__(S::kThreads, S::kWaves) void gated_product_kernel(P
     int left = 0, q_left = 0;                // contraction values from this stage on, and rows of the q source
     const bf16_t *p_src, *q_src, *q_src2;    // the stage's; q_src2: the other weight (gated: of the same stage, dx: from Fp on)
     const int64_t p_step = kPRows ? S::BK : static_cast<int64_t>(S::BK) * p_ld, q_step = kQRows ? S::BK : static_cast<int64_t>(S::BK) * q_ld;
+    bool cut = false;                        // whether this stage's units are fewer than a whole one's
+    auto whole_units = [&]() __attribute__((always_inline)) {
+        pu.template set<false>(p_valid, p_ld);
+        qu.template set<kQRows>(q_valid, q_ld);
+    };
+    auto cut_units = [&]() __attribute__((always_inline)) {
+        cut = left < S::BK || q_left < S::BK;
+        if (FAST && cut) {
+            pu.cut(left);
+            qu.cut(q_left);
+        }
+    };
     auto enter = [&]() __attribute__((always_inline)) {
         const Tile o = tile_of(lt);
         lk = 0;
@@ -320,19 +338,18 @@ __global__ __launch_bounds__(S::kThreads, S::kWaves) void gated_product_kernel(P
         q_left = MODE == kDx ? a.F : o.K;
         p_valid = static_cast<int>(kPRows ? min(static_cast<int64_t>(S::BM), a.rows - o.p0) : 2 * a.Fp - o.p0);
         q_valid = kQRows ? min(kQTile, a.F - o.q0) : a.C - o.q0;
-        pu.template set<false>(p_valid, p_ld);
-        qu.template set<kQRows>(q_valid, q_ld);
         p_src = kPRows ? (kGated ? a.x : a.d) + o.p0 * p_ld : a.d + o.m0 * p_ld + o.p0;
         const int64_t q_at = kQRows ? static_cast<int64_t>(o.q0) * q_ld : o.q0;
         q_src = MODE == kDw ? a.x + o.m0 * q_ld + q_at : a.wg + q_at;
         q_src2 = a.wu + q_at;
+        whole_units();
+        cut_units();
     };
     auto issue = [&](int i, char* st) __attribute__((always_inline)) {
         const bool is_p = i < S::kPLoads;
         const int j = is_p ? i : i - S::kPLoads;
         const bf16_t* src = is_p ? p_src : kQRows && qu.second(j) ? q_src2 : q_src;
-        const uint32_t off = (is_p ? pu.k(j) < left : qu.k(j) < q_left) ? (is_p ? pu.off[j] : qu.off[j]) : kOutside;
-        dma16(dma_rsrc(src, kAll), off, lds_addr(st + (is_p ? 0 : S::kPBytes) + (j * S::kThreads + wave * 64) * 16));
+        dma16(dma_rsrc(src, kAll), is_p ? pu.off[j] : qu.off[j], lds_addr(st + (is_p ? 0 : S::kPBytes) + (j * S::kThreads + wave * 64) * 16));
     };
     // Rows of any length and alignment pass through registers.
     uint4 held[FAST ? 1 : S::kLoads];
@@ -362,10 +379,23 @@ __global__ __launch_bounds__(S::kThreads, S::kWaves) void gated_product_kernel(P
             q_src += q_step;
             if (kQRows) q_src2 += q_step;
             if (MODE == kDx && lk * S::BK == a.Fp) q_src = q_src2, q_left = a.F;  // Fp is a multiple of BK
+            if (cut || left < S::BK || q_left < S::BK) {
+                if (cut) whole_units();
+                cut_units();
+            }
             return;
         }
         lt += step;
-        if (lt < end) enter();
+        if (lt < end) {
+            enter();
+        } else if (FAST) {
+            // no stage is left: the loads that still go out fetch nothing
+            lstages = 0x7fffffff;
+            pu.cut(0);
+            qu.cut(0);
+            left = q_left = 0x7fffffff;
+            cut = false;
+        }
     };
 
     f32x16 acc[S::TQ][S::TP];
@@ -384,13 +414,12 @@ __global__ __launch_bounds__(S::kThreads, S::kWaves) void gated_product_kernel(P
 
     if (first >= end) return;
     enter();
-    int ahead = 0;       // stages on their way or waiting
     int cur = S::NS - 1;  // place of the stage being multiplied
-    bool more = false;   // whether the stage that fills the place before it exists
     if constexpr (FAST) {
-        for (; ahead < S::NS - 1 && lt < end; ++ahead) {
+#pragma unroll 1
+        for (int n = 0; n < S::NS - 1; ++n) {
 #pragma unroll
-            for (int i = 0; i < S::kLoads; ++i) issue(i, ring + ahead * S::kStage);
+            for (int i = 0; i < S::kLoads; ++i) issue(i, ring + n * S::kStage);
             advance();
         }
     } else {
@@ -399,36 +428,50 @@ __global__ __launch_bounds__(S::kThreads, S::kWaves) void gated_product_kernel(P
         advance();
         if (lt < end) fetch();
     }
-    auto place = [&](int by) __attribute__((always_inline)) {
-        const int n = cur + by;
-        return ring + (n >= S::NS ? n - S::NS : n) * S::kStage;
-    };
+    const char* here = nullptr;  // the stage being read, and the place of the one before it
+    char* freed = nullptr;
     // Turns to the next stage.  It has landed for every wave after its own wait
     // and the barrier, and every wave has then read the one before into its
     // registers, so that one's place is free.
     auto turn_to_next = [&]() __attribute__((always_inline)) {
         if constexpr (FAST) {
-            if (ahead == S::NS - 1) wait_vm_lds<(S::NS - 2) * S::kLoads>();
-            else wait_vm_lds<0>();
+            wait_vm_lds<(S::NS - 2) * S::kLoads>();
             barrier_no_fence();
-            more = lt < end;
-            ahead += more ? 0 : -1;
         } else {
             __syncthreads();
             if (lt < end) {
-                put(place(2 % S::NS));
+                const int to = cur + 2 >= S::NS ? cur + 2 - S::NS : cur + 2;
+                put(ring + to * S::kStage);
                 advance();
                 if (lt < end) fetch();
             }
         }
+        freed = ring + cur * S::kStage;
         cur = cur + 1 == S::NS ? 0 : cur + 1;
+        here = ring + cur * S::kStage;
     };
-    // The loads that fill the freed place go out over the steps until the next turn.
-    auto issue_part = [&](int part) __attribute__((always_inline)) {
-        if (!FAST || !more) return;
+    // One step: the products of `f`, and between them the reads of the next
+    // step's operands (`next` of stage `here`) and part `part` of the loads that
+    // fill the freed place, one at a time: a wave issues in order, and a bunch
+    // of other instructions leaves the matrix unit without work.
+    auto step_of = [&](auto turn, Frags& f, Frags& n, int next, int part) __attribute__((always_inline)) {
+        constexpr int kProducts = S::TP * S::TQ, kReads = S::TP + S::TQ, kPart = FAST ? S::kLoads / kSteps : 0;
+        constexpr int kItems = kReads + kPart + 1;
+        auto item = [&](int x) __attribute__((always_inline)) {
+            if (x < S::TQ) read_q(n, here, next, x);
+            else if (x < kReads) read_p(n, here, next, x - S::TQ);
+            else if (x < kReads + kPart) issue(part * kPart + x - kReads, freed);
+            else if (FAST && part + 1 == kSteps) advance();
+        };
 #pragma unroll
-        for (int i = part * S::kLoads / kSteps; i < (part + 1) * S::kLoads / kSteps; ++i) issue(i, place(S::NS - 1));
-        if (part + 1 == kSteps) advance();
+        for (int m = 0; m < kProducts; ++m) {
+            const int i = m / S::TP, j = m % S::TP;
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.q[i], f.p[j], acc[i][j], 0, 0, 0);
+            if (m == 0 && turn()) turn_to_next();
+#pragma unroll
+            for (int x = m * kItems / kProducts; x < (m + 1) * kItems / kProducts; ++x) item(x);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     };
 
     for (int t = first; t < end; t += step) {
@@ -446,42 +489,36 @@ __global__ __launch_bounds__(S::kThreads, S::kWaves) void gated_product_kernel(P
 #pragma unroll
                 for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
         turn_to_next();
-        issue_part(0);
+        if constexpr (FAST) {
 #pragma unroll
-        for (int i = 0; i < S::TQ; ++i) read_q(frags[0], place(0), 0, i);
-#pragma unroll
-        for (int j = 0; j < S::TP; ++j) read_p(frags[0], place(0), 0, j);
-        for (int kt = 0; kt < nk; ++kt) {
-#pragma unroll
-            for (int kk = 0; kk < kSteps; ++kk) {
-                const bool last = kk + 1 == kSteps;
-                const bool next = !last || kt + 1 < nk;
-                // The last step's operands are in registers: on to the next
-                // stage, whose first operands arrive during this step.
-                if (last && next) turn_to_next();
-                Frags &f = frags[kk & 1], &n = frags[(kk + 1) & 1];
-                static_assert(kSteps % 2 == 0, "the next stage's operands take the first place again");
-#pragma unroll
-                for (int i = 0; i < S::TQ; ++i) {
-                    if (next) {
-                        read_q(n, place(0), last ? 0 : kk + 1, i);
-#pragma unroll
-                        for (int j = i * S::TP / S::TQ; j < (i + 1) * S::TP / S::TQ; ++j) read_p(n, place(0), last ? 0 : kk + 1, j);
-                        if (i == S::TQ - 1) issue_part(last ? 0 : kk + 1);
-                    }
-#pragma unroll
-                    for (int j = 0; j < S::TP; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.q[i], f.p[j], acc[i][j], 0, 0, 0);
-                }
-            }
+            for (int i = 0; i < S::kLoads / kSteps; ++i) issue(i, freed);
         }
+#pragma unroll
+        for (int i = 0; i < S::TQ; ++i) read_q(frags[0], here, 0, i);
+#pragma unroll
+        for (int j = 0; j < S::TP; ++j) read_p(frags[0], here, 0, j);
+        static_assert(kSteps % 2 == 0 && S::kLoads % kSteps == 0, "the next stage's operands take the first place again");
+        auto first_steps = [&]() __attribute__((always_inline)) {
+#pragma unroll
+            for (int kk = 0; kk + 1 < kSteps; ++kk) step_of(std::false_type{}, frags[kk & 1], frags[(kk + 1) & 1], kk + 1, kk + 1);
+        };
+        for (int kt = 1; kt < nk; ++kt) {
+            first_steps();
+            // The last step's operands are in registers: on to the next stage,
+            // whose first operands arrive during this step.
+            step_of(std::true_type{}, frags[1], frags[0], 0, 0);
+        }
+        first_steps();
+#pragma unroll
+        for (int m = 0; m < S::TP * S::TQ; ++m)
+            acc[m / S::TP][m % S::TP] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(frags[1].q[m / S::TP], frags[1].p[m % S::TP], acc[m / S::TP][m % S::TP], 0, 0, 0);
         // Every wave is done with the last stage, whose place the outputs pass
         // through; it is filled again after the next turn.
         float* biases = reinterpret_cast<float*>(ring + S::NS * S::kStage);
         if (kGated && a.bg && threadIdx.x < S::BN) biases[threadIdx.x] = bias;
         wait_vm_lds<63>();
         barrier_no_fence();
-        char* turn = place(0) + wave * S::kWaveLds;
+        char* turn = const_cast<char*>(here) + wave * S::kWaveLds;
 
         // A lane holds columns 8v + 4q + {0..3} of a q tile and p row `col`.
         if constexpr (kGated) {
@@ -661,6 +698,7 @@ __global__ __launch_bounds__(S::kThreads, S::kWaves) void gated_product_kernel(P
             }
         }
     }
+    if constexpr (FAST) wait_vm_lds<0>();  // no load may arrive in LDS that is no longer this workgroup's
 }
 
 // Few rows: the layer is a stream over its weights.  A workgroup takes 16
