@@ -119,7 +119,8 @@ hipError_t launch_gated_bias_sums(const GatedArgs& a, const float* sums, int row
     k.dtype = dtype;
     k.out[0] = a.dbg;
     k.out[1] = a.dbu;
-    return launch_column_sums(k, 2, s);
+    k.nq = 2;
+    return launch_column_sums(k, s);
 }
 
 hipError_t launch_gated_weight_sums(const GatedArgs& a, const float* part, int pieces, int dtype, hipStream_t s)
@@ -134,7 +135,8 @@ hipError_t launch_gated_weight_sums(const GatedArgs& a, const float* part, int p
     k.dtype = dtype;
     k.out[0] = a.dwg;
     k.out[1] = a.dwu;
-    return launch_column_sums(k, 2, s);
+    k.nq = 2;
+    return launch_column_sums(k, s);
 }
 
 hipError_t launch_gated_fwd(const GatedArgs& a, int dtype, hipStream_t s)

@@ -96,8 +96,14 @@ struct SumArgs {
     int dtype;
     int64_t q_pitch;      // distance of two q blocks within a row of `part`, in values
     void* out[kSumOutputs];
+    int nq;               // outputs
+    // Also, for each of gate_groups groups, gate_split consecutive rows of
+    // `part` from value gate_at on go to a row of gate_out.
+    void* gate_out;
+    int64_t gate_at;
+    int gate_split, gate_groups;
 };
-hipError_t launch_column_sums(const SumArgs& a, int nq, hipStream_t s);
+hipError_t launch_column_sums(const SumArgs& a, hipStream_t s);
 
 // Norms before and after a block with gate and residual scale (see
 // conv_block_norm_fwd / conv_block_norm_bwd in include/convmi.h).
