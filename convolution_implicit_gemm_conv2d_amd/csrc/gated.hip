@@ -1,946 +1,10 @@
-// Gated feed-forward layer in bf16 on the matrix units:
-//
-//   g = x Wg^T + bg,  u = x Wu^T + bu,  h = act(g) u,
-//   dg = dh u act'(g),  du = dh act(g),
-//   dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x.
-//
-// One product kernel serves all of it.  An output tile is BM "p" rows by BN
-// "q" columns; the q operand is the matrix instruction's first (its rows are
-// the output's contiguous dimension, so a lane ends with runs of four
-// consecutive values of one output row):
-//   forward, and g and u again:  p: rows of x,        q: rows of Wg and Wu
-//   dx:                          p: rows of [dg|du],  q: columns of [Wg; Wu]
-//   dW:                          p: columns of [dg|du], q: columns of x
-// A wave's q tiles alternate between Wg and Wu in the forward product, so a
-// lane holds g and u of the same elements and the activation, the product and
-// the biases happen in registers.  Operands whose contraction index is
-// contiguous are staged in LDS as rows of BK values, the others as they lie in
-// memory, rows of one contraction index, and are read with the LDS transpose
-// read.
-//
-// dg and du are rounded to bf16 once, as operands of the products that follow
-// (their column sums, the bias gradients, are taken before); sums are fp32.
-#include "gated.hpp"
-
-#include <algorithm>
-#include <atomic>
-#include <type_traits>
+// The gated feed-forward layer in bf16 (see gated_product.hpp).
+#include "gated_product.hpp"
 
 namespace convmi {
-namespace {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) char lds_char;
-typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
-typedef __attribute__((address_space(3))) bf16x8 lds_bf16x8;
-
-enum Mode { kFwd, kAgain, kDx, kDw };
-
-// WP x WQ waves, each TP x TQ tiles of 32x32; BK contraction values a stage,
-// NS stages in the ring.
-template <int WP_, int WQ_, int TP_, int TQ_, int BK_, int NS_>
-struct Shape {
-    static constexpr int WP = WP_, WQ = WQ_, TP = TP_, TQ = TQ_, BK = BK_, NS = NS_;
-    static constexpr int BM = WP * TP * 32, BN = WQ * TQ * 32, kThreads = WP * WQ * 64;
-    static constexpr int kPBytes = BM * BK * 2, kQBytes = BN * BK * 2, kStage = kPBytes + kQBytes;
-    static constexpr int kLds = NS * kStage + BN * 4;  // the ring and a tile's biases
-    static constexpr int kPLoads = BM * BK / 8 / kThreads, kQLoads = BN * BK / 8 / kThreads;
-    static constexpr int kLoads = kPLoads + kQLoads;
-    static constexpr int kWaveLds = kStage / (WP * WQ);  // a wave's part of a stage
-    static constexpr int kWaves = TP * TQ > 8 ? 1 : 2;  // of a SIMD: the accumulators take 16 TP TQ of its 512 registers
-    static constexpr int kPerCu = 4 * kWaves / (WP * WQ);  // workgroups
-    static_assert(kPerCu * kLds <= 163840 && BN <= kThreads, "");
-    static_assert(kWaveLds >= 4096, "a wave's output passes through its part of a stage");
-    static_assert(kPLoads > 0 && kQLoads > 0 && TQ % 2 == 0 && NS >= 2, "");
-};
-
-struct Product {
-    const bf16_t *x, *wg, *wu, *bg, *bu, *dh;
-    const bf16_t* d;      // [dg|du], rows of 2 Fp
-    bf16_t *h, *out, *out2;  // out: dx, or dWg with dWu in out2
-    bf16_t* d_out;
-    float *saved, *sums, *part;
-    int64_t rows, per;    // per: rows of a piece (dW)
-    int C, F, Fp, act;
-    int p_tiles, q_tiles, tiles;  // tiles: of all pieces
-};
-
-// Where a 16-byte unit of a staged row sits.  Rows of BK values: 8 (or, with
-// BK 32, 16) rows read at one unit reach all banks.  Rows of a contraction
-// index: the four rows and four units of a transpose read do.
-template <int BK>
-__device__ __forceinline__ int swz_row(int r) { return BK == 64 ? (r & 7) : ((r >> 2) & 3); }
-__device__ __forceinline__ int swz_k(int k) { return ((k & 3) << 2) ^ (k & 2); }
-
-// The first n >= 1 of eight values, zeros after them.
-__device__ __forceinline__ uint4 guarded16(const bf16_t* p, int n)
-{
-    if (n >= 8) return load16_any(p);
-    uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const uint32_t v = p[min(e, n - 1)];
-        w[e >> 1] |= (e < n ? v : 0u) << (16 * (e & 1));
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// Eight values at byte `off` of a buffer at any element alignment, none where
-// it is kOutside.  `ragged` (uniform: the last unit of some row is cut): the
-// first n of them by elements.  No branches but the uniform one.
-constexpr uint32_t kAll = 0x7ffffffcu;
-__device__ __forceinline__ uint4 unit_load(rsrc_t r, uint32_t off, bool ragged, int n)
-{
-    if (!ragged) return buffer_load16(r, off);
-    uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        w[e >> 1] |= static_cast<uint32_t>(__builtin_amdgcn_raw_buffer_load_b16(r, e < n ? off + 2 * e : kOutside, 0, 0)) << (16 * (e & 1));
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// Addresses of one operand's units for a thread: `off` within a tile (kOutside
-// where the tile's row or column does not exist) and the unit's contraction
-// offset.  ROWS: R rows of contraction values; otherwise BK rows of a
-// contraction index with R columns each.
-template <typename S, int R, bool ROWS>
-struct Units {
-    static constexpr int kN = R * S::BK / 8 / S::kThreads, kRow = ROWS ? S::BK / 8 : R / 8;
-    uint32_t off[kN];
-    // contraction offset (within a stage) of unit i of this thread
-    static __device__ __forceinline__ int k(int i)
-    {
-        const int idx = i * S::kThreads + threadIdx.x, r = idx / kRow;
-        return ROWS ? ((idx % kRow) ^ swz_row<S::BK>(r)) * 8 : r;
-    }
-    // `valid` rows (ROWS) or columns of the tile exist.  GATED: two sources
-    // alternate every 32 rows.
-    template <bool GATED>
-    __device__ __forceinline__ void set(int valid, int ld)
-    {
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            const int idx = i * S::kThreads + threadIdx.x, r = idx / kRow;
-            if (ROWS) {
-                const int row = GATED ? (r >> 6) * 32 + (r & 31) : r;
-                off[i] = row < valid ? (static_cast<uint32_t>(row) * ld + k(i)) * 2u : kOutside;
-            } else {
-                const int c = ((idx % kRow) ^ swz_k(r)) * 8;
-                off[i] = c < valid ? (static_cast<uint32_t>(r) * ld + c) * 2u : kOutside;
-            }
-        }
-    }
-    // Drops the units past `left` contraction values.
-    __device__ __forceinline__ void cut(int left)
-    {
-#pragma unroll
-        for (int i = 0; i < kN; ++i) off[i] = k(i) < left ? off[i] : kOutside;
-    }
-    // GATED: whether unit i of this wave comes from the second source.
-    static __device__ __forceinline__ int second(int i)
-    {
-        return (((i * S::kThreads + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 64) / kRow) >> 5) & 1;
-    }
-    // Values of unit i that exist, for the guarded loads.
-    __device__ __forceinline__ int count(int i, int k_left, int valid) const
-    {
-        if (off[i] == kOutside) return 0;
-        if (ROWS) return k_left - k(i);
-        const int idx = i * S::kThreads + threadIdx.x, r = idx / kRow;
-        return r < k_left ? valid - ((idx % kRow) ^ swz_k(r)) * 8 : 0;
-    }
-};
-
-// Reads fragments (8 contraction values of one row or column a lane) of tile
-// `t` at step kk (16 values).
-template <typename S>
-struct RowFrag {
-    int col, off[S::BK / 16];
-    __device__ __forceinline__ RowFrag(int)
-    {
-        const int lane = threadIdx.x & 63;
-        col = lane & 31;
-#pragma unroll
-        for (int kk = 0; kk < S::BK / 16; ++kk)
-            off[kk] = col * (S::BK * 2) + (((kk * 2 + (lane >> 5)) ^ swz_row<S::BK>(col)) << 4);
-    }
-    __device__ __forceinline__ bf16x8 read(const lds_char* base, int tile, int, int kk) const
-    {
-        return *reinterpret_cast<const lds_bf16x8*>(base + tile * (32 * S::BK * 2) + off[kk]);
-    }
-};
-template <typename S, int R, int T>
-struct ColFrag {
-    int off[T];
-    __device__ __forceinline__ ColFrag(int tile0)
-    {
-        const int lane = threadIdx.x & 63, g4 = lane >> 4, s16 = lane & 15;
-        const int k = 8 * (g4 >> 1) + (s16 >> 2);
-#pragma unroll
-        for (int t = 0; t < T; ++t) {
-            const int c = (tile0 + t) * 32 + 16 * (g4 & 1) + 4 * (s16 & 3);
-            off[t] = k * (R * 2) + (((c >> 3) ^ swz_k(k)) << 4) + (c & 7) * 2;
-        }
-    }
-    __device__ __forceinline__ bf16x8 read(const lds_char* base, int, int t, int kk) const
-    {
-        const lds_char* p = base + kk * 16 * (R * 2) + off[t];
-        const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)p);
-        const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(p + 4 * (R * 2)));
-        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-    }
-};
-
-// A wave's 32 output rows on their way from the accumulators' layout (a lane
-// holds columns 8v + 4q + {0..3} of row `lane & 31`) to rows in memory: through
-// the wave's own part of LDS, U units of 16 bytes a row, so that a store
-// instruction writes whole lines.  LDS serves a wave in order; only the
-// compiler has to keep the order too.
-__device__ __forceinline__ void wave_order()
-{
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_wave_barrier();
-}
-template <int U>
-__device__ __forceinline__ int turn_at(int r, int unit) { return (r * U + (unit ^ ((r >> (U == 8 ? 1 : 2)) & (U - 1)))) * 16; }
-
-// `cols` columns of T exist from `p` (uniform) on, `rows` rows of pitch ld.
-template <int U, typename T>
-__device__ __forceinline__ void turn_out(const char* lds, T* p, uint32_t ld, int rows, int cols)
-{
-    constexpr int V = 16 / sizeof(T);
-    const int lane = threadIdx.x & 63;
-    const rsrc_t out = make_rsrc(p, kAll);
-    const bool ragged = cols < U * V && cols % V != 0;
-#pragma unroll
-    for (int i = 0; i < U / 2; ++i) {
-        const int r = (i * 64 + lane) / U, unit = lane % U, n = cols - unit * V;
-        const uint4 v = *reinterpret_cast<const uint4*>(lds + turn_at<U>(r, unit));
-        const uint32_t off = r < rows && n > 0 ? (r * ld + unit * V) * static_cast<uint32_t>(sizeof(T)) : kOutside;
-        if (!ragged) {
-            buffer_store16(out, off, v);
-        } else {
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const uint32_t at = e < n && off != kOutside ? off + e * static_cast<uint32_t>(sizeof(T)) : kOutside;
-                if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1))), out, at, 0, 0);
-                else __builtin_amdgcn_raw_buffer_store_b32(w[e], out, at, 0, 0);
-            }
-        }
-    }
-}
-
-// Sums 16 values over the 32 lanes of a half wave: in each step a lane gives
-// half of its values to a partner and keeps the other half.  A lane ends with
-// the sum of value half_sum_of(lane).
-__device__ __forceinline__ int half_sum_of(int lane) { return lane >> 1 & 15; }
-template <int CTRL, int N>
-__device__ __forceinline__ void half_sum_step(float* v, bool up)
-{
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const float send = up ? v[i] : v[i + N], keep = up ? v[i + N] : v[i];
-        v[i] = keep + dpp_shift<CTRL, 0xf>(send);
-    }
-}
-__device__ __forceinline__ float half_sum16(float (&v)[16], int lane)
-{
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        // swaps the odd rows of 16 lanes of one with the even ones of the other
-        const auto t = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[i]), __float_as_uint(v[i + 8]), false, false);
-        v[i] = __uint_as_float(t[0]) + __uint_as_float(t[1]);
-    }
-    half_sum_step<0x140, 4>(v, lane & 8);  // lane 15 - i of a row
-    half_sum_step<0x141, 2>(v, lane & 4);  // 7 - i of half a row
-    half_sum_step<0x4e, 1>(v, lane & 2);   // i ^ 2
-    return v[0] + dpp_shift<0xb1, 0xf>(v[0]);  // i ^ 1
-}
-
-// Tile t of the product.  Eight p tiles share their q tiles before the next
-// eight come.
-__device__ __forceinline__ void pick_tile(int t, int p_tiles, int q_tiles, int& pt, int& qt, int& piece)
-{
-    const int tiles = p_tiles * q_tiles;
-    piece = t / tiles;
-    t -= piece * tiles;
-    constexpr int kGroup = 8;
-    const int g = t / (kGroup * q_tiles), in = t - g * kGroup * q_tiles;
-    const int size = min(kGroup, p_tiles - g * kGroup);
-    qt = in / size;
-    pt = g * kGroup + in - qt * size;
-}
-
-template <typename S, int MODE, bool FAST>
-__global__ __launch_bounds__(S::kThreads, S::kWaves) void gated_product_kernel(Product a)
-{
-    extern __shared__ char ring[];
-    constexpr bool kGated = MODE == kFwd || MODE == kAgain;
-    constexpr bool kPRows = MODE != kDw, kQRows = kGated;
-    constexpr int kQTile = kGated ? S::BN / 2 : S::BN;  // output columns of a tile
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wp = wave / S::WQ, wq = wave % S::WQ;
-    const int col = lane & 31, q = lane >> 5;
-    const int p_ld = kGated ? a.C : 2 * a.Fp, q_ld = a.C;
-
-    // Workgroup b runs on XCD b mod 8; an XCD takes a contiguous run of tiles,
-    // its workgroups take them in turn.
-    const int xcd = blockIdx.x & 7, per = a.tiles >> 3, rem = a.tiles & 7, step = gridDim.x >> 3;
-    const int first = xcd * per + min(xcd, rem) + (blockIdx.x >> 3);
-    const int end = xcd * per + min(xcd, rem) + per + (xcd < rem ? 1 : 0);
-
-    struct Tile {
-        int64_t p0, m0;  // first p row; first contraction index (dW)
-        int q0, K, pt, piece;
-    };
-    auto tile_of = [&](int t) __attribute__((always_inline)) {
-        Tile r;
-        int qt;
-        pick_tile(t, a.p_tiles, a.q_tiles, r.pt, qt, r.piece);
-        r.p0 = static_cast<int64_t>(r.pt) * S::BM;
-        r.q0 = qt * kQTile;
-        r.m0 = MODE == kDw ? r.piece * a.per : 0;
-        r.K = kGated ? a.C : MODE == kDx ? 2 * a.Fp : static_cast<int>(min(a.per, a.rows - r.m0));
-        return r;
-    };
-    auto stages = [](int K) __attribute__((always_inline)) { return max(1, (K + S::BK - 1) / S::BK); };
-
-    // The next stage to load: stage lk of tile lt.  Loads run ahead over the
-    // ends of tiles, so a tile's first stages arrive during the epilogue of the
-    // one before.
-    Units<S, S::BM, kPRows> pu;
-    Units<S, S::BN, kQRows> qu;
-    int lt = first, lk = 0, lstages = 0, p_valid = 0, q_valid = 0;
-    int left = 0, q_left = 0;                // contraction values from this stage on, and rows of the q source
-    const bf16_t *p_src, *q_src, *q_src2;    // the stage's; q_src2: the other weight (gated: of the same stage, dx: from Fp on)
-    const int64_t p_step = kPRows ? S::BK : static_cast<int64_t>(S::BK) * p_ld, q_step = kQRows ? S::BK : static_cast<int64_t>(S::BK) * q_ld;
-    bool cut = false;                        // whether this stage's units are fewer than a whole one's
-    auto whole_units = [&]() __attribute__((always_inline)) {
-        pu.template set<false>(p_valid, p_ld);
-        qu.template set<kQRows>(q_valid, q_ld);
-    };
-    auto cut_units = [&]() __attribute__((always_inline)) {
-        cut = left < S::BK || q_left < S::BK;
-        if (FAST && cut) {
-            pu.cut(left);
-            qu.cut(q_left);
-        }
-    };
-    auto enter = [&]() __attribute__((always_inline)) {
-        const Tile o = tile_of(lt);
-        lk = 0;
-        lstages = stages(o.K);
-        left = o.K;
-        q_left = MODE == kDx ? a.F : o.K;
-        p_valid = static_cast<int>(kPRows ? min(static_cast<int64_t>(S::BM), a.rows - o.p0) : 2 * a.Fp - o.p0);
-        q_valid = kQRows ? min(kQTile, a.F - o.q0) : a.C - o.q0;
-        p_src = kPRows ? (kGated ? a.x : a.d) + o.p0 * p_ld : a.d + o.m0 * p_ld + o.p0;
-        const int64_t q_at = kQRows ? static_cast<int64_t>(o.q0) * q_ld : o.q0;
-        q_src = MODE == kDw ? a.x + o.m0 * q_ld + q_at : a.wg + q_at;
-        q_src2 = a.wu + q_at;
-        whole_units();
-        cut_units();
-    };
-    auto issue = [&](int i, char* st) __attribute__((always_inline)) {
-        const bool is_p = i < S::kPLoads;
-        const int j = is_p ? i : i - S::kPLoads;
-        const bf16_t* src = is_p ? p_src : kQRows && qu.second(j) ? q_src2 : q_src;
-        dma16(dma_rsrc(src, kAll), is_p ? pu.off[j] : qu.off[j], lds_addr(st + (is_p ? 0 : S::kPBytes) + (j * S::kThreads + wave * 64) * 16));
-    };
-    // Rows of any length and alignment pass through registers.
-    uint4 held[FAST ? 1 : S::kLoads];
-    auto fetch = [&]() __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < (FAST ? 0 : S::kLoads); ++i) {
-            const bool is_p = i < S::kPLoads;
-            const int j = is_p ? i : i - S::kPLoads, have = is_p ? left : q_left;
-            const bf16_t* src = is_p ? p_src : kQRows && qu.second(j) ? q_src2 : q_src;
-            const int n = is_p ? pu.count(j, have, p_valid) : qu.count(j, have, q_valid);
-            const bool ragged = (is_p ? kPRows : kQRows) ? have < S::BK && have % 8 != 0 : (is_p ? p_valid % 8 != 0 : q_valid % 8 != 0);
-            held[i] = unit_load(make_rsrc(src, kAll), n > 0 ? (is_p ? pu.off[j] : qu.off[j]) : kOutside, ragged, n);
-        }
-    };
-    auto put = [&](char* st) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < (FAST ? 0 : S::kLoads); ++i) {
-            const int j = i < S::kPLoads ? i : i - S::kPLoads;
-            *reinterpret_cast<uint4*>(st + (i < S::kPLoads ? 0 : S::kPBytes) + (j * S::kThreads + threadIdx.x) * 16) = held[i];
-        }
-    };
-    auto advance = [&]() __attribute__((always_inline)) {
-        if (++lk < lstages) {
-            left -= S::BK;
-            q_left -= S::BK;
-            p_src += p_step;
-            q_src += q_step;
-            if (kQRows) q_src2 += q_step;
-            if (MODE == kDx && lk * S::BK == a.Fp) q_src = q_src2, q_left = a.F;  // Fp is a multiple of BK
-            if (cut || left < S::BK || q_left < S::BK) {
-                if (cut) whole_units();
-                cut_units();
-            }
-            return;
-        }
-        lt += step;
-        if (lt < end) {
-            enter();
-        } else if (FAST) {
-            // no stage is left: the loads that still go out fetch nothing
-            lstages = 0x7fffffff;
-            pu.cut(0);
-            qu.cut(0);
-            left = q_left = 0x7fffffff;
-            cut = false;
-        }
-    };
-
-    f32x16 acc[S::TQ][S::TP];
-    typename std::conditional<kPRows, RowFrag<S>, ColFrag<S, S::BM, S::TP>>::type pf(wp * S::TP);
-    typename std::conditional<kQRows, RowFrag<S>, ColFrag<S, S::BN, S::TQ>>::type qf(wq * S::TQ);
-    struct Frags {
-        bf16x8 q[S::TQ], p[S::TP];
-    } frags[2];
-    auto read_q = [&](Frags& f, const char* st, int kk, int i) __attribute__((always_inline)) {
-        f.q[i] = qf.read((const lds_char*)st + S::kPBytes, wq * S::TQ + i, i, kk);
-    };
-    auto read_p = [&](Frags& f, const char* st, int kk, int j) __attribute__((always_inline)) {
-        f.p[j] = pf.read((const lds_char*)st, wp * S::TP + j, j, kk);
-    };
-    constexpr int kSteps = S::BK / 16;
-
-    if (first >= end) return;
-    enter();
-    int cur = S::NS - 1;  // place of the stage being multiplied
-    if constexpr (FAST) {
-#pragma unroll 1
-        for (int n = 0; n < S::NS - 1; ++n) {
-#pragma unroll
-            for (int i = 0; i < S::kLoads; ++i) issue(i, ring + n * S::kStage);
-            advance();
-        }
-    } else {
-        fetch();
-        put(ring);
-        advance();
-        if (lt < end) fetch();
-    }
-    const char* here = nullptr;  // the stage being read, and the place of the one before it
-    char* freed = nullptr;
-    // Turns to the next stage.  It has landed for every wave after its own wait
-    // and the barrier, and every wave has then read the one before into its
-    // registers, so that one's place is free.
-    auto turn_to_next = [&]() __attribute__((always_inline)) {
-        if constexpr (FAST) {
-            wait_vm_lds<(S::NS - 2) * S::kLoads>();
-            barrier_no_fence();
-        } else {
-            __syncthreads();
-            if (lt < end) {
-                const int to = cur + 2 >= S::NS ? cur + 2 - S::NS : cur + 2;
-                put(ring + to * S::kStage);
-                advance();
-                if (lt < end) fetch();
-            }
-        }
-        freed = ring + cur * S::kStage;
-        cur = cur + 1 == S::NS ? 0 : cur + 1;
-        here = ring + cur * S::kStage;
-    };
-    // One step: the products of `f`, and between them the reads of the next
-    // step's operands (`next` of stage `here`) and part `part` of the loads that
-    // fill the freed place, one at a time: a wave issues in order, and a bunch
-    // of other instructions leaves the matrix unit without work.
-    auto step_of = [&](auto turn, Frags& f, Frags& n, int next, int part) __attribute__((always_inline)) {
-        constexpr int kProducts = S::TP * S::TQ, kReads = S::TP + S::TQ, kPart = FAST ? S::kLoads / kSteps : 0;
-        constexpr int kItems = kReads + kPart + 1;
-        auto item = [&](int x) __attribute__((always_inline)) {
-            if (x < S::TQ) read_q(n, here, next, x);
-            else if (x < kReads) read_p(n, here, next, x - S::TQ);
-            else if (x < kReads + kPart) issue(part * kPart + x - kReads, freed);
-            else if (FAST && part + 1 == kSteps) advance();
-        };
-#pragma unroll
-        for (int m = 0; m < kProducts; ++m) {
-            const int i = m / S::TP, j = m % S::TP;
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.q[i], f.p[j], acc[i][j], 0, 0, 0);
-            if (m == 0 && turn()) turn_to_next();
-#pragma unroll
-            for (int x = m * kItems / kProducts; x < (m + 1) * kItems / kProducts; ++x) item(x);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-    };
-
-    for (int t = first; t < end; t += step) {
-        const Tile o = tile_of(t);
-        const int nk = stages(o.K);
-        float bias = 0.f;  // of column threadIdx.x of the tile (both halves)
-        if (kGated && a.bg && threadIdx.x < S::BN) {
-            const int f = o.q0 + threadIdx.x % kQTile;
-            if (f < a.F) bias = bf16_to_f((threadIdx.x < kQTile ? a.bg : a.bu)[f]);
-        }
-#pragma unroll
-        for (int i = 0; i < S::TQ; ++i)
-#pragma unroll
-            for (int j = 0; j < S::TP; ++j)
-#pragma unroll
-                for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
-        turn_to_next();
-        if constexpr (FAST) {
-#pragma unroll
-            for (int i = 0; i < S::kLoads / kSteps; ++i) issue(i, freed);
-        }
-#pragma unroll
-        for (int i = 0; i < S::TQ; ++i) read_q(frags[0], here, 0, i);
-#pragma unroll
-        for (int j = 0; j < S::TP; ++j) read_p(frags[0], here, 0, j);
-        static_assert(kSteps % 2 == 0 && S::kLoads % kSteps == 0, "the next stage's operands take the first place again");
-        auto first_steps = [&]() __attribute__((always_inline)) {
-#pragma unroll
-            for (int kk = 0; kk + 1 < kSteps; ++kk) step_of(std::false_type{}, frags[kk & 1], frags[(kk + 1) & 1], kk + 1, kk + 1);
-        };
-        for (int kt = 1; kt < nk; ++kt) {
-            first_steps();
-            // The last step's operands are in registers: on to the next stage,
-            // whose first operands arrive during this step.
-            step_of(std::true_type{}, frags[1], frags[0], 0, 0);
-        }
-        first_steps();
-#pragma unroll
-        for (int m = 0; m < S::TP * S::TQ; ++m)
-            acc[m / S::TP][m % S::TP] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(frags[1].q[m / S::TP], frags[1].p[m % S::TP], acc[m / S::TP][m % S::TP], 0, 0, 0);
-        // Every wave is done with the last stage, whose place the outputs pass
-        // through; it is filled again after the next turn.
-        float* biases = reinterpret_cast<float*>(ring + S::NS * S::kStage);
-        if (kGated && a.bg && threadIdx.x < S::BN) biases[threadIdx.x] = bias;
-        wait_vm_lds<63>();
-        barrier_no_fence();
-        char* turn = const_cast<char*>(here) + wave * S::kWaveLds;
-
-        // A lane holds columns 8v + 4q + {0..3} of a q tile and p row `col`.
-        if constexpr (kGated) {
-            // One step takes 32 rows and 32 columns.  A loop with one copy of its
-            // code: unrolled over the accumulators it outgrows the instruction
-            // cache.
-            constexpr int M = S::TQ / 2;
-            const int f0 = o.q0 + wq * M * 32;  // the wave's first column
-            float tg[M], tu[M];                 // column sums
-#pragma unroll
-            for (int m = 0; m < M; ++m) tg[m] = tu[m] = 0.f;
-            uint4 dh[2];
-            auto load_dh = [&](int s) __attribute__((always_inline)) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int64_t r0 = o.p0 + (wp * S::TP + s / M) * 32;
-                    const int r = i * 16 + lane / 4, fs = f0 + s % M * 32, n = a.F - fs - lane % 4 * 8;
-                    const rsrc_t in = make_rsrc(a.dh + r0 * a.F + fs, kAll);
-                    const bool on = r < a.rows - r0 && n > 0;
-                    dh[i] = unit_load(in, on ? (r * a.F + lane % 4 * 8) * 2u : kOutside, fs + 32 > a.F && a.F % 8 != 0, on ? n : 0);
-                }
-            };
-            if constexpr (MODE == kAgain) load_dh(0);
-#pragma unroll 1
-            for (int s = 0; s < S::TP * M; ++s) {
-                const int64_t r0 = o.p0 + (wp * S::TP + s / M) * 32;
-                const int rows = static_cast<int>(min(static_cast<int64_t>(32), a.rows - r0));
-                const int fs = f0 + s % M * 32;
-                // Four columns 8v + 4q + {0..3}: g and u with their biases.
-                auto take = [&](int v, float (&g)[4], float (&u)[4]) __attribute__((always_inline)) {
-                    // keeps the registers of one group from overlapping the next
-                    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                    for (int n = 0; n < S::TP * M; ++n)
-                        if (s == n) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) g[e] = acc[n % M * 2][n / M][4 * v + e], u[e] = acc[n % M * 2 + 1][n / M][4 * v + e];
-                        }
-                    if (a.bg) {
-                        const float* b = biases + wq * M * 32 + s % M * 32 + 8 * v + 4 * q;
-                        const float4 bg = *reinterpret_cast<const float4*>(b), bu = *reinterpret_cast<const float4*>(b + kQTile);
-                        g[0] += bg.x; g[1] += bg.y; g[2] += bg.z; g[3] += bg.w;
-                        u[0] += bu.x; u[1] += bu.y; u[2] += bu.z; u[3] += bu.w;
-                    }
-                };
-                auto lay = [&](char* to, int v, const float* w) __attribute__((always_inline)) {
-                    *reinterpret_cast<uint2*>(to + turn_at<4>(col, v) + 8 * q) = make_uint2(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]));
-                };
-                if constexpr (MODE == kFwd) {
-                    if (a.saved) {
-#pragma unroll
-                        for (int n = 0; n < 2; ++n) {
-#pragma unroll
-                            for (int v = 0; v < 4; ++v) {
-                                float g[4], u[4];
-                                take(v, g, u);
-                                const float(&w)[4] = n ? u : g;
-                                *reinterpret_cast<float4*>(turn + turn_at<8>(col, 2 * v + q)) = make_float4(w[0], w[1], w[2], w[3]);
-                            }
-                            wave_order();
-                            turn_out<8>(turn, a.saved + r0 * 2 * a.F + (n ? a.F : 0) + fs, 2u * a.F, rows, a.F - fs);
-                            wave_order();
-                        }
-                    }
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        float g[4], u[4];
-                        take(v, g, u);
-                        with_act(a.act, [&](auto kind) __attribute__((always_inline)) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) g[e] = act_value<kind()>(g[e]) * u[e];
-                        });
-                        lay(turn, v, g);
-                    }
-                    wave_order();
-                    turn_out<4>(turn, a.h + r0 * a.F + fs, a.F, rows, a.F - fs);
-                } else {
-                    char* other = turn + 2048;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) *reinterpret_cast<uint4*>(turn + turn_at<4>(i * 16 + lane / 4, lane % 4)) = dh[i];
-                    wave_order();
-                    if (s + 1 < S::TP * M) load_dh(s + 1);
-                    float sg[16], su[16];
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        float g[4], u[4];
-                        take(v, g, u);
-                        const uint2 raw = *reinterpret_cast<const uint2*>(turn + turn_at<4>(col, v) + 8 * q);
-                        const float h[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u),
-                                            __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xffff0000u)};
-                        with_act(a.act, [&](auto kind) __attribute__((always_inline)) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const ActPair p = act_pair<kind()>(g[e]);
-                                g[e] = h[e] * u[e] * p.d;
-                                u[e] = h[e] * p.v;
-                            }
-                        });
-                        lay(turn, v, g);  // where this lane's dh was
-                        lay(other, v, u);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) sg[4 * v + e] = g[e], su[4 * v + e] = u[e];
-                    }
-                    wave_order();
-                    // the columns up to Fp too: their dh is 0, and so are they
-                    bf16_t* d = a.d_out + r0 * 2 * a.Fp + fs;
-                    turn_out<4>(turn, d, 2u * a.Fp, rows, a.Fp - fs);
-                    turn_out<4>(other, d + a.Fp, 2u * a.Fp, rows, a.Fp - fs);
-                    if (a.sums) {
-                        const float g = half_sum16(sg, lane), u = half_sum16(su, lane);
-#pragma unroll
-                        for (int m = 0; m < M; ++m)
-                            if (s % M == m) tg[m] += g, tu[m] += u;
-                    }
-                }
-                wave_order();
-            }
-            if (MODE == kAgain && a.sums) {
-#pragma unroll
-                for (int m = 0; m < M; ++m) {
-                    const int which = half_sum_of(lane);
-                    const int f = f0 + m * 32 + 8 * (which >> 2) + 4 * q + (which & 3);
-                    if ((lane & 1) == 0 && f < a.Fp) {
-                        float* row = a.sums + static_cast<int64_t>(o.pt * S::WP + wp) * 2 * a.Fp;
-                        row[f] = tg[m];
-                        row[a.Fp + f] = tu[m];
-                    }
-                }
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < S::TP; ++j) {
-                // 32 rows of dx, or (Fp is a multiple of 32) of dWg or dWu
-                const int64_t r0 = o.p0 + (wp * S::TP + j) * 32;
-                const int c0 = o.q0 + wq * S::TQ * 32;
-                bf16_t* out = a.out;
-                float* part = nullptr;
-                int64_t f = r0;
-                int rows;
-                if (MODE == kDx) {
-                    rows = static_cast<int>(min(static_cast<int64_t>(32), a.rows - r0));
-                } else {
-                    const bool up = r0 >= a.Fp;
-                    f -= up ? a.Fp : 0;
-                    rows = r0 < 2 * a.Fp ? static_cast<int>(min(static_cast<int64_t>(32), a.F - f)) : 0;
-                    out = up ? a.out2 : a.out;
-                    if (a.part) part = a.part + ((static_cast<int64_t>(o.piece) * 2 + (up ? 1 : 0)) * a.F + f) * a.C;
-                }
-                if (MODE == kDw && part) {
-#pragma unroll
-                    for (int i = 0; i < S::TQ; ++i) {
-                        __builtin_amdgcn_sched_barrier(0);
-                        const f32x16& w = acc[i][j];
-#pragma unroll
-                        for (int v = 0; v < 4; ++v)
-                            *reinterpret_cast<float4*>(turn + turn_at<8>(col, 2 * v + q)) = make_float4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
-                        wave_order();
-                        turn_out<8>(turn, part + c0 + i * 32, a.C, rows, a.C - c0 - i * 32);
-                        wave_order();
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < S::TQ; i += 2) {
-                        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                        for (int n = 0; n < 2; ++n) {
-                            const f32x16& w = acc[i + n][j];
-#pragma unroll
-                            for (int v = 0; v < 4; ++v)
-                                *reinterpret_cast<uint2*>(turn + turn_at<8>(col, n * 4 + v) + 8 * q) = make_uint2(pack_bf16x2(w[4 * v], w[4 * v + 1]), pack_bf16x2(w[4 * v + 2], w[4 * v + 3]));
-                        }
-                        wave_order();
-                        if (out) turn_out<8>(turn, out + f * a.C + c0 + i * 32, a.C, rows, a.C - c0 - i * 32);
-                        wave_order();
-                    }
-                }
-            }
-        }
-    }
-    if constexpr (FAST) wait_vm_lds<0>();  // no load may arrive in LDS that is no longer this workgroup's
-}
-
-// Few rows: the layer is a stream over its weights.  A workgroup takes 16
-// hidden channels (16 rows of Wg and of Wu), its waves share the contraction
-// in pieces of 64 values, NP groups of 16 rows of x ride along, and the waves'
-// sums are added in order.
-constexpr int kFewWaves = 8;
-template <int NP, bool FAST>
-__global__ __launch_bounds__(kFewWaves * 64) void gated_few_rows_kernel(Product a)
-{
-    __shared__ f32x4 sums[kFewWaves][2][NP][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int row = lane & 15, ku = (lane >> 4) * 8;
-    const int f0 = blockIdx.x * 16;
-    const int64_t fr = min(f0 + row, a.F - 1);
-    const bf16_t *wg = a.wg + fr * a.C, *wu = a.wu + fr * a.C;
-    const bf16_t* x[NP];
-#pragma unroll
-    for (int j = 0; j < NP; ++j) x[j] = a.x + min(static_cast<int64_t>(j * 16 + row), a.rows - 1) * a.C;
-    f32x4 g[NP], u[NP];
-#pragma unroll
-    for (int j = 0; j < NP; ++j) g[j] = u[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    auto load = [&](const bf16_t* p, int k) __attribute__((always_inline)) {
-        if (k >= a.C) return make_uint4(0, 0, 0, 0);
-        return FAST ? *reinterpret_cast<const uint4*>(p + k) : guarded16(p + k, a.C - k);
-    };
-    constexpr int U = NP == 1 ? 2 : 1;  // pieces in flight
-    for (int k0 = wave * 64; k0 < a.C; k0 += kFewWaves * 64 * U) {
-        uint4 vg[U][2], vu[U][2], vx[U][2][NP];
-#pragma unroll
-        for (int t = 0; t < U; ++t)
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const int k = k0 + t * kFewWaves * 64 + s * 32 + ku;
-                vg[t][s] = load(wg, k);
-                vu[t][s] = load(wu, k);
-#pragma unroll
-                for (int j = 0; j < NP; ++j) vx[t][s][j] = load(x[j], k);
-            }
-#pragma unroll
-        for (int t = 0; t < U; ++t)
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int j = 0; j < NP; ++j) {
-                    const bf16x8 b = __builtin_bit_cast(bf16x8, vx[t][s][j]);
-                    g[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, vg[t][s]), b, g[j], 0, 0, 0);
-                    u[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, vu[t][s]), b, u[j], 0, 0, 0);
-                }
-    }
-#pragma unroll
-    for (int j = 0; j < NP; ++j) {
-        sums[wave][0][j][lane] = g[j];
-        sums[wave][1][j][lane] = u[j];
-    }
-    __syncthreads();
-    // value (p, f): lane (f / 4) * 16 + p of a group, element f % 4
-    for (int idx = threadIdx.x; idx < NP * 256; idx += kFewWaves * 64) {
-        const int f = idx & 15, p = idx >> 4;
-        if (p >= a.rows || f0 + f >= a.F) continue;
-        const int at = (f >> 2) * 16 + (p & 15);
-        float gv = 0.f, uv = 0.f;
-#pragma unroll
-        for (int w = 0; w < kFewWaves; ++w) {
-            gv += reinterpret_cast<const float*>(&sums[w][0][p >> 4][at])[f & 3];
-            uv += reinterpret_cast<const float*>(&sums[w][1][p >> 4][at])[f & 3];
-        }
-        if (a.bg) gv += bf16_to_f(a.bg[f0 + f]), uv += bf16_to_f(a.bu[f0 + f]);
-        if (a.saved) {
-            a.saved[static_cast<int64_t>(p) * 2 * a.F + f0 + f] = gv;
-            a.saved[static_cast<int64_t>(p) * 2 * a.F + a.F + f0 + f] = uv;
-        }
-        a.h[static_cast<int64_t>(p) * a.F + f0 + f] = f_to_bf16(act_value(a.act, gv) * uv);
-    }
-}
-
-typedef Shape<2, 2, 4, 4, 32, 4> Wide;   // 256 x 256, one workgroup a CU
-typedef Shape<2, 2, 2, 4, 32, 3> Big;    // 128 x 256, two
-typedef Shape<2, 2, 2, 2, 64, 2> Small;  // 128 x 128
-
-bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-int64_t tiles(int64_t n, int t) { return (n + t - 1) / t; }
-
-template <typename S, int MODE, bool FAST>
-hipError_t run(Product& k, int64_t p, int64_t q, int pieces, hipStream_t s)
-{
-    const int64_t pt = tiles(p, S::BM), qt = tiles(q, S::BN), n = pt * qt * pieces;
-    if (n >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
-    k.p_tiles = static_cast<int>(pt);
-    k.q_tiles = static_cast<int>(qt);
-    k.tiles = static_cast<int>(n);
-    auto kernel = gated_product_kernel<S, MODE, FAST>;
-    static std::atomic<bool> ready{false};
-    if (S::kLds > 65536 && !ready.load(std::memory_order_acquire)) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, S::kLds);
-        if (e != hipSuccess) return e;
-        ready.store(true, std::memory_order_release);
-    }
-    // as many workgroups as the device holds at once, the same number on each XCD
-    const int64_t hold = std::max(8, device_cu_count() * S::kPerCu / 8 * 8);
-    return launch(kernel, dim3(static_cast<unsigned>(std::min<int64_t>((n + 7) / 8 * 8, hold))), dim3(S::kThreads), S::kLds, s, k);
-}
-
-// The largest tile that gives every CU its workgroups; the widest only for long
-// sums, where its loads and LDS reads (half as many for a product) count and
-// its epilogue, which nothing runs beside, does not.
-enum class Tile { kSmall, kBig, kWide };
-constexpr int64_t kLongSum = 1024;
-template <typename S>
-bool fills(int64_t p, int64_t q, int pieces) { return tiles(p, S::BM) * tiles(q, S::BN) * pieces >= S::kPerCu * device_cu_count(); }
-Tile pick(int64_t p, int64_t q, int pieces, int64_t K)
-{
-    if (K >= kLongSum && fills<Wide>(p, q, pieces)) return Tile::kWide;
-    return fills<Big>(p, q, pieces) ? Tile::kBig : Tile::kSmall;
-}
-// Partial rows of the column sums of `rows` rows: one for each wave's rows.
-int64_t sum_rows(int64_t rows, Tile t)
-{
-    return t == Tile::kWide ? tiles(rows, Wide::BM) * Wide::WP : t == Tile::kBig ? tiles(rows, Big::BM) * Big::WP : tiles(rows, Small::BM) * Small::WP;
-}
-
-template <int MODE>
-hipError_t run_tiles(Product& k, int64_t p, int64_t q, int pieces, Tile t, bool fast, hipStream_t s)
-{
-    if (t == Tile::kWide && fast) return run<Wide, MODE, true>(k, p, q, pieces, s);
-    if (t != Tile::kSmall) return fast ? run<Big, MODE, true>(k, p, q, pieces, s) : run<Big, MODE, false>(k, p, q, pieces, s);
-    return fast ? run<Small, MODE, true>(k, p, q, pieces, s) : run<Small, MODE, false>(k, p, q, pieces, s);
-}
-
-Product product(const GatedArgs& a)
-{
-    Product k{};
-    k.x = static_cast<const bf16_t*>(a.x);
-    k.wg = static_cast<const bf16_t*>(a.wg);
-    k.wu = static_cast<const bf16_t*>(a.wu);
-    k.bg = static_cast<const bf16_t*>(a.bg);
-    k.bu = static_cast<const bf16_t*>(a.bu);
-    k.dh = static_cast<const bf16_t*>(a.dh);
-    k.rows = a.rows;
-    k.C = a.C;
-    k.F = a.F;
-    k.act = a.act;
-    return k;
-}
-
-constexpr int64_t kFewRows = 64;
-
-}  // namespace
-
-GatedPlan gated_plan_bf16(int64_t rows, int C, int F)
-{
-    GatedPlan p{};
-    p.Fp = (F + 63) / 64 * 64;
-    // pieces of the weight gradients' sum: about one workgroup a place, no piece
-    // under 512 rows
-    const int64_t dp = 2 * static_cast<int64_t>(p.Fp), cus = device_cu_count();
-    const Tile t = pick(dp, C, 1, rows);
-    const int64_t n = t == Tile::kWide ? tiles(dp, Wide::BM) * tiles(C, Wide::BN) : t == Tile::kBig ? tiles(dp, Big::BM) * tiles(C, Big::BN) : tiles(dp, Small::BM) * tiles(C, Small::BN);
-    const int64_t hold = (t == Tile::kWide ? Wide::kPerCu : t == Tile::kBig ? Big::kPerCu : Small::kPerCu) * cus;
-    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(hold / n, rows / 512));
-    p.per = std::max<int64_t>(64, (tiles(rows, static_cast<int>(want)) + 63) / 64 * 64);
-    p.pieces = static_cast<int>(std::max<int64_t>(1, (rows + p.per - 1) / p.per));
-    int64_t chunk;
-    p.sum_rows = static_cast<int>(std::max<int64_t>(gated_kept_chunks(rows, p.Fp, &chunk), sum_rows(rows, Tile::kSmall)));
-    p.d_bytes = round256(static_cast<size_t>(rows) * 2 * p.Fp * 2);
-    p.sum_bytes = round256(static_cast<size_t>(p.sum_rows) * 2 * p.Fp * 4);
-    p.part_bytes = p.pieces > 1 ? round256(static_cast<size_t>(p.pieces) * 2 * F * C * 4) : 0;
-    return p;
-}
-
-hipError_t gated_fwd_bf16(const GatedArgs& a, hipStream_t s)
-{
-    Product k = product(a);
-    k.h = static_cast<bf16_t*>(a.h);
-    k.saved = a.saved;
-    const bool fast = a.C % 8 == 0 && aligned(a.x) && aligned(a.wg) && aligned(a.wu);
-    if (a.rows <= kFewRows) {
-        const dim3 grid((a.F + 15) / 16), block(kFewWaves * 64);
-        if (a.rows <= 16) return launch(fast ? gated_few_rows_kernel<1, true> : gated_few_rows_kernel<1, false>, grid, block, 0, s, k);
-        if (a.rows <= 32) return launch(fast ? gated_few_rows_kernel<2, true> : gated_few_rows_kernel<2, false>, grid, block, 0, s, k);
-        return launch(fast ? gated_few_rows_kernel<4, true> : gated_few_rows_kernel<4, false>, grid, block, 0, s, k);
-    }
-    return run_tiles<kFwd>(k, a.rows, 2 * static_cast<int64_t>(a.F), 1, pick(a.rows, 2 * static_cast<int64_t>(a.F), 1, a.C), fast, s);
-}
-
-hipError_t gated_bwd_bf16(const GatedArgs& a, hipStream_t s)
-{
-    const GatedPlan p = gated_plan_bf16(a.rows, a.C, a.F);
-    char* ws = static_cast<char*>(a.workspace);
-    bf16_t* d = reinterpret_cast<bf16_t*>(ws);
-    float* sums = a.dbg || a.dbu ? reinterpret_cast<float*>(ws + p.d_bytes) : nullptr;
-    float* part = reinterpret_cast<float*>(ws + p.d_bytes + p.sum_bytes);
-    const ArmedEvents armed = armed_events();
-    armed_events() = ArmedEvents{armed.start, nullptr};
-    hipError_t e = hipSuccess;
-    int summed = 0;
-    if (a.rows > 0) {
-        if (a.saved) {
-            int64_t chunk;
-            summed = gated_kept_chunks(a.rows, p.Fp, &chunk);
-            e = launch_gated_kept(a, d, sums, p.Fp, summed, chunk, 1, s);
-        } else {
-            Product k = product(a);
-            k.d_out = d;
-            k.sums = sums;
-            k.Fp = p.Fp;
-            const bool fast = a.C % 8 == 0 && aligned(a.x) && aligned(a.wg) && aligned(a.wu);
-            const Tile t = pick(a.rows, 2 * static_cast<int64_t>(a.F), 1, a.C);
-            summed = static_cast<int>(sum_rows(a.rows, fast || t != Tile::kWide ? t : Tile::kBig));
-            e = run_tiles<kAgain>(k, a.rows, 2 * static_cast<int64_t>(a.F), 1, t, fast, s);
-        }
-        armed_events() = ArmedEvents{nullptr, nullptr};
-        if (e != hipSuccess) return e;
-        if (a.dx) {
-            Product k = product(a);
-            k.d = d;
-            k.Fp = p.Fp;
-            k.out = static_cast<bf16_t*>(a.dx);
-            e = run_tiles<kDx>(k, a.rows, a.C, 1, pick(a.rows, a.C, 1, 2 * static_cast<int64_t>(p.Fp)), a.C % 8 == 0 && aligned(a.wg) && aligned(a.wu), s);
-            if (e != hipSuccess) return e;
-        }
-    }
-    if (sums) {
-        e = launch_gated_bias_sums(a, sums, summed, p.Fp, 1, s);
-        if (e != hipSuccess) return e;
-    }
-    if (a.dwg || a.dwu) {
-        Product k = product(a);
-        k.d = d;
-        k.Fp = p.Fp;
-        k.out = static_cast<bf16_t*>(a.dwg);
-        k.out2 = static_cast<bf16_t*>(a.dwu);
-        k.part = p.pieces > 1 ? part : nullptr;
-        k.per = p.per;
-        if (p.pieces == 1) armed_events() = ArmedEvents{nullptr, armed.stop};
-        e = run_tiles<kDw>(k, 2 * static_cast<int64_t>(p.Fp), a.C, p.pieces, pick(2 * static_cast<int64_t>(p.Fp), a.C, 1, a.rows),
-                           a.C % 8 == 0 && aligned(a.x), s);
-        armed_events() = ArmedEvents{nullptr, p.pieces > 1 ? armed.stop : nullptr};
-        if (e == hipSuccess && p.pieces > 1) e = launch_gated_weight_sums(a, part, p.pieces, 1, s);
-    }
-    armed_events() = ArmedEvents{nullptr, nullptr};
-    return e;
-}
+hipError_t gated_fwd_bf16(const GatedArgs& a, hipStream_t s) { return gated_fwd<bf16_t>(a, s); }
+hipError_t gated_bwd_bf16(const GatedArgs& a, hipStream_t s) { return gated_bwd<bf16_t>(a, s); }
+GatedPlan gated_plan_bf16(int64_t rows, int C, int F) { return gated_plan<bf16_t>(rows, C, F); }
 
 }  // namespace convmi

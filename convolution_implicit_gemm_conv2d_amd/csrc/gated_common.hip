@@ -123,6 +123,18 @@ hipError_t launch_gated_bias_sums(const GatedArgs& a, const float* sums, int row
     return launch_column_sums(k, s);
 }
 
+hipError_t launch_gated_dx_sums(const GatedArgs& a, const float* part, int pieces, int dtype, hipStream_t s)
+{
+    SumArgs k{};
+    k.part = part;
+    k.pitch = k.cols = a.rows * a.C;
+    k.pieces = pieces;
+    k.dtype = dtype;
+    k.nq = 1;
+    k.out[0] = a.dx;
+    return launch_column_sums(k, s);
+}
+
 hipError_t launch_gated_weight_sums(const GatedArgs& a, const float* part, int pieces, int dtype, hipStream_t s)
 {
     SumArgs k{};

@@ -213,3 +213,8 @@ def test_tensor_level_refusals():
         with pytest.raises(ValueError):
             call()
             print(i)
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_gated_workspace_without_rows(dtype):
+    assert cm.conv_gated_bwd_workspace_size(0, 16, 24, dtype) >= 0
