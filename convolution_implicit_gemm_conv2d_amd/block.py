@@ -142,6 +142,13 @@ def _here(device) -> int:
     return torch._C._cuda_getCurrentRawStream(device)
 
 
+def _like():
+    """Allocates a tensor like another (all inputs were found contiguous)."""
+    import torch
+
+    return torch.empty_like
+
+
 def _at(name, t, shape, dtype, device):
     """Address of an optional tensor, after its checks."""
     if t is None:
@@ -231,11 +238,11 @@ def gated_feed_forward_grad(dh, x, w_gate, w_up, b_gate=None, b_up=None, activat
         raise ValueError("dh must be a tensor")
     if _elsewhere(x, stream):
         return _entered(gated_feed_forward_grad, x, stream, dh, x, w_gate, w_up, b_gate, b_up, activation, saved, workspace)
-    device, new = x.get_device(), x.new_empty
-    dx, dwg, dwu = new(x.shape), new(w_gate.shape), new(w_gate.shape)
+    device, like = x.get_device(), _like()
+    dx, dwg, dwu = like(x), like(w_gate), like(w_up)
     dbg = dbu = pbg = pbu = None
     if b_gate is not None:
-        dbg, dbu = new(F), new(F)
+        dbg, dbu = like(b_gate), like(b_up)
         pbg, pbu = dbg.data_ptr(), dbu.data_ptr()
     ws, size = _workspace(workspace, x, _size("conv_gated_bwd_workspace_size", device, rows, C, F, dt))
     _check(_lib.load().conv_gated_bwd(dh_at, *at, kept, dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(), pbg, pbu,
@@ -299,11 +306,12 @@ def block_norm(x, branch=None, gate=None, scale=None, post_weight=None, post_bia
         return _entered(block_norm, x, stream, x, branch, gate, scale, post_weight, post_bias, pre_weight, pre_bias, post,
                         pre, gate_activation, eps)
     y = a = to_y = to_a = None
+    like = _like()
     if branch is not None:
-        y = x.new_empty(x.shape)
+        y = like(x)
         to_y = y.data_ptr()
     if pre != "none":
-        a = x.new_empty(x.shape)
+        a = like(x)
         to_a = a.data_ptr()
     _check(_lib.load().conv_block_norm_fwd(*at, to_y, to_a, rows, C, gate_rows, k_post, k_pre, act, eps, dt,
                                            _here(x.get_device())))
@@ -327,8 +335,8 @@ def block_norm_grad(dy, da, x, branch=None, gate=None, scale=None, post_weight=N
     if _elsewhere(x, stream):
         return _entered(block_norm_grad, x, stream, dy, da, x, branch, gate, scale, post_weight, post_bias, pre_weight,
                         pre_bias, post, pre, gate_activation, eps, workspace)
-    new = x.new_empty
-    d = [None if t is None else new(t.shape)
+    like = _like()
+    d = [None if t is None else like(t)
          for t in (x, branch, gate, scale, post_weight, post_bias, pre_weight, pre_bias)]
     ws, size = _workspace(workspace, x, _size("conv_block_norm_bwd_workspace_size", device, rows, C,
                                               gate_rows if gate is not None else 0))

@@ -38,18 +38,19 @@ __device__ __forceinline__ float tanh_f(float t)
     return fabsf(t) < 0.6f ? near : far;
 }
 
-// The normal distribution function Phi(t) and exp(-t^2 / 2).  The tail
+// The normal distribution function.  The tail
 // Phi(-|t|) is exp(-t^2 / 2) times a polynomial in s = 1 / (1 + P|t|) without
 // a constant term, fitted for its relative error (1.3e-7 up to 13.5, past which
 // the tail is below the smallest fp32 value), so small values of t Phi(t) are
 // good too; the larger side is one minus it.
 struct Normal {
-    float p, e;
+    float p, m, e;  // Phi(t), |t| Phi(-|t|), exp(-t^2 / 2)
 };
 __device__ __forceinline__ Normal normal_f(float t)
 {
     const float e = exp2_hw((-0.5f * kLog2e) * t * t);
-    const float s = rcp_hw(__builtin_fmaf(0.3f, fabsf(t), 1.0f));
+    const float m = __builtin_fminf(fabsf(t), 64.0f);  // the tail is 0 long before
+    const float s = rcp_hw(__builtin_fmaf(0.3f, m, 1.0f));
     float q = 0.035931705f;
     q = __builtin_fmaf(q, s, -0.158275877f);
     q = __builtin_fmaf(q, s, 0.208206396f);
@@ -59,7 +60,7 @@ __device__ __forceinline__ Normal normal_f(float t)
     q = __builtin_fmaf(q, s, 0.120798354f);
     q = __builtin_fmaf(q, s, 0.119626390f);
     const float tail = q * s * e;
-    return {t < 0.f ? tail : 1.0f - tail, e};
+    return {t < 0.f ? tail : 1.0f - tail, tail * m, e};
 }
 
 // x / 2 (1 + tanh(w)) is x times the logistic function of 2 w.
@@ -71,7 +72,7 @@ __device__ __forceinline__ float act_value(float t)
 {
     if constexpr (K == kActSigmoid) return sigmoid_f(t);
     else if constexpr (K == kActSilu) return t * sigmoid_f(t);
-    else if constexpr (K == kActGelu) return t * normal_f(t).p;
+    else if constexpr (K == kActGelu) return __builtin_fmaxf(t, 0.f) - normal_f(t).m;  // t Phi(t) on either side
     else if constexpr (K == kActGeluTanh) return t * gelu_tanh_p(t);
     else if constexpr (K == kActRelu) return t <= 0.f ? 0.f : t;  // NaN stays NaN
     else if constexpr (K == kActTanh) return tanh_f(t);
@@ -89,7 +90,7 @@ __device__ __forceinline__ ActPair act_pair(float t)
         return {t * p, p * (1.0f + t * (1.0f - p))};
     } else if constexpr (K == kActGelu) {
         const Normal n = normal_f(t);
-        return {t * n.p, n.p + t * 0.39894228040143268f * n.e};
+        return {__builtin_fmaxf(t, 0.f) - n.m, n.p + t * 0.39894228040143268f * n.e};
     } else if constexpr (K == kActGeluTanh) {
         const float p = gelu_tanh_p(t);
         return {t * p, p + t * p * (1.0f - p) * (2.0f * kTanhScale) * (1.0f + 3.0f * kTanhCube * t * t)};

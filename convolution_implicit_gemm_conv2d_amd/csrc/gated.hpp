@@ -9,8 +9,8 @@ namespace convmi {
 
 // The gradient's workspace: dg and du as rows [2 * Fp] of the type (Fp: F
 // rounded up so that a K tile never holds both), partial column sums of dg and
-// du, and fp32 partials of dx and then of the weight gradients, where their
-// sums are cut into pieces.
+// du, and fp32 partials of dx and of the weight gradients, where their sums are
+// cut into pieces.
 struct GatedPlan {
     int Fp;
     int sum_rows;          // partial rows of the column sums, [2][Fp] each
@@ -18,8 +18,8 @@ struct GatedPlan {
     int64_t per;           // rows of a piece
     int x_pieces;          // of dx's sum, and values of a piece
     int64_t x_per;
-    size_t d_bytes, sum_bytes, part_bytes;
-    size_t total() const { return d_bytes + sum_bytes + part_bytes; }
+    size_t d_bytes, sum_bytes, x_bytes, w_bytes;
+    size_t total() const { return d_bytes + sum_bytes + x_bytes + w_bytes; }
 };
 inline size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -35,11 +35,5 @@ GatedPlan gated_plan_f32(int64_t rows, int C, int F);
 hipError_t launch_gated_kept(const GatedArgs& a, void* d, float* sums, int Fp, int chunks, int64_t chunk, int dtype,
                              hipStream_t s);
 int gated_kept_chunks(int64_t rows, int Fp, int64_t* chunk);
-// The bias gradients from partial column sums.
-hipError_t launch_gated_bias_sums(const GatedArgs& a, const float* sums, int rows, int Fp, int dtype, hipStream_t s);
-// dx from `pieces` partials [rows][C].
-hipError_t launch_gated_dx_sums(const GatedArgs& a, const float* part, int pieces, int dtype, hipStream_t s);
-// The weight gradients from `pieces` partials [2F][C].
-hipError_t launch_gated_weight_sums(const GatedArgs& a, const float* part, int pieces, int dtype, hipStream_t s);
 
 }  // namespace convmi

@@ -108,49 +108,6 @@ hipError_t launch_gated_kept(const GatedArgs& a, void* d, float* sums, int Fp, i
                           static_cast<float*>(d), sums, a.rows, chunk, a.F, Fp, a.act);
 }
 
-hipError_t launch_gated_bias_sums(const GatedArgs& a, const float* sums, int rows, int Fp, int dtype, hipStream_t s)
-{
-    SumArgs k{};
-    k.part = sums;
-    k.pitch = 2 * static_cast<int64_t>(Fp);
-    k.q_pitch = Fp;
-    k.pieces = rows;
-    k.cols = a.F;
-    k.dtype = dtype;
-    k.out[0] = a.dbg;
-    k.out[1] = a.dbu;
-    k.nq = 2;
-    return launch_column_sums(k, s);
-}
-
-hipError_t launch_gated_dx_sums(const GatedArgs& a, const float* part, int pieces, int dtype, hipStream_t s)
-{
-    SumArgs k{};
-    k.part = part;
-    k.pitch = k.cols = a.rows * a.C;
-    k.pieces = pieces;
-    k.dtype = dtype;
-    k.nq = 1;
-    k.out[0] = a.dx;
-    return launch_column_sums(k, s);
-}
-
-hipError_t launch_gated_weight_sums(const GatedArgs& a, const float* part, int pieces, int dtype, hipStream_t s)
-{
-    SumArgs k{};
-    const int64_t n = static_cast<int64_t>(a.F) * a.C;
-    k.part = part;
-    k.pitch = 2 * n;
-    k.q_pitch = n;
-    k.pieces = pieces;
-    k.cols = n;
-    k.dtype = dtype;
-    k.out[0] = a.dwg;
-    k.out[1] = a.dwu;
-    k.nq = 2;
-    return launch_column_sums(k, s);
-}
-
 hipError_t launch_gated_fwd(const GatedArgs& a, int dtype, hipStream_t s)
 {
     return dtype ? gated_fwd_bf16(a, s) : gated_fwd_f32(a, s);

@@ -83,27 +83,27 @@ bool can_dx_band(const Geom& g, int dtype);
 hipError_t launch_dx_band(const void* dy, const void* w, const void* bias, void* dx,
                           const Geom& g, hipStream_t s);
 
-// Sums `pieces` rows of fp32 partials in row order (fixed-order tree), column
-// by column, and rounds once: column q * q_pitch + c goes to out[q][c] (a null
-// out[q] is skipped).  `pitch` is the row length of `part` in values.  With
-// no pieces the outputs become zero.
-constexpr int kSumOutputs = 6;
-struct SumArgs {
+// Sums of fp32 partials in row order, rounded once: column c of `pieces`
+// consecutive rows of `pitch` values goes to out[c], for each of `groups`
+// groups (of `pieces` rows and `cols` outputs each, one after another).  No
+// pieces: zeros.  A null out is skipped.
+constexpr int kSumJobs = 6;
+struct SumJob {
     const float* part;
-    int64_t pitch;
-    int pieces;
-    int64_t cols;
-    int dtype;
-    int64_t q_pitch;      // distance of two q blocks within a row of `part`, in values
-    void* out[kSumOutputs];
-    int nq;               // outputs
-    // Also, for each of gate_groups groups, gate_split consecutive rows of
-    // `part` from value gate_at on go to a row of gate_out.
-    void* gate_out;
-    int64_t gate_at;
-    int gate_split, gate_groups;
+    int64_t pitch, cols;
+    int pieces, groups;
+    void* out;
 };
-hipError_t launch_column_sums(const SumArgs& a, hipStream_t s);
+struct SumArgs {
+    SumJob job[kSumJobs];
+    uint32_t begin[kSumJobs];  // first workgroup (filled at the launch)
+    int jobs;
+};
+inline void add_sum(SumArgs& a, const float* part, int64_t pitch, int64_t cols, int pieces, void* out, int groups = 1)
+{
+    a.job[a.jobs++] = SumJob{part, pitch, cols, pieces, groups, out};
+}
+hipError_t launch_sums(SumArgs a, int dtype, hipStream_t s);
 
 // Norms before and after a block with gate and residual scale (see
 // conv_block_norm_fwd / conv_block_norm_bwd in include/convmi.h).

@@ -749,45 +749,6 @@ __global__ __launch_bounds__(kLongThreads) void norm_bwd_long_kernel(NormArgs k,
     }
 }
 
-// Adds partial rows: a workgroup takes 64 columns of one output, its W waves
-// every W-th piece, and their sums are added in order.  The rows of the grid
-// past the outputs are the gate rows of groups that were cut into `gate_split`
-// pieces each.
-template <typename T, int W>
-__global__ __launch_bounds__(W * 64) void column_sums_kernel(SumArgs a)
-{
-    __shared__ float sums[W][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 64 + lane;
-    const bool gate = static_cast<int>(blockIdx.y) >= a.nq;
-    const int64_t group = static_cast<int64_t>(blockIdx.y) - a.nq;
-    T* out = gate ? static_cast<T*>(a.gate_out) + group * a.cols : static_cast<T*>(a.out[blockIdx.y]);
-    if (!out) return;
-    const int pieces = gate ? a.gate_split : a.pieces;
-    float acc = 0.f;
-    if (c < a.cols) {
-        constexpr int kBatch = 16;
-        const float* p = gate ? a.part + group * a.gate_split * a.pitch + a.gate_at + c : a.part + blockIdx.y * a.q_pitch + c;
-        for (int s = wave; s < pieces; s += W * kBatch) {
-            float v[kBatch];
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                if (i == 0 || s + W * i < pieces) v[i] = p[static_cast<int64_t>(s + W * i) * a.pitch];
-                else v[i] = 0.f;
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) acc += v[i];
-        }
-    }
-    sums[wave][lane] = acc;
-    __syncthreads();
-    if (wave == 0 && c < a.cols) {
-        float t = 0.f;
-#pragma unroll
-        for (int w = 0; w < W; ++w) t += sums[w][lane];
-        store_f(out + c, t);
-    }
-}
-
 // Rows of up to this many channels stay in the registers of a workgroup.
 constexpr int kRegisterRow = 16384;
 
@@ -858,40 +819,24 @@ hipError_t bwd(const NormArgs& a, hipStream_t s)
     armed_events() = ArmedEvents{nullptr, nullptr};
     if (e != hipSuccess) return e;
     SumArgs sums{};
-    sums.part = a.part;
-    sums.pitch = static_cast<int64_t>(kSums) * a.C;
-    sums.q_pitch = a.C;
-    sums.pieces = pc.count;
-    sums.cols = a.C;
-    sums.dtype = sizeof(T) == 2;
-    void* out[kSumOutputs] = {a.dpre_w, a.dpost_w, a.ds, a.dpre_b, a.dpost_b, nullptr};
-    for (int q = 0; q < kSumOutputs; ++q) {
-        sums.out[q] = out[q];
-        if (out[q]) sums.nq = q + 1;
+    const int64_t pitch = static_cast<int64_t>(kSums) * a.C;
+    void* out[kSumGate] = {a.dpre_w, a.dpost_w, a.ds, a.dpre_b, a.dpost_b};
+    bool any = false;
+    for (int q = 0; q < kSumGate; ++q) {
+        add_sum(sums, a.part + static_cast<int64_t>(q) * a.C, pitch, a.C, pc.count, out[q]);
+        any |= out[q] != nullptr;
     }
     if (shared && a.dz && pc.split > 1) {
-        sums.gate_out = a.dz;
-        sums.gate_at = static_cast<int64_t>(kSumGate) * a.C;
-        sums.gate_split = pc.split;
-        sums.gate_groups = static_cast<int>(a.rows / pc.group);
+        add_sum(sums, a.part + static_cast<int64_t>(kSumGate) * a.C, pitch, a.C, pc.split, a.dz, static_cast<int>(a.rows / pc.group));
+        any = true;
     }
     armed_events() = ArmedEvents{nullptr, armed.stop};
-    if (sums.nq + sums.gate_groups > 0) e = launch_column_sums(sums, s);
+    if (any) e = launch_sums(sums, sizeof(T) == 2, s);
     armed_events() = ArmedEvents{nullptr, nullptr};
     return e;
 }
 
 }  // namespace
-
-hipError_t launch_column_sums(const SumArgs& a, hipStream_t s)
-{
-    const dim3 grid(static_cast<unsigned>((a.cols + 63) / 64), a.nq + a.gate_groups);
-    // sixteen waves once each has several pieces (512 pieces of 3 x 4096
-    // columns: 18 us with four waves, 13 us with sixteen)
-    if (a.pieces >= 64)
-        return a.dtype ? launch(column_sums_kernel<bf16_t, 16>, grid, dim3(1024), 0, s, a) : launch(column_sums_kernel<float, 16>, grid, dim3(1024), 0, s, a);
-    return a.dtype ? launch(column_sums_kernel<bf16_t, 4>, grid, dim3(256), 0, s, a) : launch(column_sums_kernel<float, 4>, grid, dim3(256), 0, s, a);
-}
 
 hipError_t launch_norm_fwd(const NormArgs& a, int dtype, hipStream_t s)
 {
