@@ -15,6 +15,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libconvmi.so")
+# The native part of the Python binding (host code against PyTorch's headers).
+BINDING = os.path.join(PKG, "_native.so")
 # Host code under AddressSanitizer and UndefinedBehaviorSanitizer (the device
 # code is built as usual); loaded instead of LIB when CONVMI_SANITIZED=1.
 OBJ_SAN = os.path.join(PKG, "_build_san")
@@ -46,14 +48,39 @@ def _compile(src: str, sanitize: bool = False) -> str:
     return obj
 
 
+def build_binding() -> str:
+    """Compile ``csrc/binding.cpp`` into ``_native.so``; returns its path."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", os.path.join(ROOT, "include"), "-I", sysconfig.get_paths()["include"]]
+    for path in cpp_extension.include_paths():
+        cmd += ["-isystem", path]
+    cmd += [os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(jobs: int = 8, sanitize: bool = False) -> str:
-    """Compile every ``csrc/*.hip`` and link ``libconvmi.so`` (with
+    """Compile every ``csrc/*.hip`` and link ``libconvmi.so``, and compile the
+    native binding (with
     ``sanitize``: ``libconvmi_san.so``, host code under ASan and UBSan);
     returns its path."""
     os.makedirs(OBJ_SAN if sanitize else OBJ, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.hip")))
     with concurrent.futures.ThreadPoolExecutor(max_workers=jobs) as ex:
+        binding = None if sanitize else ex.submit(build_binding)
         objs = list(ex.map(lambda f: _compile(f, sanitize), srcs))
+        if binding:
+            binding.result()
     lib = LIB_SAN if sanitize else LIB
     tmp = lib + ".tmp"
     link = [HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", "-o", tmp, *objs]

@@ -16,28 +16,37 @@
 // fp32 gradient neither overflows nor vanishes, and the order of the sums
 // (lane, wave, workgroup, list) is fixed, so the norm is the same on every
 // run.  The second pass has no launch between it and the first: every
-// workgroup sums the same partials, in the same order.
+// workgroup sums the same partials, in the same order; and it goes through the
+// list backwards, so that what the first pass read last comes out of the
+// memory-side cache.  290 tensors, 300M elements, 831 MB: 547 us forwards, 528
+// backwards, 495 backwards with streaming stores (5.0 TB/s over the three
+// passes).
 #include "kernels.hpp"
 
 #include <algorithm>
+#include <vector>
 
 namespace convmi {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr size_t kStreamBytes = size_t(128) << 20;
 
+// Up to N tensors.
+template <int N>
 struct Table {
-    const void* src[kClipTensors];
-    void* dst[kClipTensors];
-    uint64_t count[kClipTensors];        // elements * 2 + (1: bf16, 0: fp32)
-    uint32_t begin[kClipTensors + 1];    // first chunk of each tensor
+    const void* src[N];
+    void* dst[N];
+    uint64_t count[N];        // elements * 2 + (1: bf16, 0: fp32)
+    uint32_t begin[N + 1];    // first chunk of each tensor
     int n;
-    uint32_t chunk;                      // elements in a chunk
+    uint32_t chunk;           // elements in a chunk
 };
-static_assert(sizeof(Table) + 64 <= 4096, "the table is a kernel argument");
+static_assert(sizeof(Table<kClipTensors>) + 64 <= 4096, "the table is a kernel argument");
 
 // The tensor that holds chunk c.
-__device__ __forceinline__ int find(const Table& t, uint32_t c)
+template <int N>
+__device__ __forceinline__ int find(const Table<N>& t, uint32_t c)
 {
     int lo = 0, hi = t.n;  // begin[lo] <= c < begin[hi]
     while (hi - lo > 1) {
@@ -95,7 +104,8 @@ __device__ __forceinline__ double chunk_squares(const char* p, uint32_t n)
     return acc[0] + acc[1];
 }
 
-__global__ __launch_bounds__(kThreads) void clip_norm_kernel(Table t, double* __restrict__ part)
+template <int N>
+__global__ __launch_bounds__(kThreads) void clip_norm_kernel(Table<N> t, double* __restrict__ part)
 {
     __shared__ double waves[kThreads / 64];
     double acc = 0.0;
@@ -136,7 +146,16 @@ __device__ __forceinline__ uint4 scaled(uint4 v, float c, bool bf16)
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <bool BF16>
+template <bool STREAM>
+__device__ __forceinline__ void put16(void* p, uint4 v)
+{
+    uint32x4_any t;
+    t.x = v.x; t.y = v.y; t.z = v.z; t.w = v.w;
+    if constexpr (STREAM) __builtin_nontemporal_store(t, static_cast<uint32x4_any*>(p));
+    else *static_cast<uint32x4_any*>(p) = t;
+}
+
+template <bool BF16, bool STREAM>
 __device__ __forceinline__ void chunk_scale(const char* p, char* q, uint32_t n, float c)
 {
     constexpr uint32_t V = BF16 ? 8 : 4, E = 16 / V;
@@ -147,7 +166,7 @@ __device__ __forceinline__ void chunk_scale(const char* p, char* q, uint32_t n, 
 #pragma unroll
         for (int u = 0; u < U; ++u) v[u] = load16_any(p + static_cast<size_t>(i + u * V * kThreads) * E);
 #pragma unroll
-        for (int u = 0; u < U; ++u) store16_any(q + static_cast<size_t>(i + u * V * kThreads) * E, scaled(v[u], c, BF16));
+        for (int u = 0; u < U; ++u) put16<STREAM>(q + static_cast<size_t>(i + u * V * kThreads) * E, scaled(v[u], c, BF16));
     }
     for (; i + V <= n; i += V * kThreads)
         store16_any(q + static_cast<size_t>(i) * E, scaled(load16_any(p + static_cast<size_t>(i) * E), c, BF16));
@@ -158,7 +177,8 @@ __device__ __forceinline__ void chunk_scale(const char* p, char* q, uint32_t n, 
         }
 }
 
-__global__ __launch_bounds__(kThreads) void clip_scale_kernel(Table t, const double* __restrict__ part, int parts,
+template <int N, bool STREAM>
+__global__ __launch_bounds__(kThreads) void clip_scale_kernel(Table<N> t, const double* __restrict__ part, int parts,
                                                               float max_norm, float eps, float* norm)
 {
     __shared__ double waves[kThreads / 64];
@@ -166,15 +186,16 @@ __global__ __launch_bounds__(kThreads) void clip_scale_kernel(Table t, const dou
     if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = v;
     float c = max_norm / (v + eps);
     c = c > 1.0f ? 1.0f : c;  // NaN stays
-    for (uint32_t b = blockIdx.x; b < t.begin[t.n]; b += gridDim.x) {
+    for (uint32_t i = blockIdx.x; i < t.begin[t.n]; i += gridDim.x) {
+        const uint32_t b = t.begin[t.n] - 1 - i;  // from the end
         const int k = find(t, b);
         const char* p = static_cast<const char*>(t.src[k]);
         char* q = static_cast<char*>(t.dst[k]);
         if (c == 1.0f && p == q) continue;  // in place and unclipped: the values stand
         const uint64_t count = t.count[k] >> 1, at = static_cast<uint64_t>(b - t.begin[k]) * t.chunk;
         const uint32_t n = static_cast<uint32_t>(count - at < t.chunk ? count - at : t.chunk);
-        if (t.count[k] & 1) chunk_scale<true>(p + at * 2, q + at * 2, n, c);
-        else chunk_scale<false>(p + at * 4, q + at * 4, n, c);
+        if (t.count[k] & 1) chunk_scale<true, STREAM>(p + at * 2, q + at * 2, n, c);
+        else chunk_scale<false, STREAM>(p + at * 4, q + at * 4, n, c);
     }
 }
 
@@ -193,59 +214,80 @@ size_t clip_workspace(int n)
     return static_cast<size_t>(launches) * max_blocks(n) * sizeof(double);
 }
 
-hipError_t launch_clip(const void* const* src, void* const* dst, const size_t* counts, const int* dtypes, int n,
-                       float max_norm, float eps, float* norm, void* workspace, hipStream_t s)
+namespace {
+
+// One list, N tensors a launch.
+template <int N>
+hipError_t clip(const void* const* src, void* const* dst, const size_t* counts, const int* dtypes, int n, float max_norm,
+                float eps, float* norm, double* part, hipStream_t s)
 {
-    double* part = static_cast<double*>(workspace);
     const int limit = max_blocks(n);
-    size_t total = 0;
-    for (int i = 0; i < n; ++i) total += counts[i];
+    size_t total = 0, bytes = 0;
+    for (int i = 0; i < n; ++i) {
+        total += counts[i];
+        bytes += counts[i] * (dtypes[i] == 1 ? 2 : 4);
+    }
+    // A list larger than half of the memory-side cache is written past it, so
+    // that the writes leave what the backward walk is about to read.
+    auto scale = bytes > kStreamBytes ? clip_scale_kernel<N, true> : clip_scale_kernel<N, false>;
     // Elements in a chunk: about one chunk a workgroup for small lists (from
     // 2048 elements, two vectors a lane in bf16), at most 32768.
     uint32_t chunk = 2048;
     while (chunk < 32768 && total / chunk > static_cast<size_t>(limit)) chunk *= 2;
+    Table<N> t;
+    auto fill = [&](int i) {  // the tensors from the i-th on; returns the next one
+        t.n = 0;
+        t.chunk = chunk;
+        uint64_t chunks = 0;
+        for (; i < n && t.n < N; ++i) {
+            if (counts[i] == 0) continue;
+            t.src[t.n] = src[i];
+            t.dst[t.n] = dst ? dst[i] : nullptr;
+            t.count[t.n] = static_cast<uint64_t>(counts[i]) * 2 + (dtypes[i] == 1);
+            t.begin[t.n++] = static_cast<uint32_t>(chunks);
+            chunks += (counts[i] + chunk - 1) / chunk;
+        }
+        t.begin[t.n] = static_cast<uint32_t>(chunks);
+        return i;
+    };
+    auto grid = [&] { return dim3(static_cast<unsigned>(std::max<uint32_t>(1, std::min<uint32_t>(t.begin[t.n], limit)))); };
     const ArmedEvents armed = armed_events();
     armed_events() = ArmedEvents{armed.start, nullptr};
-    int parts = 0;
-    for (int pass = 0; pass < (dst ? 2 : 1); ++pass) {
-        int at = 0;
-        for (int i = 0; i < n || i == 0;) {
-            Table t;
-            t.n = 0;
-            t.chunk = chunk;
-            uint64_t chunks = 0;
-            for (; i < n && t.n < kClipTensors; ++i) {
-                if (counts[i] == 0) continue;
-                const uint64_t more = (counts[i] + chunk - 1) / chunk;
-                t.src[t.n] = src[i];
-                t.dst[t.n] = dst ? dst[i] : nullptr;
-                t.count[t.n] = static_cast<uint64_t>(counts[i]) * 2 + (dtypes[i] == 1);
-                t.begin[t.n++] = static_cast<uint32_t>(chunks);
-                chunks += more;
-            }
-            t.begin[t.n] = static_cast<uint32_t>(chunks);
-            const int grid = static_cast<int>(std::max<uint64_t>(1, std::min<uint64_t>(chunks, limit)));
-            const bool last = i >= n;
-            hipError_t e;
-            if (pass == 0) {
-                e = launch(clip_norm_kernel, dim3(grid), dim3(kThreads), 0, s, t, part + at);
-                at += grid;
-            } else {
-                if (last) armed_events() = ArmedEvents{nullptr, armed.stop};
-                e = launch(clip_scale_kernel, dim3(grid), dim3(kThreads), 0, s, t, part, parts, max_norm, eps,
-                           last ? norm : nullptr);
-            }
-            if (e != hipSuccess) {
-                armed_events() = ArmedEvents{nullptr, nullptr};
-                return e;
-            }
-            if (i >= n) break;
-        }
-        if (pass == 0) parts = at;
+    hipError_t e = hipSuccess;
+    std::vector<int> first;  // tensor of each launch
+    int parts = 0, i = 0;
+    do {
+        first.push_back(i);
+        i = fill(i);
+        const dim3 g = grid();
+        e = launch(clip_norm_kernel<N>, g, dim3(kThreads), 0, s, t, part + parts);
+        parts += static_cast<int>(g.x);
+    } while (e == hipSuccess && i < n);
+    armed_events() = ArmedEvents{nullptr, nullptr};
+    if (e != hipSuccess) return e;
+    if (!dst) {
+        armed_events() = ArmedEvents{nullptr, armed.stop};
+        e = launch(clip_finish_kernel, dim3(1), dim3(kThreads), 0, s, part, parts, norm);
+        armed_events() = ArmedEvents{nullptr, nullptr};
+        return e;
     }
-    if (dst) return hipSuccess;
-    armed_events() = ArmedEvents{nullptr, armed.stop};
-    return launch(clip_finish_kernel, dim3(1), dim3(kThreads), 0, s, part, parts, norm);
+    for (size_t l = first.size(); e == hipSuccess && l-- > 0;) {
+        if (first.size() > 1) fill(first[l]);  // a single launch's table is still there
+        if (l == 0) armed_events() = ArmedEvents{nullptr, armed.stop};
+        e = launch(scale, grid(), dim3(kThreads), 0, s, t, part, parts, max_norm, eps, l == 0 ? norm : nullptr);
+    }
+    armed_events() = ArmedEvents{nullptr, nullptr};
+    return e;
+}
+
+}  // namespace
+
+hipError_t launch_clip(const void* const* src, void* const* dst, const size_t* counts, const int* dtypes, int n,
+                       float max_norm, float eps, float* norm, void* workspace, hipStream_t s)
+{
+    double* part = static_cast<double*>(workspace);
+    return n <= 16 ? clip<16>(src, dst, counts, dtypes, n, max_norm, eps, norm, part, s)
+                   : clip<kClipTensors>(src, dst, counts, dtypes, n, max_norm, eps, norm, part, s);
 }
 
 }  // namespace convmi
