@@ -37,6 +37,8 @@ SIGNATURES = {
     "conv_bwd_dw_noalloc": (_I, [_P, _P, _P] + _GEOM + [_P]),
     # x w_gate w_up b_gate b_up h saved, rows C F act dtype
     "conv_gated_fwd": (_I, [_P] * 7 + [_L, _I, _I, _I, _I, _P]),
+    "conv_gated_fwd_ex": (_I, [_P] * 8 + [ctypes.c_size_t, _L, _I, _I, _I, _I, _P]),
+    "conv_gated_fwd_workspace_size": (_I, [_L, _I, _I, _I, ctypes.POINTER(ctypes.c_size_t)]),
     "conv_gated_bwd": (_I, [_P] * 13 + [ctypes.c_size_t, _L, _I, _I, _I, _I, _P]),
     "conv_gated_bwd_workspace_size": (_I, [_L, _I, _I, _I, ctypes.POINTER(ctypes.c_size_t)]),
     # ..., rows C gate_rows post pre act eps dtype

@@ -26,7 +26,7 @@ ACTIVATIONS = {"none": 0, "sigmoid": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "r
 NORMS = {"none": 0, "rms": 1, "layer": 2}
 
 __all__ = [
-    "conv_gated_fwd", "conv_gated_bwd", "conv_gated_bwd_workspace_size", "conv_block_norm_fwd", "conv_block_norm_bwd",
+    "conv_gated_fwd", "conv_gated_fwd_ex", "conv_gated_fwd_workspace_size", "conv_gated_bwd", "conv_gated_bwd_workspace_size", "conv_block_norm_fwd", "conv_block_norm_bwd",
     "conv_block_norm_bwd_workspace_size", "conv_grad_norm", "conv_grad_clip", "conv_grad_workspace_size",
     "gated_feed_forward", "gated_feed_forward_grad", "block_norm", "block_norm_grad", "gradient_norm",
     "clip_gradients", "ACTIVATIONS", "NORMS",
@@ -47,6 +47,10 @@ def _device() -> int:
     return torch.cuda.current_device() if torch.cuda.is_available() else -1
 
 
+def conv_gated_fwd_workspace_size(rows, C, F, dtype) -> int:
+    return _size("conv_gated_fwd_workspace_size", _device(), rows, C, F, dtype)
+
+
 def conv_gated_bwd_workspace_size(rows, C, F, dtype) -> int:
     return _size("conv_gated_bwd_workspace_size", _device(), rows, C, F, dtype)
 
@@ -63,6 +67,13 @@ def conv_gated_fwd(x, w_gate, w_up, b_gate, b_up, h, saved, rows, C, F, act, dty
     p, st = _ptr, _stream
     _check(_lib.load().conv_gated_fwd(p(x), p(w_gate), p(w_up), p(b_gate), p(b_up), p(h), p(saved), rows, C, F, act, dtype,
                                      st(stream)))
+
+
+def conv_gated_fwd_ex(x, w_gate, w_up, b_gate, b_up, h, saved, workspace, workspace_bytes, rows, C, F, act, dtype,
+                      stream=None) -> None:
+    p, st = _ptr, _stream
+    _check(_lib.load().conv_gated_fwd_ex(p(x), p(w_gate), p(w_up), p(b_gate), p(b_up), p(h), p(saved), p(workspace),
+                                         workspace_bytes, rows, C, F, act, dtype, st(stream)))
 
 
 def conv_gated_bwd(dh, x, w_gate, w_up, b_gate, b_up, saved, dx, dw_gate, dw_up, db_gate, db_up, workspace,
@@ -113,7 +124,8 @@ def conv_grad_clip(grads, outs, counts, dtypes, n, max_norm, eps, norm, workspac
 
 # ----------------------------------------------------------- tensor level --
 
-_ABI = ("conv_gated_fwd", "conv_gated_bwd", "conv_gated_bwd_workspace_size", "conv_block_norm_fwd", "conv_block_norm_bwd",
+_ABI = ("conv_gated_fwd_ex", "conv_gated_fwd_workspace_size", "conv_gated_bwd",
+        "conv_gated_bwd_workspace_size", "conv_block_norm_fwd", "conv_block_norm_bwd",
         "conv_block_norm_bwd_workspace_size", "conv_grad_norm", "conv_grad_clip", "conv_grad_workspace_size")
 
 

@@ -38,7 +38,8 @@ std::string text(at::IntArrayRef s)
 
 // The C ABI, bound by address (the loaded library is block.py's choice).
 struct Api {
-    decltype(&conv_gated_fwd) gated_fwd;
+    decltype(&conv_gated_fwd_ex) gated_fwd;
+    decltype(&conv_gated_fwd_workspace_size) gated_fwd_workspace;
     decltype(&conv_gated_bwd) gated_bwd;
     decltype(&conv_gated_bwd_workspace_size) gated_bwd_workspace;
     decltype(&conv_block_norm_fwd) norm_fwd;
@@ -205,11 +206,15 @@ PyObject* gated(PyObject*, PyObject* const* a, Py_ssize_t n)
         const at::Tensor* out = tensor(a[6], "out");
         g.c.fits(out, "out", g.hidden);
         g.c.on_gpu();
-        at::Tensor h = out ? *out : at::empty(g.hidden, g.x.options());
+        size_t need = 0;
+        if (int rc = api.gated_fwd_workspace(g.rows, g.C, g.F, g.c.dtype, &need)) return status(rc);
+        at::Tensor h = out ? *out : at::empty(g.hidden, g.x.options()), ws;
+        if (need) ws = bytes_like(g.x, need);
         void* stream = address(a[8]);
         const int rc = call([&] {
             return api.gated_fwd(g.x.data_ptr(), g.wg.data_ptr(), g.wu.data_ptr(), at_of(g.bg), at_of(g.bu), h.data_ptr(),
-                                 static_cast<float*>(at_of(g.saved)), g.rows, g.C, g.F, g.act, g.c.dtype, stream);
+                                 static_cast<float*>(at_of(g.saved)), need ? ws.data_ptr() : nullptr, need, g.rows, g.C, g.F, g.act,
+                                 g.c.dtype, stream);
         });
         return rc ? status(rc) : THPVariable_Wrap(h);
     });
@@ -400,9 +405,9 @@ PyObject* clip(PyObject*, PyObject* const* a, Py_ssize_t n)
 // The addresses of the C functions, in the order of Api.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    static_assert(sizeof(Api) == 9 * sizeof(void*), "");
-    return guarded(n, 9, [&]() -> PyObject* {
-        for (int i = 0; i < 9; ++i) reinterpret_cast<void**>(&api)[i] = address(a[i]);
+    static_assert(sizeof(Api) == 10 * sizeof(void*), "");
+    return guarded(n, 10, [&]() -> PyObject* {
+        for (int i = 0; i < 10; ++i) reinterpret_cast<void**>(&api)[i] = address(a[i]);
         Py_RETURN_NONE;
     });
 }

@@ -171,10 +171,9 @@ int conv_block_norm_bwd(const void* dy, const void* da, const void* x, const voi
     return launched(convmi::launch_norm_bwd(k, dtype, static_cast<hipStream_t>(stream)), op);
 }
 
-int conv_gated_fwd(const void* x, const void* w_gate, const void* w_up, const void* b_gate, const void* b_up, void* h,
-                   float* saved, long long rows, int C, int F, int act, int dtype, void* stream)
+static int gated_forward(const char* op, const void* x, const void* w_gate, const void* w_up, const void* b_gate, const void* b_up,
+                         void* h, float* saved, void* workspace, long long rows, int C, int F, int act, int dtype, void* stream)
 {
-    static const char* op = "conv_gated_fwd";
     if (int rc = check_gated(op, rows, C, F, act, dtype)) return rc;
     if (rows == 0) return CONV_OK;
     if (!x || !w_gate || !w_up || !h)
@@ -185,8 +184,34 @@ int conv_gated_fwd(const void* x, const void* w_gate, const void* w_up, const vo
     if (int rc = check_aligned(op, {saved}, 4)) return rc;
     convmi::GatedArgs k{};
     k.x = x; k.wg = w_gate; k.wu = w_up; k.bg = b_gate; k.bu = b_up; k.h = h; k.saved = saved;
+    k.workspace = workspace;
     k.rows = rows; k.C = C; k.F = F; k.act = act;
     return launched(convmi::launch_gated_fwd(k, dtype, static_cast<hipStream_t>(stream)), op);
+}
+
+int conv_gated_fwd(const void* x, const void* w_gate, const void* w_up, const void* b_gate, const void* b_up, void* h,
+                   float* saved, long long rows, int C, int F, int act, int dtype, void* stream)
+{
+    return gated_forward("conv_gated_fwd", x, w_gate, w_up, b_gate, b_up, h, saved, nullptr, rows, C, F, act, dtype, stream);
+}
+
+int conv_gated_fwd_workspace_size(long long rows, int C, int F, int dtype, size_t* bytes)
+{
+    static const char* op = "conv_gated_fwd_workspace_size";
+    if (!bytes) return fail(CONV_ERR_INVALID_ARG, "%s: bytes is NULL", op);
+    if (int rc = check_gated(op, rows, C, F, CONV_ACT_NONE, dtype)) return rc;
+    *bytes = convmi::gated_fwd_workspace(rows, C, F, dtype);
+    return CONV_OK;
+}
+
+int conv_gated_fwd_ex(const void* x, const void* w_gate, const void* w_up, const void* b_gate, const void* b_up, void* h,
+                      float* saved, void* workspace, size_t workspace_bytes, long long rows, int C, int F, int act, int dtype,
+                      void* stream)
+{
+    static const char* op = "conv_gated_fwd_ex";
+    if (int rc = check_gated(op, rows, C, F, act, dtype)) return rc;
+    if (int rc = check_workspace(op, workspace, workspace_bytes, convmi::gated_fwd_workspace(rows, C, F, dtype))) return rc;
+    return gated_forward(op, x, w_gate, w_up, b_gate, b_up, h, saved, workspace, rows, C, F, act, dtype, stream);
 }
 
 int conv_gated_bwd_workspace_size(long long rows, int C, int F, int dtype, size_t* bytes)

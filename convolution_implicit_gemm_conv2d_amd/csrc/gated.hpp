@@ -10,7 +10,7 @@ namespace convmi {
 // The gradient's workspace: dg and du as rows [2 * Fp] of the type (Fp: F
 // rounded up so that a K tile never holds both), partial column sums of dg and
 // du, and fp32 partials of dx and of the weight gradients, where their sums are
-// cut into pieces.
+// cut into pieces, and copies of x and the weights with padded rows.
 struct GatedPlan {
     int Fp;
     int sum_rows;          // partial rows of the column sums, [2][Fp] each
@@ -18,17 +18,19 @@ struct GatedPlan {
     int64_t per;           // rows of a piece
     int x_pieces;          // of dx's sum, and values of a piece
     int64_t x_per;
-    size_t d_bytes, sum_bytes, x_bytes, w_bytes;
-    size_t total() const { return d_bytes + sum_bytes + x_bytes + w_bytes; }
+    size_t d_bytes, sum_bytes, x_bytes, w_bytes, pad_bytes;
+    size_t total() const { return d_bytes + sum_bytes + x_bytes + w_bytes + pad_bytes; }
 };
 inline size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 hipError_t gated_fwd_bf16(const GatedArgs& a, hipStream_t s);
 hipError_t gated_bwd_bf16(const GatedArgs& a, hipStream_t s);
 GatedPlan gated_plan_bf16(int64_t rows, int C, int F);
+size_t gated_fwd_workspace_bf16(int64_t rows, int C, int F);
 hipError_t gated_fwd_f32(const GatedArgs& a, hipStream_t s);
 hipError_t gated_bwd_f32(const GatedArgs& a, hipStream_t s);
 GatedPlan gated_plan_f32(int64_t rows, int C, int F);
+size_t gated_fwd_workspace_f32(int64_t rows, int C, int F);
 
 // dg and du from kept projections: d[row] = [dg | du], with partial column
 // sums of `chunk` rows each when sums is not null.

@@ -118,6 +118,11 @@ hipError_t launch_gated_bwd(const GatedArgs& a, int dtype, hipStream_t s)
     return dtype ? gated_bwd_bf16(a, s) : gated_bwd_f32(a, s);
 }
 
+size_t gated_fwd_workspace(int64_t rows, int C, int F, int dtype)
+{
+    return dtype ? gated_fwd_workspace_bf16(rows, C, F) : gated_fwd_workspace_f32(rows, C, F);
+}
+
 size_t gated_bwd_workspace(int64_t rows, int C, int F, int dtype)
 {
     return (dtype ? gated_plan_bf16(rows, C, F) : gated_plan_f32(rows, C, F)).total();

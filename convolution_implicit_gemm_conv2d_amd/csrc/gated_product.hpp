@@ -59,8 +59,8 @@ struct Shape {
     static constexpr int kWaveLds = kStage / (WP * WQ);  // a wave's part of a stage
     // of a SIMD: the accumulators take 16 TP TQ of its 512 registers
     static constexpr int kWaves = TP * TQ > 8 ? 1 : TP * TQ > 2 ? 2 : 3;
-    static constexpr int kPerCu = 4 * kWaves / (WP * WQ);  // workgroups
-    static_assert(kPerCu * kLds <= 163840 && BN <= kThreads, "");
+    static constexpr int kPerCu = 163840 / kLds < 4 * kWaves / (WP * WQ) ? 163840 / kLds : 4 * kWaves / (WP * WQ);  // workgroups
+    static_assert(kPerCu > 0 && BN <= kThreads, "");
     static_assert(kWaveLds >= 4096, "a wave's output passes through its part of a stage");
     static_assert(kPLoads > 0 && kQLoads > 0 && TQ % 2 == 0 && NS >= 2, "");
     static_assert((kRowBytes == 64 || kRowBytes == 128) && 64 % BK == 0, "");
@@ -75,6 +75,7 @@ struct Product {
     float *saved, *sums, *part;
     int64_t rows, per;    // per: contraction values of a piece (dx, dW)
     int C, F, Fp, act;
+    int x_ld, w_ld;       // row pitches of x and of the weights: C, or that of their padded copies
     int p_tiles, q_tiles, tiles;  // tiles: of all pieces
 };
 
@@ -308,7 +309,7 @@ __global__ __launch_bounds__(S::kThreads, S::kWaves) void gated_product_kernel(P
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wp = wave / S::WQ, wq = wave % S::WQ;
     const int col = lane & 31, q = lane >> 5;
-    const int p_ld = kGated ? a.C : 2 * a.Fp, q_ld = a.C;
+    const int p_ld = kGated ? a.x_ld : 2 * a.Fp, q_ld = MODE == kDw ? a.x_ld : a.w_ld;
 
     // Workgroup b runs on XCD b mod 8; an XCD takes a contiguous run of tiles,
     // its workgroups take them in turn.
@@ -763,7 +764,7 @@ __global__ __launch_bounds__(S::kThreads, S::kWaves) void gated_product_kernel(P
 // Few rows: the layer is a stream over its weights.  A workgroup takes 16
 // hidden channels (16 rows of Wg and of Wu), its waves share the contraction
 // in pieces, NP groups of 16 rows of x ride along, and the waves' sums are
-// added in order.  A 16-byte load a lane is one 16x16x32 instruction in bf16,
+// added in order.  MODE kFwd: h; kAgain: dg and du, and their column sums.  A 16-byte load a lane is one 16x16x32 instruction in bf16,
 // four 16x16x4 in fp32.
 constexpr int kFewWaves = 8;
 template <typename T>
@@ -778,7 +779,7 @@ __device__ __forceinline__ f32x4 multiply16(uint4 w, uint4 x, f32x4 acc)
         return acc;
     }
 }
-template <typename T, int NP, bool FAST>
+template <typename T, int MODE, int NP, bool FAST>
 __global__ __launch_bounds__(kFewWaves * 64) void gated_few_rows_kernel(Product<T> a)
 {
     constexpr int kUnit = 16 / sizeof(T), kLoad = 4 * kUnit, kPiece = 2 * kLoad;  // contraction values of a load, of a piece
@@ -786,11 +787,11 @@ __global__ __launch_bounds__(kFewWaves * 64) void gated_few_rows_kernel(Product<
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int row = lane & 15, ku = (lane >> 4) * kUnit;
     const int f0 = blockIdx.x * 16;
-    const int64_t fr = min(f0 + row, a.F - 1);
-    const T *wg = a.wg + fr * a.C, *wu = a.wu + fr * a.C;
+    const int64_t fr = min(f0 + row, a.F - 1);  // past F (up to Fp): not used
+    const T *wg = a.wg + fr * a.w_ld, *wu = a.wu + fr * a.w_ld;
     const T* x[NP];
 #pragma unroll
-    for (int j = 0; j < NP; ++j) x[j] = a.x + min(static_cast<int64_t>(j * 16 + row), a.rows - 1) * a.C;
+    for (int j = 0; j < NP; ++j) x[j] = a.x + min(static_cast<int64_t>(j * 16 + row), a.rows - 1) * a.x_ld;
     f32x4 g[NP], u[NP];
 #pragma unroll
     for (int j = 0; j < NP; ++j) g[j] = u[j] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -839,9 +840,10 @@ __global__ __launch_bounds__(kFewWaves * 64) void gated_few_rows_kernel(Product<
     }
     __syncthreads();
     // value (p, f): lane (f / 4) * 16 + p of a group, element f % 4
+    __shared__ float down[MODE == kAgain ? 2 : 1][MODE == kAgain ? NP * 16 : 1][16];
     for (int idx = threadIdx.x; idx < NP * 256; idx += kFewWaves * 64) {
         const int f = idx & 15, p = idx >> 4;
-        if (p >= a.rows || f0 + f >= a.F) continue;
+        const bool on = p < a.rows && f0 + f < a.F;
         const int at = (f >> 2) * 16 + (p & 15);
         float gv = 0.f, uv = 0.f;
 #pragma unroll
@@ -849,12 +851,37 @@ __global__ __launch_bounds__(kFewWaves * 64) void gated_few_rows_kernel(Product<
             gv += reinterpret_cast<const float*>(&sums[w][0][p >> 4][at])[f & 3];
             uv += reinterpret_cast<const float*>(&sums[w][1][p >> 4][at])[f & 3];
         }
-        if (a.bg) gv += load_f(a.bg + f0 + f), uv += load_f(a.bu + f0 + f);
-        if (a.saved) {
-            a.saved[static_cast<int64_t>(p) * 2 * a.F + f0 + f] = gv;
-            a.saved[static_cast<int64_t>(p) * 2 * a.F + a.F + f0 + f] = uv;
+        if (a.bg && on) gv += load_f(a.bg + f0 + f), uv += load_f(a.bu + f0 + f);
+        if constexpr (MODE == kFwd) {
+            if (!on) continue;
+            if (a.saved) {
+                a.saved[static_cast<int64_t>(p) * 2 * a.F + f0 + f] = gv;
+                a.saved[static_cast<int64_t>(p) * 2 * a.F + a.F + f0 + f] = uv;
+            }
+            store_f(a.h + static_cast<int64_t>(p) * a.F + f0 + f, act_value(a.act, gv) * uv);
+        } else {
+            // the columns up to Fp too: zeros
+            const float dh = on ? load_f(a.dh + static_cast<int64_t>(p) * a.F + f0 + f) : 0.f;
+            const ActPair t = act_pair(a.act, gv);
+            const float dg = on ? dh * uv * t.d : 0.f, du = on ? dh * t.v : 0.f;
+            if (p < a.rows) {
+                T* d = a.d_out + static_cast<int64_t>(p) * 2 * a.Fp + f0 + f;
+                store_f(d, dg);
+                store_f(d + a.Fp, du);
+            }
+            down[0][p][f] = dg;
+            down[1][p][f] = du;
         }
-        store_f(a.h + static_cast<int64_t>(p) * a.F + f0 + f, act_value(a.act, gv) * uv);
+    }
+    if constexpr (MODE == kAgain) {
+        if (!a.sums) return;
+        __syncthreads();
+        if (threadIdx.x < 32) {
+            const int f = threadIdx.x & 15, half = threadIdx.x >> 4;
+            float t = 0.f;
+            for (int p = 0; p < NP * 16; ++p) t += down[half][p][f];
+            a.sums[static_cast<int64_t>(half) * a.Fp + f0 + f] = t;
+        }
     }
 }
 
@@ -864,12 +891,14 @@ struct Tiles {
     typedef Shape<bf16_t, 2, 2, 4, 4, 32, 4> Wide;   // 256 x 256, one workgroup a CU
     typedef Shape<bf16_t, 2, 2, 2, 4, 32, 3> Big;    // 128 x 256, two
     typedef Shape<bf16_t, 2, 2, 2, 2, 64, 2> Small;  // 128 x 128
+    typedef Shape<bf16_t, 4, 1, 1, 2, 64, 4> Thin;   // 128 x 64, a deep ring
 };
 template <>
 struct Tiles<float> {
     typedef Shape<float, 2, 2, 2, 4, 16, 3> Wide;  // none: the fp32 instructions leave time for every load
     typedef Shape<float, 2, 2, 2, 4, 16, 3> Big;
     typedef Shape<float, 2, 2, 1, 2, 32, 2> Small;  // 64 x 128
+    typedef Small Thin;  // none: 64 x 64 with a ring of four took 21 us where 64 x 128 took 15 (1001 rows, 190 -> 2 x 517)
 };
 
 bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -898,7 +927,12 @@ hipError_t run(Product<typename S::T>& k, int64_t p, int64_t q, int pieces, hipS
 // The largest tile that gives every CU its workgroups; the widest only for long
 // sums in bf16, where its loads and LDS reads (half as many for a product)
 // count and its epilogue, which nothing runs beside, does not.
-enum class Tile { kSmall, kBig, kWide };
+//
+// The forward product's sum is not cut into pieces.  Where its small tiles are
+// fewer than the CUs it is a stream over the weights, bound by the loads in
+// flight: the thin tile has twice the workgroups and three stages of loads
+// ahead instead of one (128 rows, 4096 -> 2 x 8192: 34 us, 28 the weights' stream).
+enum class Tile { kThin, kSmall, kBig, kWide };
 constexpr int64_t kLongSum = 1024;
 template <typename S>
 bool fills(int64_t p, int64_t q) { return tiles(p, S::BM) * tiles(q, S::BN) >= S::kPerCu * device_cu_count(); }
@@ -908,12 +942,21 @@ Tile pick(int64_t p, int64_t q, int64_t K)
     if (sizeof(T) == 2 && K >= kLongSum && fills<typename Tiles<T>::Wide>(p, q)) return Tile::kWide;
     return fills<typename Tiles<T>::Big>(p, q) ? Tile::kBig : Tile::kSmall;
 }
+template <typename T>
+Tile pick_gated(const GatedArgs& a)
+{
+    typedef typename Tiles<T>::Small Small;
+    const int64_t q = 2 * static_cast<int64_t>(a.F);
+    const Tile t = pick<T>(a.rows, q, a.C);
+    return sizeof(T) == 2 && t == Tile::kSmall && tiles(a.rows, Small::BM) * tiles(q, Small::BN) < device_cu_count() ? Tile::kThin : t;
+}
 // Calls f with the tile's shape.
 template <typename T, typename F>
 auto with_tile(Tile t, F f)
 {
     if (t == Tile::kWide) return f(typename Tiles<T>::Wide{});
     if (t == Tile::kBig) return f(typename Tiles<T>::Big{});
+    if (t == Tile::kThin) return f(typename Tiles<T>::Thin{});
     return f(typename Tiles<T>::Small{});
 }
 // Partial rows of the column sums of `rows` rows: one for each wave's rows.
@@ -948,9 +991,13 @@ hipError_t run_tiles(Product<T>& k, int64_t p, int64_t q, int pieces, Tile t, bo
     typedef Tiles<T> X;
     if constexpr (sizeof(T) == 2)
         if (t == Tile::kWide && fast) return run<typename X::Wide, MODE, true>(k, p, q, pieces, s);
+    if constexpr (sizeof(T) == 2 && (MODE == kFwd || MODE == kAgain))
+        if (t == Tile::kThin) return fast ? run<typename X::Thin, MODE, true>(k, p, q, pieces, s) : run<typename X::Thin, MODE, false>(k, p, q, pieces, s);
     if (t != Tile::kSmall) return fast ? run<typename X::Big, MODE, true>(k, p, q, pieces, s) : run<typename X::Big, MODE, false>(k, p, q, pieces, s);
     return fast ? run<typename X::Small, MODE, true>(k, p, q, pieces, s) : run<typename X::Small, MODE, false>(k, p, q, pieces, s);
 }
+
+constexpr int64_t kFewRows = 64;
 
 template <typename T>
 Product<T> product(const GatedArgs& a)
@@ -966,11 +1013,90 @@ Product<T> product(const GatedArgs& a)
     k.C = a.C;
     k.F = a.F;
     k.act = a.act;
+    k.x_ld = k.w_ld = a.C;
     return k;
 }
 
-constexpr int64_t kFewRows = 64;
-constexpr int64_t kLeastRows = 512, kLeastHidden = 512;  // of a piece of dW's sum, of dx's
+// Rows of a length that is no whole number of 16-byte units cannot go straight
+// to LDS, and passing them through registers takes the products to a third of
+// their rate.  So x and the weights are copied to rows with zeros behind them
+// first, which costs a launch and their bytes twice.  Training step, with
+// copies and without: 2000 rows, 1001 -> 2 x 3001: 176 and 385 us; 500 rows,
+// 101 -> 2 x 333: 49 and 85; 5 rows, 1001 -> 2 x 3001: 48 and 63.  The forward product alone (rows of x and weights
+// only, no columns) is slowed less: 42 and 52 us, 11 and 7, 1000 rows, 301 ->
+// 2 x 733: 14 and 10; it copies from kPadForward products on.
+constexpr int64_t kPadForward = int64_t(1) << 30;
+template <typename T>
+struct Padded {
+    int ld = 0;  // values; 0: no copies
+    size_t bytes = 0;
+    Padded(int64_t rows, int C, int F, bool forward)
+    {
+        if (C % (16 / sizeof(T)) == 0 || rows == 0 || (forward && (rows <= kFewRows || rows * F * C < kPadForward))) return;
+        ld = (C + 63) / 64 * 64;
+        bytes = round256((static_cast<size_t>(rows) + 2 * static_cast<size_t>(F)) * ld * sizeof(T));
+    }
+};
+template <typename T>
+struct PadArgs {
+    const T* src[3];
+    T* dst[3];
+    int64_t rows[3];
+    int C, ld;
+};
+// A wave a row; lanes past the row write zeros.
+template <typename T>
+__global__ __launch_bounds__(256) void gated_pad_kernel(PadArgs<T> a)
+{
+    constexpr int kUnit = 16 / sizeof(T);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const T* src = a.src[blockIdx.y];
+    T* dst = a.dst[blockIdx.y];
+    for (int64_t r = static_cast<int64_t>(blockIdx.x) * 4 + wave; r < a.rows[blockIdx.y]; r += static_cast<int64_t>(gridDim.x) * 4)
+        for (int c = lane * kUnit; c < a.ld; c += 64 * kUnit) {
+            const T* p = src + r * a.C + c;
+            const int n = a.C - c;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (n >= kUnit) {
+                v = load16_any(p);
+            } else if (n > 0) {
+                uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int e = 0; e < kUnit; ++e)
+                    if (e < n) {
+                        if constexpr (sizeof(T) == 2) w[e >> 1] |= static_cast<uint32_t>(p[e]) << (16 * (e & 1));
+                        else w[e] = __float_as_uint(p[e]);
+                    }
+                v = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            *reinterpret_cast<uint4*>(dst + r * a.ld + c) = v;
+        }
+}
+// Copies x and the weights to `at` and points k to the copies.
+template <typename T>
+hipError_t pad(Product<T>& k, int ld, char* at, hipStream_t s)
+{
+    PadArgs<T> a{};
+    a.C = k.C;
+    a.ld = ld;
+    const T* src[3] = {k.x, k.wg, k.wu};
+    T* dst = reinterpret_cast<T*>(at);
+    for (int i = 0; i < 3; ++i) {
+        a.src[i] = src[i];
+        a.dst[i] = dst;
+        a.rows[i] = i ? k.F : k.rows;
+        dst += a.rows[i] * ld;
+    }
+    const int64_t most = std::max<int64_t>(k.rows, k.F);
+    const hipError_t e = launch(gated_pad_kernel<T>, dim3(static_cast<unsigned>(std::min<int64_t>((most + 3) / 4, 8 * device_cu_count())), 3), dim3(256), 0, s, a);
+    k.x = a.dst[0];
+    k.wg = a.dst[1];
+    k.wu = a.dst[2];
+    k.x_ld = k.w_ld = ld;
+    return e;
+}
+
+constexpr int64_t kLeastRows = 256, kLeastHidden = 512;  // of a piece of dW's sum, of dx's
 
 template <typename T>
 GatedPlan gated_plan(int64_t rows, int C, int F)
@@ -984,12 +1110,22 @@ GatedPlan gated_plan(int64_t rows, int C, int F)
     p.x_per = x.per;
     p.x_pieces = x.pieces;
     int64_t chunk;
-    p.sum_rows = static_cast<int>(std::max<int64_t>(gated_kept_chunks(rows, p.Fp, &chunk), sum_rows<T>(rows, Tile::kSmall)));
+    p.sum_rows = static_cast<int>(std::max<int64_t>(gated_kept_chunks(rows, p.Fp, &chunk), std::max(sum_rows<T>(rows, Tile::kSmall), sum_rows<T>(rows, Tile::kThin))));
     p.d_bytes = round256(static_cast<size_t>(rows) * 2 * p.Fp * sizeof(T));
     p.sum_bytes = round256(static_cast<size_t>(p.sum_rows) * 2 * p.Fp * 4);
+    p.pad_bytes = Padded<T>(rows, C, F, false).bytes;
     p.x_bytes = p.x_pieces > 1 ? round256(static_cast<size_t>(p.x_pieces) * rows * C * 4) : 0;
     p.w_bytes = p.pieces > 1 ? round256(static_cast<size_t>(p.pieces) * 2 * F * C * 4) : 0;
     return p;
+}
+
+template <int MODE, typename T>
+hipError_t few_rows(const Product<T>& k, int columns, bool fast, hipStream_t s)
+{
+    const dim3 grid((columns + 15) / 16), block(kFewWaves * 64);
+    if (k.rows <= 16) return launch(fast ? gated_few_rows_kernel<T, MODE, 1, true> : gated_few_rows_kernel<T, MODE, 1, false>, grid, block, 0, s, k);
+    if (k.rows <= 32) return launch(fast ? gated_few_rows_kernel<T, MODE, 2, true> : gated_few_rows_kernel<T, MODE, 2, false>, grid, block, 0, s, k);
+    return launch(fast ? gated_few_rows_kernel<T, MODE, 4, true> : gated_few_rows_kernel<T, MODE, 4, false>, grid, block, 0, s, k);
 }
 
 template <typename T>
@@ -998,16 +1134,25 @@ hipError_t gated_fwd(const GatedArgs& a, hipStream_t s)
     Product<T> k = product<T>(a);
     k.h = static_cast<T*>(a.h);
     k.saved = a.saved;
-    const bool fast = a.C % (16 / sizeof(T)) == 0 && aligned(a.x) && aligned(a.wg) && aligned(a.wu);
-    if (a.rows <= kFewRows) {
-        const dim3 grid((a.F + 15) / 16), block(kFewWaves * 64);
-        if (a.rows <= 16) return launch(fast ? gated_few_rows_kernel<T, 1, true> : gated_few_rows_kernel<T, 1, false>, grid, block, 0, s, k);
-        if (a.rows <= 32) return launch(fast ? gated_few_rows_kernel<T, 2, true> : gated_few_rows_kernel<T, 2, false>, grid, block, 0, s, k);
-        return launch(fast ? gated_few_rows_kernel<T, 4, true> : gated_few_rows_kernel<T, 4, false>, grid, block, 0, s, k);
+    bool fast = a.C % (16 / sizeof(T)) == 0 && aligned(a.x) && aligned(a.wg) && aligned(a.wu);
+    if (a.rows <= kFewRows) return few_rows<kFwd>(k, a.F, fast, s);
+    const Padded<T> padded(a.rows, a.C, a.F, true);
+    if (padded.ld && a.workspace) {
+        const ArmedEvents armed = armed_events();
+        armed_events() = ArmedEvents{armed.start, nullptr};
+        const hipError_t e = pad(k, padded.ld, static_cast<char*>(a.workspace), s);
+        armed_events() = ArmedEvents{nullptr, armed.stop};
+        if (e != hipSuccess) {
+            armed_events() = ArmedEvents{nullptr, nullptr};
+            return e;
+        }
+        fast = true;
     }
-    const int64_t q = 2 * static_cast<int64_t>(a.F);
-    return run_tiles<kFwd>(k, a.rows, q, 1, pick<T>(a.rows, q, a.C), fast, s);
+    return run_tiles<kFwd>(k, a.rows, 2 * static_cast<int64_t>(a.F), 1, pick_gated<T>(a), fast, s);
 }
+
+template <typename T>
+size_t gated_fwd_workspace(int64_t rows, int C, int F) { return Padded<T>(rows, C, F, true).bytes; }
 
 template <typename T>
 hipError_t gated_bwd(const GatedArgs& a, hipStream_t s)
@@ -1025,6 +1170,13 @@ hipError_t gated_bwd(const GatedArgs& a, hipStream_t s)
     int summed = 0;
     Product<T> k = product<T>(a);
     k.Fp = p.Fp;
+    const Padded<T> padded(a.rows, a.C, a.F, false);
+    if (padded.ld) {
+        e = pad(k, padded.ld, ws + p.d_bytes + p.sum_bytes + p.x_bytes + p.w_bytes, s);
+        armed_events() = ArmedEvents{nullptr, nullptr};
+        if (e != hipSuccess) return e;
+    }
+    const bool whole = padded.ld || a.C % kUnit == 0;  // rows are whole units
     if (a.rows > 0) {
         if (a.saved) {
             int64_t chunk;
@@ -1033,12 +1185,16 @@ hipError_t gated_bwd(const GatedArgs& a, hipStream_t s)
         } else {
             k.d_out = d;
             k.sums = sums;
-            const bool fast = a.C % kUnit == 0 && aligned(a.x) && aligned(a.wg) && aligned(a.wu);
-            const int64_t q = 2 * static_cast<int64_t>(a.F);
-            Tile t = pick<T>(a.rows, q, a.C);
-            if (t == Tile::kWide && !fast) t = Tile::kBig;
-            summed = static_cast<int>(sum_rows<T>(a.rows, t));
-            e = run_tiles<kAgain>(k, a.rows, q, 1, t, fast, s);
+            const bool fast = whole && aligned(k.x) && aligned(k.wg) && aligned(k.wu);
+            if (a.rows <= kFewRows) {
+                summed = 1;
+                e = few_rows<kAgain>(k, p.Fp, fast, s);
+            } else {
+                Tile t = pick_gated<T>(a);
+                if (t == Tile::kWide && !fast) t = Tile::kBig;
+                summed = static_cast<int>(sum_rows<T>(a.rows, t));
+                e = run_tiles<kAgain>(k, a.rows, 2 * static_cast<int64_t>(p.Fp), 1, t, fast, s);  // the columns up to Fp too
+            }
         }
         armed_events() = ArmedEvents{nullptr, nullptr};
         if (e != hipSuccess) return e;
@@ -1048,7 +1204,7 @@ hipError_t gated_bwd(const GatedArgs& a, hipStream_t s)
             k.part = x_part;
             k.per = p.x_per;
             e = run_tiles<kDx>(k, a.rows, a.C, p.x_pieces, pick<T>(a.rows, a.C, 2 * static_cast<int64_t>(p.Fp)),
-                               a.C % kUnit == 0 && aligned(a.wg) && aligned(a.wu), s);
+                               whole && aligned(k.wg) && aligned(k.wu), s);
             if (e != hipSuccess) return e;
         }
     }
@@ -1061,7 +1217,7 @@ hipError_t gated_bwd(const GatedArgs& a, hipStream_t s)
         k.per = p.per;
         if (last) armed_events() = ArmedEvents{nullptr, armed.stop};
         const int64_t dp = 2 * static_cast<int64_t>(p.Fp);
-        e = run_tiles<kDw>(k, dp, a.C, p.pieces, pick<T>(dp, a.C, a.rows), a.C % kUnit == 0 && aligned(a.x), s);
+        e = run_tiles<kDw>(k, dp, a.C, p.pieces, pick<T>(dp, a.C, a.rows), whole && aligned(k.x), s);
         armed_events() = ArmedEvents{nullptr, nullptr};
         if (e != hipSuccess) return e;
     }

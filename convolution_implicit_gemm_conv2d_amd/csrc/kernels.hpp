@@ -134,6 +134,7 @@ struct GatedArgs {
 };
 hipError_t launch_gated_fwd(const GatedArgs& a, int dtype, hipStream_t s);
 hipError_t launch_gated_bwd(const GatedArgs& a, int dtype, hipStream_t s);
+size_t gated_fwd_workspace(int64_t rows, int C, int F, int dtype);
 size_t gated_bwd_workspace(int64_t rows, int C, int F, int dtype);
 
 // Global norm of a list of gradients and clipping by it.

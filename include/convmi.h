@@ -394,6 +394,24 @@ int conv_gated_fwd(const void *x, const void *w_gate, const void *w_up,
                    int dtype, void *stream);
 
 /*
+ * conv_gated_fwd with a workspace (16-byte aligned, at least
+ * conv_gated_fwd_workspace_size bytes; NULL where that is 0), for copies of x
+ * and the weights where their rows are no whole number of 16 bytes: faster
+ * there, the same elsewhere.  Errors as conv_gated_fwd, and
+ * CONV_ERR_INVALID_ARG for the workspace.
+ */
+int conv_gated_fwd_ex(const void *x, const void *w_gate, const void *w_up,
+                      const void *b_gate, const void *b_up, void *h,
+                      float *saved, void *workspace, size_t workspace_bytes,
+                      long long rows, int C, int F, int act, int dtype,
+                      void *stream);
+
+/* Workspace bytes of conv_gated_fwd_ex for these sizes, 0 where it needs
+ * none.  Host only. */
+int conv_gated_fwd_workspace_size(long long rows, int C, int F, int dtype,
+                                  size_t *bytes);
+
+/*
  * Gradient of conv_gated_fwd from dh [rows, F]:
  *   dg = dh u act'(g), du = dh act(g);  dx = dg w_gate + du w_up;
  *   dw_gate = dg^T x, dw_up = du^T x;  db_gate, db_up: column sums of dg, du.

@@ -218,3 +218,18 @@ def test_tensor_level_refusals():
 @pytest.mark.parametrize("dtype", [0, 1])
 def test_gated_workspace_without_rows(dtype):
     assert cm.conv_gated_bwd_workspace_size(0, 16, 24, dtype) >= 0
+
+
+def test_gated_forward_workspace():
+    assert cm.conv_gated_fwd_workspace_size(4096, 256, 1024, 1) == 0  # whole units
+    need = cm.conv_gated_fwd_workspace_size(4096, 255, 2048, 1)
+    assert need >= (4096 + 2 * 2048) * 256 * 2
+    lib = _lib.load()
+    assert lib.conv_gated_fwd_workspace_size(1, 1, 1, 1, None) == cm.CONV_ERR_INVALID_ARG
+    for ws, size in ((None, need), (FAKE + 8, need), (FAKE, need - 1)):
+        assert lib.conv_gated_fwd_ex(FAKE, FAKE, FAKE, None, None, FAKE, None, ws, size, 4096, 255, 2048, 2, 1,
+                                     None) == cm.CONV_ERR_INVALID_ARG
+    for bad in GATED_BAD:
+        a = {**dict(x=FAKE, wg=FAKE, wu=FAKE, bg=None, bu=None, saved=None, rows=4, C=8, F=8, act=2, dtype=1), **bad}
+        assert lib.conv_gated_fwd_ex(a["x"], a["wg"], a["wu"], a["bg"], a["bu"], FAKE, a["saved"], None, 0, a["rows"], a["C"],
+                                     a["F"], a["act"], a["dtype"], None) == cm.CONV_ERR_INVALID_ARG
