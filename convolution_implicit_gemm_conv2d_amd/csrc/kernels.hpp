@@ -107,6 +107,9 @@ hipError_t launch_sums(SumArgs a, int dtype, hipStream_t s);
 
 // Norms before and after a block with gate and residual scale (see
 // conv_block_norm_fwd / conv_block_norm_bwd in include/convmi.h).
+struct RowStats {
+    float f_mean, f_r, y_mean, y_r, c1, c2;       // what the column sums of a long row need of it
+};
 struct NormArgs {
     const void *dy, *da;                          // backward only
     const void *x, *f, *z, *s;                    // stream, branch, gate, scale
@@ -114,6 +117,7 @@ struct NormArgs {
     void *y, *a;                                  // forward
     void *dx, *df, *dz, *ds, *dpost_w, *dpost_b, *dpre_w, *dpre_b;
     float* part;                                  // fp32 partial sums
+    RowStats* stats;                              // of long rows, behind them
     int64_t rows, gate_rows;                      // gate_rows: rows that share one gate row
     int C;
     int post, pre, act;

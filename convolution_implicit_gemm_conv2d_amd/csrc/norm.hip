@@ -220,6 +220,34 @@ __device__ __forceinline__ void load_param(const void* p, const Part<VPT>& part,
         if (p) v[i].load(rows_from<T>(p, 0), part.template off<T>(i, 0));
     }
 }
+// A parameter's values for a lane's channels: kept in registers over the rows
+// with one vector a lane, read again for each row with two.
+template <typename T, int VPT>
+struct Param {
+    static constexpr bool kKept = VPT == 1;
+    Raw<T> raw[kKept ? VPT : 1];
+    const void* p;
+    float other;
+    __device__ __forceinline__ Param(const void* from, const Part<VPT>& part, float fill) : p(from), other(fill)
+    {
+        if constexpr (kKept) load_param(p, part, other, raw);
+    }
+    __device__ __forceinline__ void stay()
+    {
+        if constexpr (kKept) raw[0].stay();
+    }
+    __device__ __forceinline__ void get(const Part<VPT>& part, Row<VPT>& v) const
+    {
+        if constexpr (kKept) {
+            raw[0].get(v[0]);
+        } else {
+            Raw<T> now[VPT];
+            load_param(p, part, other, now);
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) now[i].get(v[i]);
+        }
+    }
+};
 template <typename T, int VPT>
 __device__ __forceinline__ void get_row(const Raw<T> (&r)[VPT], Row<VPT>& v)
 {
@@ -248,17 +276,21 @@ __device__ __forceinline__ float lane_sum(const Part<VPT>& part, F term)
     return t;
 }
 
-// Normalises a row in place and returns r.
+// Normalises a row in place; its mean (layer) and r.
+struct Stats {
+    float mean, r;
+};
 template <int L, int VPT>
-__device__ __forceinline__ float normalise(int kind, const Part<VPT>& part, float inv_c, float eps, RowSum<L>& rs, Row<VPT>& v)
+__device__ __forceinline__ Stats normalise(int kind, const Part<VPT>& part, float inv_c, float eps, RowSum<L>& rs, Row<VPT>& v)
 {
+    float mean = 0.f;
     if (kind == kNormLayer) {
-        const float mean = rs.one(lane_sum(part, [&](int i, int e) { return v[i][e]; })) * inv_c;
+        mean = rs.one(lane_sum(part, [&](int i, int e) { return v[i][e]; })) * inv_c;
         CONVMI_EACH(i, e) v[i][e] -= mean;
     }
     const float r = 1.0f / sqrtf(rs.one(lane_sum(part, [&](int i, int e) { return v[i][e] * v[i][e]; })) * inv_c + eps);
     CONVMI_EACH(i, e) v[i][e] *= r;
-    return r;
+    return {mean, r};
 }
 
 struct NormGrid {
@@ -280,12 +312,8 @@ __global__ __launch_bounds__(MAXT, 4) void norm_fwd_kernel(NormArgs k, NormGrid 
     const Part<VPT> part(k.C, lanes, lane);
     const float inv_c = 1.0f / k.C;
     const bool each = k.z && k.gate_rows == 1;  // a gate for every element
-    Raw<T> post_w[VPT], post_b[VPT], pre_w[VPT], pre_b[VPT], s[VPT];
-    load_param(k.post_w, part, 1.f, post_w);
-    load_param(k.post_b, part, 0.f, post_b);
-    load_param(k.pre_w, part, 1.f, pre_w);
-    load_param(k.pre_b, part, 0.f, pre_b);
-    load_param(k.s, part, 1.f, s);
+    Param<T, VPT> post_w(k.post_w, part, 1.f), post_b(k.post_b, part, 0.f), pre_w(k.pre_w, part, 1.f), pre_b(k.pre_b, part, 0.f), s(k.s, part, 1.f);
+    constexpr bool kAhead = VPT == 1;  // a row's loads go out before the row before it is worked on
 
     // A wave's rows follow each other: the 64 / L rows that it takes at a time
     // are neighbours, and so are those it takes next.
@@ -304,14 +332,14 @@ __global__ __launch_bounds__(MAXT, 4) void norm_fwd_kernel(NormArgs k, NormGrid 
         if (k.f) load_row(rows_from<T>(k.f, r * k.C), off, fr);
         if (each) load_row(rows_from<T>(k.z, r * k.C), off, zr);
     };
-    fetch(first);
+    if (kAhead) fetch(first);
     Row<VPT> g;  // s act(z)
-    get_row(s, g);
+    s.get(part, g);
     int64_t gate_at = -1;
     for (int64_t r = first; r < end; r += R) {  // rows r to r + R - 1
         Row<VPT> v, n, w, b;
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) post_w[i].stay(), post_b[i].stay(), pre_w[i].stay(), pre_b[i].stay(), s[i].stay();
+        post_w.stay(), post_b.stay(), pre_w.stay(), pre_b.stay(), s.stay();
+        if (!kAhead) fetch(r);
         get_row(xr, v);
         if (k.f) get_row(fr, n);
         if (k.z) {
@@ -327,18 +355,18 @@ __global__ __launch_bounds__(MAXT, 4) void norm_fwd_kernel(NormArgs k, NormGrid 
                             for (int h = 0; h < Raw<T>::kWords; ++h) zr[i].u[h] = load16_any(p + h * 4);
                         }
                 }
-                get_row(s, g);
+                s.get(part, g);
                 get_row(zr, w);
                 with_act(k.act, [&](auto kind) __attribute__((always_inline)) { CONVMI_EACH(i, e) g[i][e] *= act_value<kind()>(w[i][e]); });
             }
         }
-        if (r + R < end) fetch(r + R);
+        if (kAhead && r + R < end) fetch(r + R);
         if (sub >= end - r) break;
         if (k.f) {
             if (k.post != kNormNone) {
                 normalise(k.post, part, inv_c, k.eps, rs, n);
-                get_row(post_w, w);
-                get_row(post_b, b);
+                post_w.get(part, w);
+                post_b.get(part, b);
                 CONVMI_EACH(i, e) n[i][e] = n[i][e] * w[i][e] + b[i][e];
             }
             CONVMI_EACH(i, e) v[i][e] += g[i][e] * n[i][e];
@@ -346,8 +374,8 @@ __global__ __launch_bounds__(MAXT, 4) void norm_fwd_kernel(NormArgs k, NormGrid 
         if (k.y) store_row<T>(rows_from<T>(k.y, r * k.C), off, v);
         if (k.a) {
             normalise(k.pre, part, inv_c, k.eps, rs, v);
-            get_row(pre_w, w);
-            get_row(pre_b, b);
+            pre_w.get(part, w);
+            pre_b.get(part, b);
             CONVMI_EACH(i, e) v[i][e] = v[i][e] * w[i][e] + b[i][e];
             store_row<T>(rows_from<T>(k.a, r * k.C), off, v);
         }
@@ -364,6 +392,7 @@ struct Pieces {
     int split;         // pieces of a group
     int count;
 };
+bool sums_apart(int C);
 Pieces make_pieces(int64_t rows, int64_t gate_rows, int C, bool has_gate)
 {
     Pieces p{};
@@ -373,7 +402,8 @@ Pieces make_pieces(int64_t rows, int64_t gate_rows, int C, bool has_gate)
     // As many workgroups as the device holds at once (four a CU for rows of a
     // wave, two for longer ones); fewer where a piece would have too few rows
     // to pay for its partial sums.
-    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(C <= 512 ? 1024 : std::max(512, std::min(1024, 8388608 / C / 2)), rows / (C <= 512 ? 8 : 2)));
+    const int64_t want = sums_apart(C) ? std::max<int64_t>(1, std::min<int64_t>(std::max(1, 1024 / ((C + 2047) / 2048)), rows / 4))
+                                       : std::max<int64_t>(1, std::min<int64_t>(C <= 512 ? 1024 : std::max(512, std::min(1024, 8388608 / C / 2)), rows / (C <= 512 ? 8 : 2)));
     if (groups <= want) {
         p.groups = 1;
         const int64_t split = std::min<int64_t>(std::max<int64_t>(1, want / std::max<int64_t>(groups, 1)), p.group);
@@ -397,9 +427,10 @@ Pieces make_pieces(int64_t rows, int64_t gate_rows, int C, bool has_gate)
 template <typename T, int L, int MAXT, bool MORE>
 constexpr int bwd_waves() { return MAXT > 512 || (sizeof(T) == 2 && !MORE && !L) ? 4 : 2; }
 // BIAS: with the sums of a layer norm's biases.  SHARED: a gate row serves
-// several rows.
-template <typename T, int VPT, int L, int MAXT, bool BIAS, bool SHARED>
-__global__ __launch_bounds__(MAXT, (bwd_waves<T, L, MAXT, BIAS || SHARED>())) void norm_bwd_kernel(NormArgs k, Pieces pc)
+// several rows.  Without SUMS, for rows whose sums do not fit in the registers
+// beside them: the rows alone, and their statistics.
+template <typename T, int VPT, int L, int MAXT, bool BIAS, bool SHARED, bool SUMS>
+__global__ __launch_bounds__(MAXT, (bwd_waves<T, L, MAXT, BIAS || SHARED>())) void norm_bwd_kernel(NormArgs k, Pieces pc, FastDiv gate_rows)
 {
     __shared__ __align__(16) float slots[2][2][kMaxWaves];
     __shared__ float joined[L ? 4 : 1][L ? 64 * VPT * kVec : 1];
@@ -413,6 +444,7 @@ __global__ __launch_bounds__(MAXT, (bwd_waves<T, L, MAXT, BIAS || SHARED>())) vo
     const int wave = L ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0, sub = L ? (threadIdx.x & 63) / (L ? L : 64) : 0;
     const Part<VPT> part(k.C, lanes, lane);
     const float inv_c = 1.0f / k.C;
+    static_assert(SUMS || (!L && !SHARED && !BIAS), "");
     const bool each = !SHARED && k.z;
     const int64_t mine = static_cast<int64_t>(blockIdx.x) * kSums * k.C;  // in k.part
     uint32_t off[VPT], param_off[VPT], sum_off[VPT];  // in rows, in one row, in a row of fp32
@@ -422,15 +454,12 @@ __global__ __launch_bounds__(MAXT, (bwd_waves<T, L, MAXT, BIAS || SHARED>())) vo
         param_off[i] = part.template off<T>(i, 0);
         sum_off[i] = part.template off<float>(i, 0);
     }
-    Raw<T> post_w[VPT], post_b[VPT], pre_w[VPT], s[VPT];
-    load_param(k.post_w, part, 1.f, post_w);
-    load_param(k.post_b, part, 0.f, post_b);
-    load_param(k.pre_w, part, 1.f, pre_w);
-    load_param(k.s, part, 1.f, s);
+    Param<T, VPT> post_w(k.post_w, part, 1.f), post_b(k.post_b, part, 0.f), pre_w(k.pre_w, part, 1.f), s(k.s, part, 1.f);
+    constexpr bool kAhead = VPT == 1;  // a row's loads go out before the row before it is worked on
 
     // In the order of the partial rows; for a shared gate [kSumScale] is the
     // group's sum of P, from which dz and the group's part of ds follow.
-    constexpr int NS = BIAS ? kSumGate : 3;
+    constexpr int NS = !SUMS ? 1 : BIAS ? kSumGate : 3;
     float sum[NS][VPT][kVec], scale_sum[SHARED ? VPT : 1][kVec];
 #pragma unroll
     for (int q = 0; q < NS; ++q) CONVMI_EACH(i, e) sum[q][i][e] = 0.f;
@@ -466,14 +495,14 @@ __global__ __launch_bounds__(MAXT, (bwd_waves<T, L, MAXT, BIAS || SHARED>())) vo
     };
 
     const int64_t group0 = pc.split > 1 ? blockIdx.x / pc.split : blockIdx.x * pc.groups;
-    int64_t r0 = group0 * pc.group + (pc.split > 1 ? (blockIdx.x % pc.split) * pc.per : 0);
-    const int64_t end = min(pc.split > 1 ? (group0 + 1) * pc.group : k.rows, r0 + pc.per);
-    const int64_t step = L ? 4 * R : 1;
+    int64_t r0 = SUMS ? group0 * pc.group + (pc.split > 1 ? (blockIdx.x % pc.split) * pc.per : 0) : blockIdx.x;
+    const int64_t end = SUMS ? min(pc.split > 1 ? (group0 + 1) * pc.group : k.rows, r0 + pc.per) : k.rows;
+    const int64_t step = L ? 4 * R : SUMS ? 1 : gridDim.x;
     Raw<T> xr[VPT], fr[VPT], zr[VPT], yr[VPT], ar[VPT];
     auto fetch = [&](int64_t r) __attribute__((always_inline)) {
         load_row(rows_from<T>(k.x, r * k.C), off, xr);
         if (k.f) load_row(rows_from<T>(k.f, r * k.C), off, fr);
-        if (each) load_row(rows_from<T>(k.z, r * k.C), off, zr);
+        if (each) load_row(rows_from<T>(k.z, (SUMS ? r : fdiv(static_cast<uint32_t>(r), gate_rows)) * static_cast<int64_t>(k.C)), off, zr);
     };
     auto fetch_grads = [&](int64_t r) __attribute__((always_inline)) {
         if (k.dy) load_row(rows_from<T>(k.dy, r * k.C), off, yr);
@@ -484,7 +513,7 @@ __global__ __launch_bounds__(MAXT, (bwd_waves<T, L, MAXT, BIAS || SHARED>())) vo
     while (r0 < end) {
         const int64_t stop = SHARED ? min(end, (r0 / pc.group + 1) * pc.group) : end;
         const int64_t begin = r0 + wave * R;
-        if (sub < stop - begin) {
+        if (kAhead && sub < stop - begin) {
             fetch(begin);
             fetch_grads(begin);
         }
@@ -507,68 +536,71 @@ __global__ __launch_bounds__(MAXT, (bwd_waves<T, L, MAXT, BIAS || SHARED>())) vo
         }
         for (int64_t r = begin; r < stop; r += step) {  // rows r to r + R - 1
             if (sub >= stop - r) break;
-            const bool more = sub < stop - r - step;
+            const bool more = kAhead && sub < stop - r - step;
             Row<VPT> v, n, d, w, b;
-            float rf = 1.f, ry = 1.f;
+            Stats sf{0.f, 1.f}, sy{0.f, 1.f};
+            float c1 = 0.f, c2 = 0.f;
             auto stay = [&]() __attribute__((always_inline)) {
-#pragma unroll
-                for (int i = 0; i < VPT; ++i) post_w[i].stay(), post_b[i].stay(), pre_w[i].stay(), s[i].stay();
+                post_w.stay(), post_b.stay(), pre_w.stay(), s.stay();
             };
             stay();
+            if (!kAhead) fetch(r);
             get_row(xr, v);
             if (k.f) get_row(fr, n);
             if (each) gate();
             if (more) fetch(r + step);
             // y again: v, with fh in n
             if (k.f) {
-                if (k.post != kNormNone) rf = normalise(k.post, part, inv_c, k.eps, rs, n);
+                if (k.post != kNormNone) sf = normalise(k.post, part, inv_c, k.eps, rs, n);
                 Row<VPT> g;
-                get_row(s, g);
-                get_row(post_w, w);
-                get_row(post_b, b);
+                s.get(part, g);
+                post_w.get(part, w);
+                post_b.get(part, b);
                 CONVMI_EACH(i, e) v[i][e] += g[i][e] * zv[i][e] * (n[i][e] * w[i][e] + b[i][e]);
             }
-            if (k.da) ry = normalise(k.pre, part, inv_c, k.eps, rs, v);
+            if (k.da) sy = normalise(k.pre, part, inv_c, k.eps, rs, v);
             // D in d
+            if (!kAhead) fetch_grads(r);
             get_row(yr, d);
             if (k.da) {
                 Row<VPT> t;
                 get_row(ar, t);
-                get_row(pre_w, w);
+                pre_w.get(part, w);
                 CONVMI_EACH(i, e)
                 {
-                    sum[kSumPreW][i][e] += t[i][e] * v[i][e];
+                    if constexpr (SUMS) sum[kSumPreW][i][e] += t[i][e] * v[i][e];
                     if constexpr (BIAS) sum[kSumPreB][i][e] += t[i][e];
                     t[i][e] *= w[i][e];
                 }
                 if (more) fetch_grads(r + step);
-                float c1 = lane_sum(part, [&](int i, int e) { return t[i][e]; });
-                float c2 = lane_sum(part, [&](int i, int e) { return t[i][e] * v[i][e]; });
+                c1 = lane_sum(part, [&](int i, int e) { return t[i][e]; });
+                c2 = lane_sum(part, [&](int i, int e) { return t[i][e] * v[i][e]; });
                 rs.two(c1, c2);
                 c1 = k.pre == kNormLayer ? c1 * inv_c : 0.f;
                 c2 *= inv_c;
-                CONVMI_EACH(i, e) d[i][e] += ry * (t[i][e] - c1 - v[i][e] * c2);
+                CONVMI_EACH(i, e) d[i][e] += sy.r * (t[i][e] - c1 - v[i][e] * c2);
             } else if (more) {
                 fetch_grads(r + step);
             }
             if (k.dx) store_row<T>(rows_from<T>(k.dx, r * k.C), off, d);
+            if (!SUMS && threadIdx.x == 0) k.stats[r] = RowStats{sf.mean, sf.r, sy.mean, sy.r, c1, c2};
             if (!k.f) continue;
             // gate, scale and branch: fh in n, D in d; v is free
             stay();
-            get_row(post_w, w);
-            get_row(post_b, b);
+            post_w.get(part, w);
+            post_b.get(part, b);
             CONVMI_EACH(i, e) v[i][e] = d[i][e] * (n[i][e] * w[i][e] + b[i][e]);  // P
             Row<VPT> g;
-            get_row(s, g);
-            CONVMI_EACH(i, e) sum[kSumScale][i][e] += SHARED ? v[i][e] : v[i][e] * zv[i][e];
-            if (each && k.dz) {
+            s.get(part, g);
+            if constexpr (SUMS) CONVMI_EACH(i, e) sum[kSumScale][i][e] += SHARED ? v[i][e] : v[i][e] * zv[i][e];
+            if (each && k.dz && (SUMS || k.gate_rows == 1)) {
                 CONVMI_EACH(i, e) v[i][e] *= g[i][e] * zd[i][e];
                 store_row<T>(rows_from<T>(k.dz, r * k.C), off, v);
             }
             CONVMI_EACH(i, e)
             {
                 const float dn = d[i][e] * (g[i][e] * zv[i][e]);
-                sum[kSumPostW][i][e] += dn * n[i][e];
+                if constexpr (SUMS) sum[kSumPostW][i][e] += dn * n[i][e];
                 if constexpr (BIAS) sum[kSumPostB][i][e] += dn;
                 v[i][e] = dn * w[i][e];  // without a post norm w is 1
             }
@@ -578,13 +610,13 @@ __global__ __launch_bounds__(MAXT, (bwd_waves<T, L, MAXT, BIAS || SHARED>())) vo
                 rs.two(e1, e2);
                 e1 = k.post == kNormLayer ? e1 * inv_c : 0.f;
                 e2 *= inv_c;
-                CONVMI_EACH(i, e) v[i][e] = rf * (v[i][e] - e1 - n[i][e] * e2);
+                CONVMI_EACH(i, e) v[i][e] = sf.r * (v[i][e] - e1 - n[i][e] * e2);
             }
             if (k.df) store_row<T>(rows_from<T>(k.df, r * k.C), off, v);
         }
         if constexpr (SHARED) {
             Row<VPT> g, t;
-            get_row(s, g);
+            s.get(part, g);
             CONVMI_EACH(i, e)
             {
                 t[i][e] = sum[kSumScale][i][e] * g[i][e] * zd[i][e];
@@ -602,7 +634,7 @@ __global__ __launch_bounds__(MAXT, (bwd_waves<T, L, MAXT, BIAS || SHARED>())) vo
     }
     if constexpr (SHARED) CONVMI_EACH(i, e) sum[kSumScale][i][e] = scale_sum[i][e];
 #pragma unroll
-    for (int q = 0; q < NS; ++q)
+    for (int q = 0; q < (SUMS ? NS : 0); ++q)
         join(sum[q], [&](Row<VPT>& v) { store_row<float>(rows_from<float>(k.part, mine + static_cast<int64_t>(q) * k.C), sum_off, v); });
 }
 #undef CONVMI_EACH
@@ -670,24 +702,15 @@ __global__ __launch_bounds__(kLongThreads) void norm_fwd_long_kernel(NormArgs k)
     }
 }
 
-// The same walk for the gradient.  A lane owns its channels, so it adds their
-// sums up in the workgroup's partial row in memory.
+// The same walk for the gradient's rows.
 template <typename T>
-__global__ __launch_bounds__(kLongThreads) void norm_bwd_long_kernel(NormArgs k, Pieces pc)
+__global__ __launch_bounds__(kLongThreads) void norm_bwd_long_kernel(NormArgs k)
 {
     __shared__ __align__(16) float slots[2][2][kMaxWaves];
     if (threadIdx.x < 4 * kMaxWaves) (&slots[0][0][0])[threadIdx.x] = 0.f;
     __syncthreads();
     LongRow row{k, 1.0f / k.C, RowSum<0>{slots, 0}};
-    const bool shared = k.z && k.gate_rows > 1;
-    float* mine = k.part + static_cast<int64_t>(blockIdx.x) * kSums * k.C;
-    for (int c = threadIdx.x; c < k.C; c += kLongThreads)
-#pragma unroll
-        for (int q = 0; q < kSums; ++q) mine[static_cast<int64_t>(q) * k.C + c] = 0.f;
-    const int64_t group0 = pc.split > 1 ? blockIdx.x / pc.split : blockIdx.x * pc.groups;
-    const int64_t r0 = group0 * pc.group + (pc.split > 1 ? (blockIdx.x % pc.split) * pc.per : 0);
-    const int64_t end = min(pc.split > 1 ? (group0 + 1) * pc.group : k.rows, r0 + pc.per);
-    for (int64_t r = r0; r < end; ++r) {
+    for (int64_t r = blockIdx.x; r < k.rows; r += gridDim.x) {
         const T* x = static_cast<const T*>(k.x) + r * k.C;
         const T* f = k.f ? static_cast<const T*>(k.f) + r * k.C : nullptr;
         const T* z = k.z ? static_cast<const T*>(k.z) + r / k.gate_rows * k.C : nullptr;
@@ -705,6 +728,7 @@ __global__ __launch_bounds__(kLongThreads) void norm_bwd_long_kernel(NormArgs k,
             if (k.pre == kNormLayer) c1 = row.sum(q) * row.inv_c;
             c2 = row.sum([&](int c) { return q(c) * (value(c) - ym) * yr; }) * row.inv_c;
         }
+        if (threadIdx.x == 0) k.stats[r] = RowStats{fm, fr, ym, yr, c1, c2};
         auto grad = [&](int c) {
             const float d = dy ? load_f(dy + c) : 0.f;
             return da ? d + yr * (q(c) - c1 - (value(c) - ym) * yr * c2) : d;
@@ -716,41 +740,123 @@ __global__ __launch_bounds__(kLongThreads) void norm_bwd_long_kernel(NormArgs k,
         }
         for (int c = threadIdx.x; c < k.C; c += kLongThreads) {
             const float d = grad(c);
-            auto add = [&](int which, float v) { mine[static_cast<int64_t>(which) * k.C + c] += v; };
-            if (da) {
-                add(kSumPreW, load_f(da + c) * (value(c) - ym) * yr);
-                add(kSumPreB, load_f(da + c));
-            }
-            if (f) {
-                const float P = d * branch(c), s = param<T>(k.s, c, 1.f), dn = d * factor(c);
-                if (z) {
-                    const ActPair a = act_pair(k.act, load_f(z + c));
-                    const float g = P * s * a.d;
-                    if (shared) add(kSumGate, g);
-                    else if (k.dz) store_f(static_cast<T*>(k.dz) + r * k.C + c, g);
-                    add(kSumScale, P * a.v);
-                } else {
-                    add(kSumScale, P);
-                }
-                add(kSumPostW, dn * fh(c));
-                add(kSumPostB, dn);
-                if (k.df) {
-                    const float t = k.post == kNormNone ? dn : fr * (dn * param<T>(k.post_w, c, 1.f) - e1 - fh(c) * e2);
-                    store_f(static_cast<T*>(k.df) + r * k.C + c, t);
-                }
-            }
             if (k.dx) store_f(static_cast<T*>(k.dx) + r * k.C + c, d);
-            if (shared && pc.split == 1 && (r + 1) % pc.group == 0) {
-                float& sum = mine[static_cast<int64_t>(kSumGate) * k.C + c];
-                if (k.dz) store_f(static_cast<T*>(k.dz) + r / pc.group * k.C + c, sum);
-                sum = 0.f;
+            if (!f) continue;
+            if (z && k.dz && k.gate_rows == 1)
+                store_f(static_cast<T*>(k.dz) + r * k.C + c, d * branch(c) * param<T>(k.s, c, 1.f) * act_pair(k.act, load_f(z + c)).d);
+            if (k.df) {
+                const float dn = d * factor(c);
+                const float t = k.post == kNormNone ? dn : fr * (dn * param<T>(k.post_w, c, 1.f) - e1 - fh(c) * e2);
+                store_f(static_cast<T*>(k.df) + r * k.C + c, t);
             }
         }
     }
 }
 
-// Rows of up to this many channels stay in the registers of a workgroup.
-constexpr int kRegisterRow = 16384;
+// The column sums of rows that were worked on without them, from their
+// statistics: a second stream over dy, da, x, f and z, in which a lane owns V
+// columns of a piece of the rows and nothing crosses lanes.  975 rows of 11823:
+// COLFIG.
+template <typename T, int V>
+__global__ __launch_bounds__(256) void norm_columns_kernel(NormArgs k, Pieces pc)
+{
+    const int want = (blockIdx.x * 256 + threadIdx.x) * V;
+    if (want >= k.C) return;
+    const int c = min(want, k.C - V);  // the last lane repeats columns of the one before: the same sums
+    const bool shared = k.z && k.gate_rows > 1;
+    auto get = [&](const void* p, int64_t row, float (&v)[V]) __attribute__((always_inline)) {
+        const T* t = static_cast<const T*>(p) + row * k.C + c;
+        if constexpr (V == 1) {
+            v[0] = load_f(t);
+        } else {
+            Raw<T> r;
+#pragma unroll
+            for (int i = 0; i < Raw<T>::kWords; ++i) r.u[i] = load16_any(t + i * 4);
+            r.get(v);
+        }
+    };
+    float post_w[V], post_b[V], pre_w[V], s[V], sum[kSums][V], zv[V], zd[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) post_w[e] = pre_w[e] = s[e] = zv[e] = 1.f, post_b[e] = zd[e] = 0.f;
+#pragma unroll
+    for (int q = 0; q < kSums; ++q)
+#pragma unroll
+        for (int e = 0; e < V; ++e) sum[q][e] = 0.f;
+    if (k.post_w) get(k.post_w, 0, post_w);
+    if (k.post_b) get(k.post_b, 0, post_b);
+    if (k.pre_w) get(k.pre_w, 0, pre_w);
+    if (k.s) get(k.s, 0, s);
+    const int piece = blockIdx.y;
+    const int64_t group0 = pc.split > 1 ? piece / pc.split : piece * pc.groups;
+    int64_t r0 = group0 * pc.group + (pc.split > 1 ? (piece % pc.split) * pc.per : 0);
+    const int64_t end = min(pc.split > 1 ? (group0 + 1) * pc.group : k.rows, r0 + pc.per);
+    float* mine = k.part + static_cast<int64_t>(piece) * kSums * k.C + c;
+    auto gate = [&](int64_t row) __attribute__((always_inline)) {
+        get(k.z, row, zv);
+        with_act(k.act, [&](auto kind) __attribute__((always_inline)) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const ActPair p = act_pair<kind()>(zv[e]);
+                zv[e] = p.v;
+                zd[e] = p.d;
+            }
+        });
+    };
+    while (r0 < end) {
+        const int64_t stop = shared ? min(end, (r0 / pc.group + 1) * pc.group) : end;
+        if (shared) gate(r0 / pc.group);
+        float P[V];  // the group's sum
+#pragma unroll
+        for (int e = 0; e < V; ++e) P[e] = 0.f;
+#pragma unroll 2
+        for (int64_t r = r0; r < stop; ++r) {
+            const RowStats t = k.stats[r];
+            float d[V], q[V], v[V], n[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) d[e] = q[e] = n[e] = 0.f;
+            get(k.x, r, v);
+            if (k.f) get(k.f, r, n);
+            if (k.dy) get(k.dy, r, d);
+            if (k.da) get(k.da, r, q);
+            if (k.z && !shared) gate(r);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float fh = k.post != kNormNone ? (n[e] - t.f_mean) * t.f_r : n[e];
+                const float branch = fh * post_w[e] + post_b[e], factor = s[e] * zv[e];
+                if (k.da) {
+                    const float yh = ((k.f ? v[e] + factor * branch : v[e]) - t.y_mean) * t.y_r;
+                    sum[kSumPreW][e] += q[e] * yh;
+                    sum[kSumPreB][e] += q[e];
+                    d[e] += t.y_r * (q[e] * pre_w[e] - t.c1 - yh * t.c2);
+                }
+                const float p = d[e] * branch, dn = d[e] * factor;
+                if (shared) P[e] += p;
+                else sum[kSumScale][e] += p * zv[e];
+                sum[kSumPostW][e] += dn * fh;
+                sum[kSumPostB][e] += dn;
+            }
+        }
+        if (shared) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                sum[kSumScale][e] += P[e] * zv[e];
+                const float g = P[e] * s[e] * zd[e];
+                if (pc.split > 1) mine[static_cast<int64_t>(kSumGate) * k.C + e] = g;
+                else if (k.dz) store_f(static_cast<T*>(k.dz) + r0 / pc.group * k.C + c + e, g);
+            }
+        }
+        r0 = stop;
+    }
+#pragma unroll
+    for (int q = 0; q < kSumGate; ++q)
+#pragma unroll
+        for (int e = 0; e < V; ++e) mine[static_cast<int64_t>(q) * k.C + e] = sum[q][e];
+}
+
+// Rows of up to this many channels stay in the registers of a workgroup, and of
+// up to this many with their column sums.
+constexpr int kRegisterRow = 16384, kSumRow = 8192;
+bool sums_apart(int C) { return C > kSumRow || C < kVec; }
 
 // Calls f with the vectors of a lane, the lanes of a row (0: a workgroup) and
 // the threads of its limit.  Rows of a wave use as many lanes as they have
@@ -797,9 +903,11 @@ hipError_t fwd(const NormArgs& a, hipStream_t s)
 }
 
 template <typename T>
-hipError_t bwd(const NormArgs& a, hipStream_t s)
+hipError_t bwd(const NormArgs& given, hipStream_t s)
 {
-    const Pieces pc = make_pieces(a.rows, a.gate_rows, a.C, a.z != nullptr);
+    const Pieces pc = make_pieces(given.rows, given.gate_rows, given.C, given.z != nullptr);
+    NormArgs a = given;
+    a.stats = reinterpret_cast<RowStats*>(a.part + static_cast<int64_t>(pc.count) * kSums * a.C);
     const bool shared = a.z && a.gate_rows > 1;
     const bool bias = a.dpre_b || a.dpost_b;
     const ArmedEvents armed = armed_events();
@@ -807,14 +915,27 @@ hipError_t bwd(const NormArgs& a, hipStream_t s)
     hipError_t e = hipSuccess;
     if (pc.count > 0) {
         const dim3 grid(pc.count);
-        if (a.C > kRegisterRow || a.C < kVec)
-            e = launch(norm_bwd_long_kernel<T>, grid, dim3(kLongThreads), 0, s, a, pc);
-        else
+        const FastDiv gate = make_fastdiv(static_cast<uint32_t>(a.gate_rows));
+        if (sums_apart(a.C)) {
+            const dim3 rows(static_cast<unsigned>(std::min<int64_t>(a.rows, device_cu_count() * (a.C > kRegisterRow ? 4 : 1))));
+            if (a.C > kRegisterRow || a.C < kVec)
+                e = launch(norm_bwd_long_kernel<T>, rows, dim3(kLongThreads), 0, s, a);
+            else
+                e = launch(norm_bwd_kernel<T, 2, 0, 1024, false, false, false>, rows, dim3(row_threads(a.C)), 0, s, a, pc, gate);
+            armed_events() = ArmedEvents{nullptr, nullptr};
+            if (e != hipSuccess) return e;
+            const unsigned v = a.C < kVec ? 1 : kVec;
+            const bool any = a.dpre_w || a.dpost_w || a.ds || a.dpre_b || a.dpost_b || (shared && a.dz);
+            if (any) e = launch(v == 1 ? norm_columns_kernel<T, 1> : norm_columns_kernel<T, kVec>, dim3((a.C + 256 * v - 1) / (256 * v), pc.count), dim3(256), 0, s, a, pc);
+        } else {
             with_shape(a.C, [&](auto vpt, auto l, auto maxt) {
-                auto kernel = bias ? (shared ? norm_bwd_kernel<T, vpt(), l(), maxt(), true, true> : norm_bwd_kernel<T, vpt(), l(), maxt(), true, false>)
-                                   : (shared ? norm_bwd_kernel<T, vpt(), l(), maxt(), false, true> : norm_bwd_kernel<T, vpt(), l(), maxt(), false, false>);
-                e = launch(kernel, grid, dim3(l() ? 256 : row_threads(a.C)), 0, s, a, pc);
+                if constexpr (vpt() == 1) {
+                    auto kernel = bias ? (shared ? norm_bwd_kernel<T, 1, l(), maxt(), true, true, true> : norm_bwd_kernel<T, 1, l(), maxt(), true, false, true>)
+                                       : (shared ? norm_bwd_kernel<T, 1, l(), maxt(), false, true, true> : norm_bwd_kernel<T, 1, l(), maxt(), false, false, true>);
+                    e = launch(kernel, grid, dim3(l() ? 256 : row_threads(a.C)), 0, s, a, pc, gate);
+                }
             });
+        }
     }
     armed_events() = ArmedEvents{nullptr, nullptr};
     if (e != hipSuccess) return e;
@@ -846,7 +967,7 @@ hipError_t launch_norm_fwd(const NormArgs& a, int dtype, hipStream_t s)
 size_t norm_bwd_workspace(int64_t rows, int64_t gate_rows, int C, int has_gate)
 {
     const Pieces pc = make_pieces(rows, gate_rows, C, has_gate != 0);
-    return static_cast<size_t>(pc.count) * kSums * C * sizeof(float);
+    return static_cast<size_t>(pc.count) * kSums * C * sizeof(float) + (sums_apart(C) ? static_cast<size_t>(rows) * sizeof(RowStats) : 0);
 }
 
 hipError_t launch_norm_bwd(const NormArgs& a, int dtype, hipStream_t s)
