@@ -16,8 +16,10 @@ struct GatedPlan {
     int sum_rows;          // partial rows of the column sums, [2][Fp] each
     int pieces;            // of the weight gradients' sum; 1: no partials
     int64_t per;           // rows of a piece
-    int x_pieces;          // of dx's sum, and values of a piece
+    int tile;              // and the product's tile
+    int x_pieces;          // of dx's sum, values of a piece, tile
     int64_t x_per;
+    int x_tile;
     size_t d_bytes, sum_bytes, x_bytes, w_bytes, pad_bytes;
     size_t total() const { return d_bytes + sum_bytes + x_bytes + w_bytes + pad_bytes; }
 };

@@ -895,9 +895,8 @@ struct Tiles {
 };
 template <>
 struct Tiles<float> {
-    typedef Shape<float, 2, 2, 2, 4, 16, 3> Wide;  // none: the fp32 instructions leave time for every load
-    typedef Shape<float, 2, 2, 2, 4, 16, 3> Big;
     typedef Shape<float, 2, 2, 1, 2, 32, 2> Small;  // 64 x 128
+    typedef Small Wide, Big;
     typedef Small Thin;  // none: 64 x 64 with a ring of four took 21 us where 64 x 128 took 15 (1001 rows, 190 -> 2 x 517)
 };
 
@@ -924,31 +923,56 @@ hipError_t run(Product<typename S::T>& k, int64_t p, int64_t q, int pieces, hipS
     return launch(kernel, dim3(static_cast<unsigned>(std::min<int64_t>((n + 7) / 8 * 8, hold))), dim3(S::kThreads), S::kLds, s, k);
 }
 
-// The largest tile that gives every CU its workgroups; the widest only for long
-// sums in bf16, where its loads and LDS reads (half as many for a product)
-// count and its epilogue, which nothing runs beside, does not.
+// Which tile: the one whose rounds take the least time.  A round is one tile in
+// every place of the device, and takes the tile's products at the rate that the
+// tile reaches plus its epilogue (us; what the other workgroup of a CU does not
+// hide of it).  Rates (TFLOP/s) and epilogues as measured: 256 x 256 tiles
+// reach 1150, have half the loads and LDS reads for a product, and nothing
+// beside their epilogue; 128 x 256 1050, 128 x 128 750 (all bf16); fp32's
+// instructions leave time for every load, 64 x 128 reach 105, 128 x 256 no more.
 //
 // The forward product's sum is not cut into pieces.  Where its small tiles are
 // fewer than the CUs it is a stream over the weights, bound by the loads in
 // flight: the thin tile has twice the workgroups and three stages of loads
 // ahead instead of one (128 rows, 4096 -> 2 x 8192: 34 us, 28 the weights' stream).
 enum class Tile { kThin, kSmall, kBig, kWide };
-constexpr int64_t kLongSum = 1024;
 template <typename S>
-bool fills(int64_t p, int64_t q) { return tiles(p, S::BM) * tiles(q, S::BN) >= S::kPerCu * device_cu_count(); }
-template <typename T>
-Tile pick(int64_t p, int64_t q, int64_t K)
+double tile_us(int64_t K, double rate, double epilogue)
 {
-    if (sizeof(T) == 2 && K >= kLongSum && fills<typename Tiles<T>::Wide>(p, q)) return Tile::kWide;
-    return fills<typename Tiles<T>::Big>(p, q) ? Tile::kBig : Tile::kSmall;
+    return 2e-6 * S::BM * S::BN * static_cast<double>(K) / rate * S::kPerCu * device_cu_count() + epilogue;
+}
+template <typename S>
+double rounds_us(int64_t n, int64_t K, double rate, double epilogue)
+{
+    const int64_t places = S::kPerCu * static_cast<int64_t>(device_cu_count());
+    return static_cast<double>((n + places - 1) / places) * tile_us<S>(K, rate, epilogue);
+}
+// The time of `pieces` products over K values each, by tile.
+template <typename T>
+double product_us(Tile t, int64_t p, int64_t q, int64_t K, int pieces)
+{
+    typedef Tiles<T> X;
+    if constexpr (sizeof(T) == 4) return rounds_us<typename X::Small>(tiles(p, X::Small::BM) * tiles(q, X::Small::BN) * pieces, K, 105, 1);
+    if (t == Tile::kWide) return rounds_us<typename X::Wide>(tiles(p, X::Wide::BM) * tiles(q, X::Wide::BN) * pieces, K, 1150, 10);
+    if (t == Tile::kBig) return rounds_us<typename X::Big>(tiles(p, X::Big::BM) * tiles(q, X::Big::BN) * pieces, K, 1050, 4);
+    return rounds_us<typename X::Small>(tiles(p, X::Small::BM) * tiles(q, X::Small::BN) * pieces, K, 750, 2);
+}
+template <typename T>
+Tile pick(int64_t p, int64_t q, int64_t K, int pieces = 1)
+{
+    if (sizeof(T) == 4) return Tile::kSmall;
+    Tile best = Tile::kSmall;
+    for (Tile t : {Tile::kBig, Tile::kWide})
+        if (product_us<T>(t, p, q, K, pieces) < product_us<T>(best, p, q, K, pieces)) best = t;
+    return best;
 }
 template <typename T>
 Tile pick_gated(const GatedArgs& a)
 {
     typedef typename Tiles<T>::Small Small;
     const int64_t q = 2 * static_cast<int64_t>(a.F);
-    const Tile t = pick<T>(a.rows, q, a.C);
-    return sizeof(T) == 2 && t == Tile::kSmall && tiles(a.rows, Small::BM) * tiles(q, Small::BN) < device_cu_count() ? Tile::kThin : t;
+    if (sizeof(T) == 2 && tiles(a.rows, Small::BM) * tiles(q, Small::BN) < device_cu_count()) return Tile::kThin;
+    return pick<T>(a.rows, q, a.C);
 }
 // Calls f with the tile's shape.
 template <typename T, typename F>
@@ -966,23 +990,31 @@ int64_t sum_rows(int64_t rows, Tile t)
     return with_tile<T>(t, [&](auto shape) { return tiles(rows, shape.BM) * shape.WP; });
 }
 
-// Pieces of a sum over K for a p x q output: as many as fill the device, none
-// under `least` values, a whole number of stages each.
+// Pieces of a sum over K for a p x q output, none under `least` values, a whole
+// number of stages each, and the tile: where the rounds of the pieces and the
+// stream over their partials (written and read, 3.5 TB/s, and their sums' launch)
+// take the least time.
 struct Split {
     int64_t per;
     int pieces;
+    Tile tile;
 };
 template <typename T>
 Split split(int64_t p, int64_t q, int64_t K, int64_t least)
 {
-    const int64_t n = with_tile<T>(pick<T>(p, q, K), [&](auto shape) {
-        return shape.kPerCu * static_cast<int64_t>(device_cu_count()) / std::max<int64_t>(1, tiles(p, shape.BM) * tiles(q, shape.BN));
-    });
-    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(n, K / least));
-    Split r;
-    r.per = std::max<int64_t>(64, (tiles(K, static_cast<int>(want)) + 63) / 64 * 64);
-    r.pieces = static_cast<int>(std::max<int64_t>(1, (K + r.per - 1) / r.per));
-    return r;
+    Split best{std::max<int64_t>(64, (K + 63) / 64 * 64), 1, pick<T>(p, q, K)};
+    double time = product_us<T>(best.tile, p, q, K, 1);
+    for (int64_t n = 2; n <= K / least && n <= 64; ++n) {
+        const int64_t per = (tiles(K, static_cast<int>(n)) + 63) / 64 * 64;
+        const int pieces = static_cast<int>((K + per - 1) / per);
+        const double sums = 3 + 8.0 * pieces * p * q / 3.5e6;
+        for (Tile t : {Tile::kSmall, Tile::kBig, Tile::kWide}) {
+            if (sizeof(T) == 4 && t != Tile::kSmall) continue;
+            const double us = product_us<T>(t, p, q, per, pieces) + sums;
+            if (us < time) time = us, best = Split{per, pieces, t};
+        }
+    }
+    return best;
 }
 
 template <int MODE, typename T>
@@ -993,7 +1025,8 @@ hipError_t run_tiles(Product<T>& k, int64_t p, int64_t q, int pieces, Tile t, bo
         if (t == Tile::kWide && fast) return run<typename X::Wide, MODE, true>(k, p, q, pieces, s);
     if constexpr (sizeof(T) == 2 && (MODE == kFwd || MODE == kAgain))
         if (t == Tile::kThin) return fast ? run<typename X::Thin, MODE, true>(k, p, q, pieces, s) : run<typename X::Thin, MODE, false>(k, p, q, pieces, s);
-    if (t != Tile::kSmall) return fast ? run<typename X::Big, MODE, true>(k, p, q, pieces, s) : run<typename X::Big, MODE, false>(k, p, q, pieces, s);
+    if constexpr (sizeof(T) == 2)
+        if (t != Tile::kSmall) return fast ? run<typename X::Big, MODE, true>(k, p, q, pieces, s) : run<typename X::Big, MODE, false>(k, p, q, pieces, s);
     return fast ? run<typename X::Small, MODE, true>(k, p, q, pieces, s) : run<typename X::Small, MODE, false>(k, p, q, pieces, s);
 }
 
@@ -1107,8 +1140,10 @@ GatedPlan gated_plan(int64_t rows, int C, int F)
     const Split w = split<T>(dp, C, rows, kLeastRows / least), x = split<T>(rows, C, dp, kLeastHidden / least);
     p.per = w.per;
     p.pieces = w.pieces;
+    p.tile = static_cast<int>(w.tile);
     p.x_per = x.per;
     p.x_pieces = x.pieces;
+    p.x_tile = static_cast<int>(x.tile);
     int64_t chunk;
     p.sum_rows = static_cast<int>(std::max<int64_t>(gated_kept_chunks(rows, p.Fp, &chunk), std::max(sum_rows<T>(rows, Tile::kSmall), sum_rows<T>(rows, Tile::kThin))));
     p.d_bytes = round256(static_cast<size_t>(rows) * 2 * p.Fp * sizeof(T));
@@ -1203,7 +1238,7 @@ hipError_t gated_bwd(const GatedArgs& a, hipStream_t s)
             k.out = static_cast<T*>(a.dx);
             k.part = x_part;
             k.per = p.x_per;
-            e = run_tiles<kDx>(k, a.rows, a.C, p.x_pieces, pick<T>(a.rows, a.C, 2 * static_cast<int64_t>(p.Fp)),
+            e = run_tiles<kDx>(k, a.rows, a.C, p.x_pieces, static_cast<Tile>(p.x_tile),
                                whole && aligned(k.wg) && aligned(k.wu), s);
             if (e != hipSuccess) return e;
         }
@@ -1217,7 +1252,7 @@ hipError_t gated_bwd(const GatedArgs& a, hipStream_t s)
         k.per = p.per;
         if (last) armed_events() = ArmedEvents{nullptr, armed.stop};
         const int64_t dp = 2 * static_cast<int64_t>(p.Fp);
-        e = run_tiles<kDw>(k, dp, a.C, p.pieces, pick<T>(dp, a.C, a.rows), whole && aligned(k.x), s);
+        e = run_tiles<kDw>(k, dp, a.C, p.pieces, static_cast<Tile>(p.tile), whole && aligned(k.x), s);
         armed_events() = ArmedEvents{nullptr, nullptr};
         if (e != hipSuccess) return e;
     }

@@ -421,16 +421,16 @@ Pieces make_pieces(int64_t rows, int64_t gate_rows, int C, bool has_gate)
 }
 
 // Waves of a SIMD: four where the registers hold a row of bf16 (a few spill),
-// two where more sums or fp32 rows would spill hundreds.  16384 x 4096 bf16:
-// 290 us with four, 310 with two; 1239 x 1001 fp32 layer norms with a shared
-// gate: 43 us with four, 20 with two.
-template <typename T, int L, int MAXT, bool MORE>
-constexpr int bwd_waves() { return MAXT > 512 || (sizeof(T) == 2 && !MORE && !L) ? 4 : 2; }
+// two where more sums, fp32 rows or a second vector a lane would spill
+// hundreds.  16384 x 4096 bf16: 290 us with four, 310 with two; 1239 x 1001
+// fp32 layer norms with a shared gate: 43 us with four, 20 with two.
+template <typename T, int VPT, int L, bool MORE>
+constexpr int bwd_waves() { return sizeof(T) == 2 && VPT == 1 && !MORE && !L ? 4 : 2; }
 // BIAS: with the sums of a layer norm's biases.  SHARED: a gate row serves
 // several rows.  Without SUMS, for rows whose sums do not fit in the registers
 // beside them: the rows alone, and their statistics.
 template <typename T, int VPT, int L, int MAXT, bool BIAS, bool SHARED, bool SUMS>
-__global__ __launch_bounds__(MAXT, (bwd_waves<T, L, MAXT, BIAS || SHARED>())) void norm_bwd_kernel(NormArgs k, Pieces pc, FastDiv gate_rows)
+__global__ __launch_bounds__(MAXT, (MAXT > 512 ? 4 : bwd_waves<T, VPT, L, BIAS || SHARED>())) void norm_bwd_kernel(NormArgs k, Pieces pc, FastDiv gate_rows)
 {
     __shared__ __align__(16) float slots[2][2][kMaxWaves];
     __shared__ float joined[L ? 4 : 1][L ? 64 * VPT * kVec : 1];
@@ -755,8 +755,9 @@ __global__ __launch_bounds__(kLongThreads) void norm_bwd_long_kernel(NormArgs k)
 
 // The column sums of rows that were worked on without them, from their
 // statistics: a second stream over dy, da, x, f and z, in which a lane owns V
-// columns of a piece of the rows and nothing crosses lanes.  975 rows of 11823:
-// COLFIG.
+// columns of a piece of the rows and nothing crosses lanes.  975 x 11823 bf16,
+// layer norms, a full gate, forward and gradient: 202 us; 652 with the sums in
+// the first pass, whose registers then spill.
 template <typename T, int V>
 __global__ __launch_bounds__(256) void norm_columns_kernel(NormArgs k, Pieces pc)
 {
@@ -860,7 +861,9 @@ bool sums_apart(int C) { return C > kSumRow || C < kVec; }
 
 // Calls f with the vectors of a lane, the lanes of a row (0: a workgroup) and
 // the threads of its limit.  Rows of a wave use as many lanes as they have
-// vectors; longer ones a workgroup, two vectors a lane past 8192 channels.
+// vectors; longer ones a workgroup, two vectors a lane past 4096 channels (2000 x
+// 6000 fp32 layer norms, forward and gradient: 239 us; 308 with one vector and
+// twice the threads, whose halved registers spill).
 template <typename F>
 void with_shape(int C, F f)
 {
@@ -874,10 +877,10 @@ void with_shape(int C, F f)
     else if (n <= 32) f(N1{}, std::integral_constant<int, 32>{}, T256{});
     else if (n <= 64) f(N1{}, std::integral_constant<int, 64>{}, T256{});
     else if (n <= 512) f(N1{}, N0{}, std::integral_constant<int, 512>{});
-    else if (n <= 1024) f(N1{}, N0{}, std::integral_constant<int, 1024>{});
+    else if (n <= 1024) f(N2{}, N0{}, std::integral_constant<int, 512>{});
     else f(N2{}, N0{}, std::integral_constant<int, 1024>{});
 }
-int row_threads(int C) { return C <= 8192 ? (C + 511) / 512 * 64 : (C + 1023) / 1024 * 64; }
+int row_threads(int C) { return C <= 4096 ? (C + 511) / 512 * 64 : (C + 1023) / 1024 * 64; }
 
 template <typename T>
 hipError_t fwd(const NormArgs& a, hipStream_t s)
@@ -929,9 +932,9 @@ hipError_t bwd(const NormArgs& given, hipStream_t s)
             if (any) e = launch(v == 1 ? norm_columns_kernel<T, 1> : norm_columns_kernel<T, kVec>, dim3((a.C + 256 * v - 1) / (256 * v), pc.count), dim3(256), 0, s, a, pc);
         } else {
             with_shape(a.C, [&](auto vpt, auto l, auto maxt) {
-                if constexpr (vpt() == 1) {
-                    auto kernel = bias ? (shared ? norm_bwd_kernel<T, 1, l(), maxt(), true, true, true> : norm_bwd_kernel<T, 1, l(), maxt(), true, false, true>)
-                                       : (shared ? norm_bwd_kernel<T, 1, l(), maxt(), false, true, true> : norm_bwd_kernel<T, 1, l(), maxt(), false, false, true>);
+                if constexpr (maxt() < 1024) {
+                    auto kernel = bias ? (shared ? norm_bwd_kernel<T, vpt(), l(), maxt(), true, true, true> : norm_bwd_kernel<T, vpt(), l(), maxt(), true, false, true>)
+                                       : (shared ? norm_bwd_kernel<T, vpt(), l(), maxt(), false, true, true> : norm_bwd_kernel<T, vpt(), l(), maxt(), false, false, true>);
                     e = launch(kernel, grid, dim3(l() ? 256 : row_threads(a.C)), 0, s, a, pc, gate);
                 }
             });
