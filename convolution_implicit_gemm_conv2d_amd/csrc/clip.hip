@@ -24,7 +24,6 @@
 #include "kernels.hpp"
 
 #include <algorithm>
-#include <vector>
 
 namespace convmi {
 namespace {
@@ -254,10 +253,9 @@ hipError_t clip(const void* const* src, void* const* dst, const size_t* counts, 
     const ArmedEvents armed = armed_events();
     armed_events() = ArmedEvents{armed.start, nullptr};
     hipError_t e = hipSuccess;
-    std::vector<int> first;  // tensor of each launch
-    int parts = 0, i = 0;
+    int parts = 0, i = 0, launches = 0;
     do {
-        first.push_back(i);
+        ++launches;
         i = fill(i);
         const dim3 g = grid();
         e = launch(clip_norm_kernel<N>, g, dim3(kThreads), 0, s, t, part + parts);
@@ -271,8 +269,11 @@ hipError_t clip(const void* const* src, void* const* dst, const size_t* counts, 
         armed_events() = ArmedEvents{nullptr, nullptr};
         return e;
     }
-    for (size_t l = first.size(); e == hipSuccess && l-- > 0;) {
-        if (first.size() > 1) fill(first[l]);  // a single launch's table is still there
+    for (int l = launches; e == hipSuccess && l-- > 0;) {
+        if (launches > 1) {  // a single launch's table is still there
+            i = 0;
+            for (int before = 0; before <= l; ++before) i = fill(i);
+        }
         if (l == 0) armed_events() = ArmedEvents{nullptr, armed.stop};
         e = launch(scale, grid(), dim3(kThreads), 0, s, t, part, parts, max_norm, eps, l == 0 ? norm : nullptr);
     }
