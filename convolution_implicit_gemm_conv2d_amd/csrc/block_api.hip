@@ -137,7 +137,7 @@ int conv_block_norm_bwd_workspace_size(long long rows, int C, long long gate_row
     if (int rc = check_sizes(op, rows, C, "C")) return rc;
     if (gate_rows < 0 || (gate_rows > 0 && rows % gate_rows != 0))
         return fail(CONV_ERR_INVALID_ARG, "%s: gate_rows must divide rows (got %lld for %lld)", op, gate_rows, rows);
-    *bytes = convmi::norm_bwd_workspace(rows, gate_rows, C, gate_rows > 0);
+    *bytes = convmi::norm_bwd_workspace(rows, C);
     return CONV_OK;
 }
 
@@ -166,7 +166,7 @@ int conv_block_norm_bwd(const void* dy, const void* da, const void* x, const voi
     if (((dpost_w || dpost_b) && post == CONV_NORM_NONE) || ((dpre_w || dpre_b) && pre == CONV_NORM_NONE) ||
         (dpost_b && post != CONV_NORM_LAYER) || (dpre_b && pre != CONV_NORM_LAYER))
         return fail(CONV_ERR_INVALID_ARG, "%s: a weight gradient needs its norm, a bias gradient its layer norm", op);
-    const size_t need = convmi::norm_bwd_workspace(rows, k.gate_rows, C, gate != nullptr);
+    const size_t need = convmi::norm_bwd_workspace(rows, C);
     if (int rc = check_workspace(op, workspace, workspace_bytes, need)) return rc;
     return launched(convmi::launch_norm_bwd(k, dtype, static_cast<hipStream_t>(stream)), op);
 }

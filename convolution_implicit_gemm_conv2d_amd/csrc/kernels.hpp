@@ -125,7 +125,7 @@ struct NormArgs {
 };
 hipError_t launch_norm_fwd(const NormArgs& a, int dtype, hipStream_t s);
 hipError_t launch_norm_bwd(const NormArgs& a, int dtype, hipStream_t s);
-size_t norm_bwd_workspace(int64_t rows, int64_t gate_rows, int C, int has_gate);
+size_t norm_bwd_workspace(int64_t rows, int C);
 
 // Gated feed-forward layer (see conv_gated_fwd / conv_gated_bwd).
 struct GatedArgs {

@@ -20,7 +20,7 @@
 // squared differences, both in fp32).  A lane holds 8 consecutive channels of
 // each of its vectors; rows of up to 512 channels share a wave with others (8,
 // 16, 32 or 64 lanes each), longer ones take a workgroup.
-// Parameters stay in registers over a workgroup's rows, and a row's loads go
+// Parameters stay in registers or LDS over a workgroup's rows, and a row's loads go
 // out before the row before it is worked on.
 //
 // A row whose length is no multiple of 8 ends in a vector that starts early
@@ -38,6 +38,8 @@
 #include "kernels.hpp"
 
 #include <algorithm>
+#include <atomic>
+#include <limits>
 #include <type_traits>
 
 namespace convmi {
@@ -220,17 +222,24 @@ __device__ __forceinline__ void load_param(const void* p, const Part<VPT>& part,
         if (p) v[i].load(rows_from<T>(p, 0), part.template off<T>(i, 0));
     }
 }
-// A parameter's values for a lane's channels: kept in registers over the rows
-// with one vector a lane, read again for each row with two.
-template <typename T, int VPT>
+// A parameter's values for a lane's channels: kept over the rows with one
+// vector a lane, in registers or (SHELF, bf16) in the lane's own 16 bytes of
+// LDS; read again for each row with two.
+template <typename T, int VPT, bool SHELF = false>
 struct Param {
-    static constexpr bool kKept = VPT == 1;
+    static constexpr bool kKept = VPT == 1 && !SHELF;
     Raw<T> raw[kKept ? VPT : 1];
     const void* p;
     float other;
-    __device__ __forceinline__ Param(const void* from, const Part<VPT>& part, float fill) : p(from), other(fill)
+    uint4* shelf;
+    __device__ __forceinline__ Param(const void* from, const Part<VPT>& part, float fill, uint4* own = nullptr) : p(from), other(fill), shelf(own)
     {
         if constexpr (kKept) load_param(p, part, other, raw);
+        if constexpr (SHELF) {
+            Raw<T> now[VPT];
+            load_param(p, part, other, now);
+            *shelf = now[0].u[0];
+        }
     }
     __device__ __forceinline__ void stay()
     {
@@ -238,7 +247,11 @@ struct Param {
     }
     __device__ __forceinline__ void get(const Part<VPT>& part, Row<VPT>& v) const
     {
-        if constexpr (kKept) {
+        if constexpr (SHELF) {
+            Raw<T> now;
+            now.u[0] = *shelf;
+            now.get(v[0]);
+        } else if constexpr (kKept) {
             raw[0].get(v[0]);
         } else {
             Raw<T> now[VPT];
@@ -382,6 +395,11 @@ __global__ __launch_bounds__(MAXT, 4) void norm_fwd_kernel(NormArgs k, NormGrid 
     }
 }
 
+// Threads of the workgroup that takes a row of more than 512 channels, and of
+// the gradient's for any.
+int row_threads(int C) { return C <= 4096 ? (C + 511) / 512 * 64 : (C + 1023) / 1024 * 64; }
+int bwd_threads(int C) { return C <= 512 ? 256 : row_threads(C); }
+
 // The pieces of the rows that the gradient's workgroups take.  A shared gate
 // row's group is cut into `split` pieces, or (split 1) a piece is `groups`
 // whole groups; without a shared gate the rows are one group.
@@ -393,17 +411,25 @@ struct Pieces {
     int count;
 };
 bool sums_apart(int C);
-Pieces make_pieces(int64_t rows, int64_t gate_rows, int C, bool has_gate)
+// Pieces wanted where the device holds `hold` workgroups at once: one each, so
+// that all end together; fewer where a piece would have too few rows to pay for
+// its partial sums, four a CU (or sixteen waves) at most.  Forward and gradient,
+// 1024 pieces against as many as are held: 16384 x 4096 bf16 rms norms 405 and
+// 388 us, layer norms 490 and 463; 2000 x 3001 fp32 88 and 63; but 9000 x 1500
+// bf16 layer norms, of which four workgroups a CU are held, 102 with 1024, 119
+// with 512.
+int64_t want_pieces(int64_t rows, int C, int64_t hold)
+{
+    if (sums_apart(C)) return std::max<int64_t>(1, std::min<int64_t>(std::max(1, 1024 / ((C + 2047) / 2048)), rows / 4));
+    const int64_t cus = device_cu_count(), most = std::min<int64_t>(4 * cus, cus * 1024 / bwd_threads(C));
+    return std::max<int64_t>(1, std::min(std::min(hold, most), rows / (C <= 512 ? 8 : 2)));
+}
+Pieces make_pieces(int64_t rows, int64_t gate_rows, bool has_gate, int64_t want)
 {
     Pieces p{};
     const bool shared = has_gate && gate_rows > 1;
     p.group = shared ? gate_rows : std::max<int64_t>(rows, 1);
     const int64_t groups = rows / p.group;
-    // As many workgroups as the device holds at once (four a CU for rows of a
-    // wave, two for longer ones); fewer where a piece would have too few rows
-    // to pay for its partial sums.
-    const int64_t want = sums_apart(C) ? std::max<int64_t>(1, std::min<int64_t>(std::max(1, 1024 / ((C + 2047) / 2048)), rows / 4))
-                                       : std::max<int64_t>(1, std::min<int64_t>(C <= 512 ? 1024 : std::max(512, std::min(1024, 8388608 / C / 2)), rows / (C <= 512 ? 8 : 2)));
     if (groups <= want) {
         p.groups = 1;
         const int64_t split = std::min<int64_t>(std::max<int64_t>(1, want / std::max<int64_t>(groups, 1)), p.group);
@@ -420,17 +446,22 @@ Pieces make_pieces(int64_t rows, int64_t gate_rows, int C, bool has_gate)
     return p;
 }
 
-// Waves of a SIMD: four where the registers hold a row of bf16 (a few spill),
-// two where more sums, fp32 rows or a second vector a lane would spill
-// hundreds.  16384 x 4096 bf16: 290 us with four, 310 with two; 1239 x 1001
-// fp32 layer norms with a shared gate: 43 us with four, 20 with two.
+// Waves of a SIMD: four where the registers hold a row of bf16, its parameters
+// and the gate's slope being in LDS then (its lane's own places: no barrier);
+// two where the biases' sums, fp32 rows or a second vector a lane would spill.
+// 16384 x 4096 bf16, gradient: 240 us with the shelf; 290 with the parameters
+// in registers, where 56 spills made 300 MB of the 1.4 GB; 310 with two waves.
+// 8192 x 2048 with a shared gate, forward and gradient: 81 us with four waves,
+// 92 with two.
 template <typename T, int VPT, int L, bool MORE>
-constexpr int bwd_waves() { return sizeof(T) == 2 && VPT == 1 && !MORE && !L ? 4 : 2; }
+constexpr bool bwd_shelf() { return sizeof(T) == 2 && VPT == 1 && !MORE && !L; }
+template <typename T, int VPT, int L, bool MORE>
+constexpr int bwd_waves() { return bwd_shelf<T, VPT, L, MORE>() ? 4 : 2; }
 // BIAS: with the sums of a layer norm's biases.  SHARED: a gate row serves
 // several rows.  Without SUMS, for rows whose sums do not fit in the registers
 // beside them: the rows alone, and their statistics.
 template <typename T, int VPT, int L, int MAXT, bool BIAS, bool SHARED, bool SUMS>
-__global__ __launch_bounds__(MAXT, (MAXT > 512 ? 4 : bwd_waves<T, VPT, L, BIAS || SHARED>())) void norm_bwd_kernel(NormArgs k, Pieces pc, FastDiv gate_rows)
+__global__ __launch_bounds__(MAXT, (MAXT > 512 ? 4 : bwd_waves<T, VPT, L, BIAS>())) void norm_bwd_kernel(NormArgs k, Pieces pc, FastDiv gate_rows)
 {
     __shared__ __align__(16) float slots[2][2][kMaxWaves];
     __shared__ float joined[L ? 4 : 1][L ? 64 * VPT * kVec : 1];
@@ -454,7 +485,12 @@ __global__ __launch_bounds__(MAXT, (MAXT > 512 ? 4 : bwd_waves<T, VPT, L, BIAS |
         param_off[i] = part.template off<T>(i, 0);
         sum_off[i] = part.template off<float>(i, 0);
     }
-    Param<T, VPT> post_w(k.post_w, part, 1.f), post_b(k.post_b, part, 0.f), pre_w(k.pre_w, part, 1.f), s(k.s, part, 1.f);
+    constexpr bool kShelf = bwd_shelf<T, VPT, L, BIAS>();
+    __shared__ uint4 shelf[kShelf ? 4 : 1][kShelf ? MAXT : 1];
+    const int own = kShelf ? threadIdx.x : 0;
+    Param<T, VPT, kShelf> post_w(k.post_w, part, 1.f, &shelf[0][own]), post_b(k.post_b, part, 0.f, &shelf[kShelf ? 1 : 0][own]),
+        pre_w(k.pre_w, part, 1.f, &shelf[kShelf ? 2 : 0][own]), s(k.s, part, 1.f, &shelf[kShelf ? 3 : 0][own]);
+    __shared__ float4 slopes[2][kShelf ? MAXT : 1];  // a lane's act'(z)
     constexpr bool kAhead = VPT == 1;  // a row's loads go out before the row before it is worked on
 
     // In the order of the partial rows; for a shared gate [kSumScale] is the
@@ -529,6 +565,10 @@ __global__ __launch_bounds__(MAXT, (MAXT > 512 ? 4 : bwd_waves<T, VPT, L, BIAS |
                     zd[i][e] = p.d;
                 }
             });
+            if constexpr (kShelf) {
+                slopes[0][own] = make_float4(zd[0][0], zd[0][1], zd[0][2], zd[0][3]);
+                slopes[1][own] = make_float4(zd[0][4], zd[0][5], zd[0][6], zd[0][7]);
+            }
         };
         if (SHARED) {
             load_row(rows_from<T>(k.z, r0 / pc.group * k.C), param_off, zr);
@@ -594,7 +634,13 @@ __global__ __launch_bounds__(MAXT, (MAXT > 512 ? 4 : bwd_waves<T, VPT, L, BIAS |
             s.get(part, g);
             if constexpr (SUMS) CONVMI_EACH(i, e) sum[kSumScale][i][e] += SHARED ? v[i][e] : v[i][e] * zv[i][e];
             if (each && k.dz && (SUMS || k.gate_rows == 1)) {
-                CONVMI_EACH(i, e) v[i][e] *= g[i][e] * zd[i][e];
+                if constexpr (kShelf) {
+                    const float4 lo = slopes[0][own], hi = slopes[1][own];
+                    const float slope[kVec] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                    CONVMI_EACH(i, e) v[i][e] *= g[i][e] * slope[e];
+                } else {
+                    CONVMI_EACH(i, e) v[i][e] *= g[i][e] * zd[i][e];
+                }
                 store_row<T>(rows_from<T>(k.dz, r * k.C), off, v);
             }
             CONVMI_EACH(i, e)
@@ -880,7 +926,6 @@ void with_shape(int C, F f)
     else if (n <= 1024) f(N2{}, N0{}, std::integral_constant<int, 512>{});
     else f(N2{}, N0{}, std::integral_constant<int, 1024>{});
 }
-int row_threads(int C) { return C <= 4096 ? (C + 511) / 512 * 64 : (C + 1023) / 1024 * 64; }
 
 template <typename T>
 hipError_t fwd(const NormArgs& a, hipStream_t s)
@@ -905,14 +950,42 @@ hipError_t fwd(const NormArgs& a, hipStream_t s)
     return e;
 }
 
+// Workgroups of a kernel that the device holds at once.
+template <auto KERNEL>
+int64_t held(int threads)
+{
+    static std::atomic<int> known[kMaxWaves + 1];
+    std::atomic<int>& at = known[threads / 64];
+    int n = at.load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, reinterpret_cast<const void*>(KERNEL), threads, 0) != hipSuccess || n < 1) n = 1;
+        at.store(n, std::memory_order_relaxed);
+    }
+    return static_cast<int64_t>(n) * device_cu_count();
+}
+
 template <typename T>
 hipError_t bwd(const NormArgs& given, hipStream_t s)
 {
-    const Pieces pc = make_pieces(given.rows, given.gate_rows, given.C, given.z != nullptr);
     NormArgs a = given;
-    a.stats = reinterpret_cast<RowStats*>(a.part + static_cast<int64_t>(pc.count) * kSums * a.C);
     const bool shared = a.z && a.gate_rows > 1;
     const bool bias = a.dpre_b || a.dpost_b;
+    typedef void (*Kernel)(NormArgs, Pieces, FastDiv);
+    Kernel kernel = nullptr;  // rows and sums in one
+    int64_t hold = 0;
+    if (!sums_apart(a.C))
+        with_shape(a.C, [&](auto vpt, auto l, auto maxt) {
+            if constexpr (maxt() < 1024) {
+                auto take = [&](auto b, auto sh) {
+                    kernel = norm_bwd_kernel<T, vpt(), l(), maxt(), b(), sh(), true>;
+                    hold = held<norm_bwd_kernel<T, vpt(), l(), maxt(), b(), sh(), true>>(bwd_threads(a.C));
+                };
+                if (bias) shared ? take(std::true_type{}, std::true_type{}) : take(std::true_type{}, std::false_type{});
+                else shared ? take(std::false_type{}, std::true_type{}) : take(std::false_type{}, std::false_type{});
+            }
+        });
+    const Pieces pc = make_pieces(a.rows, a.gate_rows, a.z != nullptr, want_pieces(a.rows, a.C, hold));
+    a.stats = reinterpret_cast<RowStats*>(a.part + static_cast<int64_t>(pc.count) * kSums * a.C);
     const ArmedEvents armed = armed_events();
     armed_events() = ArmedEvents{armed.start, nullptr};
     hipError_t e = hipSuccess;
@@ -931,13 +1004,7 @@ hipError_t bwd(const NormArgs& given, hipStream_t s)
             const bool any = a.dpre_w || a.dpost_w || a.ds || a.dpre_b || a.dpost_b || (shared && a.dz);
             if (any) e = launch(v == 1 ? norm_columns_kernel<T, 1> : norm_columns_kernel<T, kVec>, dim3((a.C + 256 * v - 1) / (256 * v), pc.count), dim3(256), 0, s, a, pc);
         } else {
-            with_shape(a.C, [&](auto vpt, auto l, auto maxt) {
-                if constexpr (maxt() < 1024) {
-                    auto kernel = bias ? (shared ? norm_bwd_kernel<T, vpt(), l(), maxt(), true, true, true> : norm_bwd_kernel<T, vpt(), l(), maxt(), true, false, true>)
-                                       : (shared ? norm_bwd_kernel<T, vpt(), l(), maxt(), false, true, true> : norm_bwd_kernel<T, vpt(), l(), maxt(), false, false, true>);
-                    e = launch(kernel, grid, dim3(l() ? 256 : row_threads(a.C)), 0, s, a, pc, gate);
-                }
-            });
+            e = launch(kernel, grid, dim3(bwd_threads(a.C)), 0, s, a, pc, gate);
         }
     }
     armed_events() = ArmedEvents{nullptr, nullptr};
@@ -967,10 +1034,12 @@ hipError_t launch_norm_fwd(const NormArgs& a, int dtype, hipStream_t s)
     return dtype ? fwd<bf16_t>(a, s) : fwd<float>(a, s);
 }
 
-size_t norm_bwd_workspace(int64_t rows, int64_t gate_rows, int C, int has_gate)
+size_t norm_bwd_workspace(int64_t rows, int C)
 {
-    const Pieces pc = make_pieces(rows, gate_rows, C, has_gate != 0);
-    return static_cast<size_t>(pc.count) * kSums * C * sizeof(float) + (sums_apart(C) ? static_cast<size_t>(rows) * sizeof(RowStats) : 0);
+    if (rows == 0) return 0;
+    // for as many pieces as any form of the kernel may have
+    const int64_t pieces = want_pieces(rows, C, std::numeric_limits<int64_t>::max());
+    return static_cast<size_t>(pieces) * kSums * C * sizeof(float) + (sums_apart(C) ? static_cast<size_t>(rows) * sizeof(RowStats) : 0);
 }
 
 hipError_t launch_norm_bwd(const NormArgs& a, int dtype, hipStream_t s)
