@@ -903,7 +903,7 @@ template <>
 struct Tiles<float> {
     typedef Shape<float, 2, 2, 1, 2, 32, 2> Small;  // 64 x 128
     typedef Small Wide, Big;
-    typedef Small Thin;  // none: 64 x 64 with a ring of four took 21 us where 64 x 128 took 15 (1001 rows, 190 -> 2 x 517)
+    typedef Shape<float, 4, 1, 1, 2, 32, 2> Thin;   // 128 x 64
 };
 
 bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -936,6 +936,9 @@ hipError_t run(Product<typename S::T>& k, int64_t p, int64_t q, int pieces, hipS
 // reach 1150, have half the loads and LDS reads for a product, and nothing
 // beside their epilogue; 128 x 256 1050, 128 x 128 750 (all bf16); fp32's
 // instructions leave time for every load, 64 x 128 reach 105, 128 x 256 no more.
+// fp32 has tiles of 64 x 128 and 128 x 64 (1 to 2 % slower), and takes those
+// that cover the output with fewer, if by 3 %: 1001 rows, 190 -> 2 x 517, training
+// step: 61 us, 69 with 64 x 128 alone; 20000 rows, 64 -> 2 x 256: 95 and 104.
 //
 // The forward product's sum is not cut into pieces.  Where its small tiles are
 // fewer than the CUs it is a stream over the weights, bound by the loads in
@@ -953,12 +956,22 @@ double rounds_us(int64_t n, int64_t K, double rate, double epilogue)
     const int64_t places = S::kPerCu * static_cast<int64_t>(device_cu_count());
     return static_cast<double>((n + places - 1) / places) * tile_us<S>(K, rate, epilogue);
 }
+// Calls f with the tile's shape.
+template <typename T, typename F>
+auto with_tile(Tile t, F f)
+{
+    if (t == Tile::kWide) return f(typename Tiles<T>::Wide{});
+    if (t == Tile::kBig) return f(typename Tiles<T>::Big{});
+    if (t == Tile::kThin) return f(typename Tiles<T>::Thin{});
+    return f(typename Tiles<T>::Small{});
+}
 // The time of `pieces` products over K values each, by tile.
 template <typename T>
 double product_us(Tile t, int64_t p, int64_t q, int64_t K, int pieces)
 {
     typedef Tiles<T> X;
-    if constexpr (sizeof(T) == 4) return rounds_us<typename X::Small>(tiles(p, X::Small::BM) * tiles(q, X::Small::BN) * pieces, K, 105, 1);
+    if constexpr (sizeof(T) == 4)
+        return with_tile<T>(t, [&](auto shape) { return rounds_us<decltype(shape)>(tiles(p, shape.BM) * tiles(q, shape.BN) * pieces, K, 105, 1); });
     if (t == Tile::kWide) return rounds_us<typename X::Wide>(tiles(p, X::Wide::BM) * tiles(q, X::Wide::BN) * pieces, K, 1150, 10);
     if (t == Tile::kBig) return rounds_us<typename X::Big>(tiles(p, X::Big::BM) * tiles(q, X::Big::BN) * pieces, K, 1050, 4);
     return rounds_us<typename X::Small>(tiles(p, X::Small::BM) * tiles(q, X::Small::BN) * pieces, K, 750, 2);
@@ -966,7 +979,11 @@ double product_us(Tile t, int64_t p, int64_t q, int64_t K, int pieces)
 template <typename T>
 Tile pick(int64_t p, int64_t q, int64_t K, int pieces = 1)
 {
-    if (sizeof(T) == 4) return Tile::kSmall;
+    typedef Tiles<T> X;
+    if (sizeof(T) == 4) {
+        const int64_t thin = tiles(p, X::Thin::BM) * tiles(q, X::Thin::BN), small = tiles(p, X::Small::BM) * tiles(q, X::Small::BN);
+        return 33 * thin < 32 * small ? Tile::kThin : Tile::kSmall;
+    }
     Tile best = Tile::kSmall;
     for (Tile t : {Tile::kBig, Tile::kWide})
         if (product_us<T>(t, p, q, K, pieces) < product_us<T>(best, p, q, K, pieces)) best = t;
@@ -979,15 +996,6 @@ Tile pick_gated(const GatedArgs& a)
     const int64_t q = 2 * static_cast<int64_t>(a.F);
     if (sizeof(T) == 2 && tiles(a.rows, Small::BM) * tiles(q, Small::BN) < device_cu_count()) return Tile::kThin;
     return pick<T>(a.rows, q, a.C);
-}
-// Calls f with the tile's shape.
-template <typename T, typename F>
-auto with_tile(Tile t, F f)
-{
-    if (t == Tile::kWide) return f(typename Tiles<T>::Wide{});
-    if (t == Tile::kBig) return f(typename Tiles<T>::Big{});
-    if (t == Tile::kThin) return f(typename Tiles<T>::Thin{});
-    return f(typename Tiles<T>::Small{});
 }
 // Partial rows of the column sums of `rows` rows: one for each wave's rows.
 template <typename T>
@@ -1015,7 +1023,7 @@ Split split(int64_t p, int64_t q, int64_t K, int64_t least)
         const int pieces = static_cast<int>((K + per - 1) / per);
         const double sums = 3 + 8.0 * pieces * p * q / 3.5e6;
         for (Tile t : {Tile::kSmall, Tile::kBig, Tile::kWide}) {
-            if (sizeof(T) == 4 && t != Tile::kSmall) continue;
+            if (sizeof(T) == 4) t = pick<T>(p, q, per);
             const double us = product_us<T>(t, p, q, per, pieces) + sums;
             if (us < time) time = us, best = Split{per, pieces, t};
         }
@@ -1029,7 +1037,7 @@ hipError_t run_tiles(Product<T>& k, int64_t p, int64_t q, int pieces, Tile t, bo
     typedef Tiles<T> X;
     if constexpr (sizeof(T) == 2)
         if (t == Tile::kWide && fast) return run<typename X::Wide, MODE, true>(k, p, q, pieces, s);
-    if constexpr (sizeof(T) == 2 && (MODE == kFwd || MODE == kAgain))
+    if constexpr (sizeof(T) == 4 || MODE == kFwd || MODE == kAgain)
         if (t == Tile::kThin) return fast ? run<typename X::Thin, MODE, true>(k, p, q, pieces, s) : run<typename X::Thin, MODE, false>(k, p, q, pieces, s);
     if constexpr (sizeof(T) == 2)
         if (t != Tile::kSmall) return fast ? run<typename X::Big, MODE, true>(k, p, q, pieces, s) : run<typename X::Big, MODE, false>(k, p, q, pieces, s);
