@@ -938,7 +938,7 @@ hipError_t run(Product<typename S::T>& k, int64_t p, int64_t q, int pieces, hipS
 // instructions leave time for every load, 64 x 128 reach 105, 128 x 256 no more.
 // fp32 has tiles of 64 x 128 and 128 x 64 (1 to 2 % slower), and takes those
 // that cover the output with fewer, if by 3 %: 1001 rows, 190 -> 2 x 517, training
-// step: 61 us, 69 with 64 x 128 alone; 20000 rows, 64 -> 2 x 256: 95 and 104.
+// step: 61 us, 69 with 64 x 128 alone; 20000 rows, 64 -> 2 x 256: 93 and 103.
 //
 // The forward product's sum is not cut into pieces.  Where its small tiles are
 // fewer than the CUs it is a stream over the weights, bound by the loads in
