@@ -36,6 +36,7 @@
 // part of one (and the second kernel adds the group's parts).
 #include "act.hpp"
 #include "kernels.hpp"
+#include "row_walk.hpp"
 
 #include <algorithm>
 #include <atomic>
@@ -333,23 +334,22 @@ __global__ __launch_bounds__(MAXT, 4) void norm_fwd_kernel(NormArgs k, NormGrid 
     constexpr int R = L ? 64 / L : 1;
     const int sub = L ? (threadIdx.x & 63) / (L ? L : 64) : 0;
     const int wave = L ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
-    const int64_t first = (L ? static_cast<int64_t>(blockIdx.x) * 4 + wave : blockIdx.x) * R * grid.per;
-    const int64_t end = min(k.rows, first + R * grid.per);
+    const RowWalk walk(L ? static_cast<int64_t>(blockIdx.x) * 4 + wave : blockIdx.x, R, grid.per, k.rows);
     uint32_t off[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) off[i] = part.template off<T>(i, sub * static_cast<uint32_t>(k.C));
     Raw<T> xr[VPT], fr[VPT], zr[VPT];
     auto fetch = [&](int64_t r) __attribute__((always_inline)) {
-        if (sub >= end - r) return;
+        if (!walk.has(r, sub)) return;
         load_row(rows_from<T>(k.x, r * k.C), off, xr);
         if (k.f) load_row(rows_from<T>(k.f, r * k.C), off, fr);
         if (each) load_row(rows_from<T>(k.z, r * k.C), off, zr);
     };
-    if (kAhead) fetch(first);
+    if (kAhead) fetch(walk.first);
     Row<VPT> g;  // s act(z)
     s.get(part, g);
     int64_t gate_at = -1;
-    for (int64_t r = first; r < end; r += R) {  // rows r to r + R - 1
+    for (int64_t r = walk.first; walk.has(r, sub); r += R) {  // rows r to r + R - 1, as far as they exist
         Row<VPT> v, n, w, b;
         post_w.stay(), post_b.stay(), pre_w.stay(), pre_b.stay(), s.stay();
         if (!kAhead) fetch(r);
@@ -373,8 +373,7 @@ __global__ __launch_bounds__(MAXT, 4) void norm_fwd_kernel(NormArgs k, NormGrid 
                 with_act(k.act, [&](auto kind) __attribute__((always_inline)) { CONVMI_EACH(i, e) g[i][e] *= act_value<kind()>(w[i][e]); });
             }
         }
-        if (kAhead && r + R < end) fetch(r + R);
-        if (sub >= end - r) break;
+        if (kAhead) fetch(r + R);
         if (k.f) {
             if (k.post != kNormNone) {
                 normalise(k.post, part, inv_c, k.eps, rs, n);
