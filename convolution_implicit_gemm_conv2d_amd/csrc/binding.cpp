@@ -327,6 +327,9 @@ PyObject* norm_grad(PyObject*, PyObject* const* a, Py_ssize_t n)
         for (int i = 0; i < Norm::kInputs; ++i)
             if (k.in[i]) {
                 d[i] = like(*k.in[i]);
+                // To the C call a gate has rows / gate_rows rows: none, while
+                // an image's or a batch's gate may still be there.
+                if (i == 2 && k.rows == 0) d[i].zero_();
                 to[i] = d[i].data_ptr();
             }
         void* stream = address(a[15]);
