@@ -261,7 +261,9 @@ def gradient_norm(grads, stream=None):
 def clip_gradients(grads, max_norm, out=None, eps=1e-6, stream=None):
     """Scales a list of gradients by ``min(1, max_norm / (norm + eps))``, in
     place or into the tensors of ``out``, and returns the norm before it, a
-    float32 scalar on the device.  Nothing waits for the device."""
+    float32 scalar on the device.  Nothing waits for the device.  What is written
+    must not overlap another tensor of the call: a tensor twice in the list is
+    refused in place."""
     grads = list(grads)
     s = _current(grads[0], stream) if grads else 0
     if s is None:

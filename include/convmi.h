@@ -502,11 +502,12 @@ int conv_grad_norm(const void *const *grads, const size_t *counts,
 
 /*
  * Clipping by the global norm: c = min(1, max_norm / (norm + eps)) and
- * outs[i] = c * grads[i] (outs[i] may be grads[i]; it must not overlap
- * another gradient).  The norm before clipping goes to `norm` unless that is
+ * outs[i] = c * grads[i].  outs[i] may be grads[i]; it must not overlap
+ * another output, or a gradient otherwise (one tensor twice in place, say).
+ * The norm before clipping goes to `norm` unless that is
  * NULL; nothing is read back to the host.  A norm that is not finite gives c
  * by the same formula (0 or NaN).  max_norm >= 0, eps >= 0.
- * Errors as conv_grad_norm.
+ * Errors as conv_grad_norm, and CONV_ERR_INVALID_ARG for outputs that overlap.
  */
 int conv_grad_clip(const void *const *grads, void *const *outs,
                    const size_t *counts, const int *dtypes, int n,
