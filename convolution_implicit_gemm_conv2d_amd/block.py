@@ -11,6 +11,11 @@ A call works on the current stream of its tensors' device, or on ``stream``.
 With ``stream``, what the call allocates belongs to that stream; inputs made on
 another one must be ready (the caller orders the streams).
 
+Automatic differentiation records no call: results carry no graph, also where
+inputs require gradients (the ``_grad`` functions are the gradients).  A caller's
+tensor that a call writes (``out``, ``saved``, a list clipped in place) counts a
+new version, so a graph that had saved it refuses to run backwards.
+
 The checks of tensors, the allocations and the calls are native
 (``csrc/binding.cpp``): a small call costs its host time.
 """

@@ -96,6 +96,12 @@ struct Call {
 };
 
 void* at_of(const at::Tensor* t) { return t ? t->data_ptr() : nullptr; }
+// A caller's tensor that a call has written: automatic differentiation counts
+// its versions (an inference tensor has none).
+void wrote(const at::Tensor* t)
+{
+    if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
 at::Tensor like(const at::Tensor& t) { return at::empty(t.sizes(), t.options().memory_format(at::MemoryFormat::Contiguous)); }
 at::Tensor bytes_like(const at::Tensor& t, size_t n) { return at::empty({static_cast<int64_t>(n < 16 ? 16 : n)}, t.options().dtype(at::kByte)); }
 
@@ -216,7 +222,10 @@ PyObject* gated(PyObject*, PyObject* const* a, Py_ssize_t n)
                                  static_cast<float*>(at_of(g.saved)), need ? ws.data_ptr() : nullptr, need, g.rows, g.C, g.F, g.act,
                                  g.c.dtype, stream);
         });
-        return rc ? status(rc) : THPVariable_Wrap(h);
+        if (rc) return status(rc);
+        wrote(out);
+        wrote(g.saved);
+        return THPVariable_Wrap(h);
     });
 }
 
@@ -347,6 +356,7 @@ PyObject* norm_grad(PyObject*, PyObject* const* a, Py_ssize_t n)
 // --------------------------------------------------------------- lists --
 
 struct List {
+    std::vector<const at::Tensor*> tensors;
     std::vector<void*> at;
     std::vector<size_t> counts;
     std::vector<int> dtypes;
@@ -358,6 +368,7 @@ struct List {
         const Py_ssize_t n = PyList_GET_SIZE(o);
         if (n == 0) throw Refused("the list of gradients is empty");
         narrow(n, "the number of tensors");
+        tensors.reserve(n);
         at.reserve(n);
         counts.reserve(n);
         dtypes.reserve(n);
@@ -367,6 +378,7 @@ struct List {
             dtypes.push_back(Call::code(t));
             if (!t.is_cuda() || t.device() != first->device()) throw Refused("tensors passed to convmi must be on one GPU device");
             if (!t.is_contiguous()) throw Refused("tensors passed to convmi must be contiguous");
+            tensors.push_back(&t);
             at.push_back(t.data_ptr());
             counts.push_back(static_cast<size_t>(t.numel()));
         }
@@ -383,6 +395,7 @@ PyObject* clip(PyObject*, PyObject* const* a, Py_ssize_t n)
         const float max_norm = static_cast<float>(PyFloat_AsDouble(a[2])), eps = static_cast<float>(PyFloat_AsDouble(a[3]));
         if (PyErr_Occurred()) return nullptr;
         std::vector<void*> out;
+        std::vector<const at::Tensor*> written = g.tensors;
         if (!only_norm && a[1] != a[0]) {
             if (PyList_Check(a[1]) && PyList_GET_SIZE(a[1]) != PyList_GET_SIZE(a[0]))
                 throw Refused("out has " + std::to_string(PyList_GET_SIZE(a[1])) + " tensors for " + std::to_string(g.n()) + " gradients");
@@ -390,6 +403,7 @@ PyObject* clip(PyObject*, PyObject* const* a, Py_ssize_t n)
             if (o.counts != g.counts || o.dtypes != g.dtypes || o.first->device() != g.first->device())
                 throw Refused("the tensors of out must have the sizes, dtypes and device of the gradients");
             out = std::move(o.at);
+            written = std::move(o.tensors);
         }
         size_t need = 0;
         if (int rc = api.grad_workspace(g.n(), &need)) return status(rc);
@@ -401,7 +415,10 @@ PyObject* clip(PyObject*, PyObject* const* a, Py_ssize_t n)
                              : api.grad_clip(g.at.data(), out.empty() ? g.at.data() : out.data(), g.counts.data(), g.dtypes.data(), g.n(),
                                              max_norm, eps, to, ws.data_ptr(), ws.nbytes(), stream);
         });
-        return rc ? status(rc) : THPVariable_Wrap(v);
+        if (rc) return status(rc);
+        if (!only_norm)
+            for (const at::Tensor* t : written) wrote(t);
+        return THPVariable_Wrap(v);
     });
 }
 
