@@ -254,8 +254,8 @@ def block_norm_grad(dy, da, x, branch=None, gate=None, scale=None, post_weight=N
 
 
 def gradient_norm(grads, stream=None):
-    """The 2-norm over all elements of a non-empty list of tensors (float32 and
-    bfloat16 may be mixed), as a float32 scalar on their device."""
+    """The 2-norm over all elements of a non-empty list of dense tensors (float32
+    and bfloat16 may be mixed), as a float32 scalar on their device."""
     grads = list(grads)
     s = _current(grads[0], stream) if grads else 0
     if s is None:
@@ -268,7 +268,8 @@ def clip_gradients(grads, max_norm, out=None, eps=1e-6, stream=None):
     place or into the tensors of ``out``, and returns the norm before it, a
     float32 scalar on the device.  Nothing waits for the device.  What is written
     must not overlap another tensor of the call: a tensor twice in the list is
-    refused in place."""
+    refused in place.  Tensors are dense, in any order of dimensions (channels-last
+    ones, say); an output lies in memory as its gradient does."""
     grads = list(grads)
     s = _current(grads[0], stream) if grads else 0
     if s is None:

@@ -377,7 +377,8 @@ struct List {
             if (!first) first = &t;
             dtypes.push_back(Call::code(t));
             if (!t.is_cuda() || t.device() != first->device()) throw Refused("tensors passed to convmi must be on one GPU device");
-            if (!t.is_contiguous()) throw Refused("tensors passed to convmi must be contiguous");
+            // Any order of dimensions: each element counts for itself.
+            if (!t.is_non_overlapping_and_dense()) throw Refused("the tensors of a list must be dense");
             tensors.push_back(&t);
             at.push_back(t.data_ptr());
             counts.push_back(static_cast<size_t>(t.numel()));
@@ -402,6 +403,11 @@ PyObject* clip(PyObject*, PyObject* const* a, Py_ssize_t n)
             List o(a[1]);
             if (o.counts != g.counts || o.dtypes != g.dtypes || o.first->device() != g.first->device())
                 throw Refused("the tensors of out must have the sizes, dtypes and device of the gradients");
+            for (int i = 0; i < g.n(); ++i) {
+                const at::Tensor &from = *g.tensors[i], &to = *o.tensors[i];
+                if (!(from.is_contiguous() && to.is_contiguous()) && (from.sizes() != to.sizes() || from.strides() != to.strides()))
+                    throw Refused("the tensors of out must lie in memory as the gradients do");
+            }
             out = std::move(o.at);
             written = std::move(o.tensors);
         }
