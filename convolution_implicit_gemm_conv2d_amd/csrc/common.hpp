@@ -234,6 +234,25 @@ struct ArmedEvents {
 };
 ArmedEvents& armed_events();
 
+// The armed events over a call of several launches: its first one stamps the
+// start, its last one the stop.  A call that launches nothing leaves them armed.
+class CallEvents {
+public:
+    CallEvents() : left_(armed_events()) { armed_events() = ArmedEvents{nullptr, nullptr}; }
+    ~CallEvents() { armed_events() = any_ ? ArmedEvents{nullptr, nullptr} : left_; }
+    CallEvents(const CallEvents&) = delete;
+    CallEvents& operator=(const CallEvents&) = delete;
+    void next(bool last)  // before each launch
+    {
+        armed_events() = ArmedEvents{any_ ? nullptr : left_.start, last ? left_.stop : nullptr};
+        any_ = true;
+    }
+
+private:
+    ArmedEvents left_;
+    bool any_ = false;
+};
+
 // Host: launches `kernel` on stream `s`.  If events are armed, the launch goes
 // through hipExtLaunchKernel so that the runtime stamps the kernel's own start
 // and end into them (no extra packets on the stream), and the events are

@@ -1213,20 +1213,22 @@ hipError_t gated_bwd(const GatedArgs& a, hipStream_t s)
     float* sums = a.dbg || a.dbu ? reinterpret_cast<float*>(ws + p.d_bytes) : nullptr;
     float* x_part = p.x_pieces > 1 && a.dx ? reinterpret_cast<float*>(ws + p.d_bytes + p.sum_bytes) : nullptr;
     float* w_part = p.pieces > 1 ? reinterpret_cast<float*>(ws + p.d_bytes + p.sum_bytes + p.x_bytes) : nullptr;
-    const ArmedEvents armed = armed_events();
-    armed_events() = ArmedEvents{armed.start, nullptr};
+    // What comes after dg and du, to know the call's last launch.
+    const bool dx = a.dx && a.rows > 0, weights = a.dwg || a.dwu, added = (dx && x_part) || (weights && w_part) || sums;
+    CallEvents events;
     hipError_t e = hipSuccess;
     int summed = 0;
     Product<T> k = product<T>(a);
     k.Fp = p.Fp;
     const Padded<T> padded(a.rows, a.C, a.F, false);
     if (padded.ld) {
+        events.next(false);
         e = pad(k, padded.ld, ws + p.d_bytes + p.sum_bytes + p.x_bytes + p.w_bytes, s);
-        armed_events() = ArmedEvents{nullptr, nullptr};
         if (e != hipSuccess) return e;
     }
     const bool whole = padded.ld || a.C % kUnit == 0;  // rows are whole units
     if (a.rows > 0) {
+        events.next(!dx && !weights && !added);
         if (a.saved) {
             int64_t chunk;
             summed = gated_kept_chunks(a.rows, p.Fp, &chunk);
@@ -1245,35 +1247,33 @@ hipError_t gated_bwd(const GatedArgs& a, hipStream_t s)
                 e = run_tiles<kAgain>(k, a.rows, 2 * static_cast<int64_t>(p.Fp), 1, t, fast, s);  // the columns up to Fp too
             }
         }
-        armed_events() = ArmedEvents{nullptr, nullptr};
         if (e != hipSuccess) return e;
         k.d = d;
-        if (a.dx) {
+        if (dx) {
             k.out = static_cast<T*>(a.dx);
             k.part = x_part;
             k.per = p.x_per;
+            events.next(!weights && !added);
             e = run_tiles<kDx>(k, a.rows, a.C, p.x_pieces, static_cast<Tile>(p.x_tile),
                                whole && aligned(k.wg) && aligned(k.wu), s);
             if (e != hipSuccess) return e;
         }
     }
-    const bool weights = a.dwg || a.dwu, last = !x_part && !sums && (!weights || !w_part);
     if (weights) {
         k.d = d;
         k.out = static_cast<T*>(a.dwg);
         k.out2 = static_cast<T*>(a.dwu);
         k.part = w_part;
         k.per = p.per;
-        if (last) armed_events() = ArmedEvents{nullptr, armed.stop};
+        events.next(!added);
         const int64_t dp = 2 * static_cast<int64_t>(p.Fp);
         e = run_tiles<kDw>(k, dp, a.C, p.pieces, static_cast<Tile>(p.tile), whole && aligned(k.x), s);
-        armed_events() = ArmedEvents{nullptr, nullptr};
         if (e != hipSuccess) return e;
     }
-    if (last) return e;
+    if (!added) return e;
     SumArgs t{};
     const int64_t n = static_cast<int64_t>(a.F) * a.C, fp = p.Fp;
-    if (x_part && a.rows > 0) add_sum(t, x_part, a.rows * a.C, a.rows * a.C, p.x_pieces, a.dx);
+    if (dx && x_part) add_sum(t, x_part, a.rows * a.C, a.rows * a.C, p.x_pieces, a.dx);
     if (weights && w_part) {
         add_sum(t, w_part, 2 * n, n, p.pieces, a.dwg);
         add_sum(t, w_part + n, 2 * n, n, p.pieces, a.dwu);
@@ -1282,10 +1282,8 @@ hipError_t gated_bwd(const GatedArgs& a, hipStream_t s)
         add_sum(t, sums, 2 * fp, a.F, summed, a.dbg);
         add_sum(t, sums + fp, 2 * fp, a.F, summed, a.dbu);
     }
-    armed_events() = ArmedEvents{nullptr, armed.stop};
-    e = launch_sums(t, kType, s);
-    armed_events() = ArmedEvents{nullptr, nullptr};
-    return e;
+    events.next(true);
+    return launch_sums(t, kType, s);
 }
 
 }  // namespace
