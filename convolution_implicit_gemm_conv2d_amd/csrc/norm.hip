@@ -985,10 +985,20 @@ hipError_t bwd(const NormArgs& given, hipStream_t s)
         });
     const Pieces pc = make_pieces(a.rows, a.gate_rows, a.z != nullptr, want_pieces(a.rows, a.C, hold));
     a.stats = reinterpret_cast<RowStats*>(a.part + static_cast<int64_t>(pc.count) * kSums * a.C);
-    const ArmedEvents armed = armed_events();
-    armed_events() = ArmedEvents{armed.start, nullptr};
+    SumArgs sums{};
+    const int64_t pitch = static_cast<int64_t>(kSums) * a.C;
+    void* out[kSumGate] = {a.dpre_w, a.dpost_w, a.ds, a.dpre_b, a.dpost_b};
+    // whether columns are summed at all, and whether their pieces' sums are added
+    bool columns = shared && a.dz && a.rows > 0, added = columns && pc.split > 1;
+    if (added) add_sum(sums, a.part + static_cast<int64_t>(kSumGate) * a.C, pitch, a.C, pc.split, a.dz, static_cast<int>(a.rows / pc.group));
+    for (int q = 0; q < kSumGate; ++q) {
+        add_sum(sums, a.part + static_cast<int64_t>(q) * a.C, pitch, a.C, pc.count, out[q]);
+        if (out[q]) columns = added = true;
+    }
+    CallEvents events;
     hipError_t e = hipSuccess;
     if (pc.count > 0) {
+        events.next(sums_apart(a.C) ? !columns : !added);
         const dim3 grid(pc.count);
         const FastDiv gate = make_fastdiv(static_cast<uint32_t>(a.gate_rows));
         if (sums_apart(a.C)) {
@@ -997,33 +1007,19 @@ hipError_t bwd(const NormArgs& given, hipStream_t s)
                 e = launch(norm_bwd_long_kernel<T>, rows, dim3(kLongThreads), 0, s, a);
             else
                 e = launch(norm_bwd_kernel<T, 2, 0, 1024, false, false, false>, rows, dim3(row_threads(a.C)), 0, s, a, pc, gate);
-            armed_events() = ArmedEvents{nullptr, nullptr};
             if (e != hipSuccess) return e;
             const unsigned v = a.C < kVec ? 1 : kVec;
-            const bool any = a.dpre_w || a.dpost_w || a.ds || a.dpre_b || a.dpost_b || (shared && a.dz);
-            if (any) e = launch(v == 1 ? norm_columns_kernel<T, 1> : norm_columns_kernel<T, kVec>, dim3((a.C + 256 * v - 1) / (256 * v), pc.count), dim3(256), 0, s, a, pc);
+            if (columns) {
+                events.next(!added);
+                e = launch(v == 1 ? norm_columns_kernel<T, 1> : norm_columns_kernel<T, kVec>, dim3((a.C + 256 * v - 1) / (256 * v), pc.count), dim3(256), 0, s, a, pc);
+            }
         } else {
             e = launch(kernel, grid, dim3(bwd_threads(a.C)), 0, s, a, pc, gate);
         }
     }
-    armed_events() = ArmedEvents{nullptr, nullptr};
-    if (e != hipSuccess) return e;
-    SumArgs sums{};
-    const int64_t pitch = static_cast<int64_t>(kSums) * a.C;
-    void* out[kSumGate] = {a.dpre_w, a.dpost_w, a.ds, a.dpre_b, a.dpost_b};
-    bool any = false;
-    for (int q = 0; q < kSumGate; ++q) {
-        add_sum(sums, a.part + static_cast<int64_t>(q) * a.C, pitch, a.C, pc.count, out[q]);
-        any |= out[q] != nullptr;
-    }
-    if (shared && a.dz && pc.split > 1) {
-        add_sum(sums, a.part + static_cast<int64_t>(kSumGate) * a.C, pitch, a.C, pc.split, a.dz, static_cast<int>(a.rows / pc.group));
-        any = true;
-    }
-    armed_events() = ArmedEvents{nullptr, armed.stop};
-    if (any) e = launch_sums(sums, sizeof(T) == 2, s);
-    armed_events() = ArmedEvents{nullptr, nullptr};
-    return e;
+    if (e != hipSuccess || !added) return e;
+    events.next(true);
+    return launch_sums(sums, sizeof(T) == 2, s);
 }
 
 }  // namespace

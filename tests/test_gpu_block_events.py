@@ -47,6 +47,23 @@ def test_gated_gradient(rows, C, F, dtype):
         stamped(lambda: cm.conv_gated_bwd(dh, x, w, w, b, b, kept, dx, dwg, dwu, db, db if db is None else torch.empty_like(db), ws, need, rows, C, F, 2, code))
 
 
+@pytest.mark.parametrize("rows,C,dtype", [(0, 64, BF16), (12, 64, BF16), (12, 1001, F32), (12, 9000, BF16), (12, 5, F32)])
+def test_norm_gradient(rows, C, dtype):
+    x, f, dy, da, p = t(rows, C, dtype=dtype), t(rows, C, dtype=dtype), t(rows, C, dtype=dtype), t(rows, C, dtype=dtype), t(C, dtype=dtype)
+    code = cm.CONV_BF16 if dtype == BF16 else cm.CONV_F32
+    for gate_rows in (0, 1, 4, 12):
+        z = t(max(rows // gate_rows, 1), C, dtype=dtype) if gate_rows else None
+        ws = t(max(cm.conv_block_norm_bwd_workspace_size(rows, C, gate_rows), 16), dtype=torch.uint8)
+        for dx, dz, dw, db in itertools.product((None, t(rows, C, dtype=dtype)), (None, z), (None, t(C, dtype=dtype)), (None, t(C, dtype=dtype))):
+            if rows == 0 and dw is None and db is None:
+                continue  # nothing to launch
+            if dz is not None:
+                dz = t(*z.shape, dtype=dtype)
+            print(rows, C, dtype, gate_rows, [v is not None for v in (dx, dz, dw, db)], flush=True)
+            stamped(lambda: cm.conv_block_norm_bwd(dy, da, x, f, z, None, p, p, p, None, dx, None, dz, None, dw, db, None, None, ws,
+                                                   ws.numel(), rows, C, gate_rows or 1, 2, 2, 1, 1e-6, code))
+
+
 @pytest.mark.parametrize("n", [1, 129])
 def test_forward_and_lists(n):
     x, w = t(2100, 1031), t(520, 1031)  # copied to padded rows first
