@@ -92,8 +92,9 @@ __device__ __forceinline__ ActPair act_pair(float t)
         const Normal n = normal_f(t);
         return {__builtin_fmaxf(t, 0.f) - n.m, n.p + t * 0.39894228040143268f * n.e};
     } else if constexpr (K == kActGeluTanh) {
-        const float p = gelu_tanh_p(t);
-        return {t * p, p + t * p * (1.0f - p) * (2.0f * kTanhScale) * (1.0f + 3.0f * kTanhCube * t * t)};
+        // p (1 - p) is 0 from |t| = 11 on; there the square's overflow must not meet it.
+        const float p = gelu_tanh_p(t), z = __builtin_fminf(t * t, 1e4f);
+        return {t * p, p + t * p * (1.0f - p) * (2.0f * kTanhScale) * (1.0f + 3.0f * kTanhCube * z)};
     } else if constexpr (K == kActRelu) {
         return {t <= 0.f ? 0.f : t, t > 0.f ? 1.0f : 0.0f};
     } else if constexpr (K == kActTanh) {
