@@ -179,23 +179,11 @@ __device__ __forceinline__ void store16_any(void* p, uint4 v)
     *static_cast<uint32x4_any*>(p) = t;
 }
 
-// Sum over the 64 lanes of a wave, the same in every lane.  Row shifts leave
-// each 16-lane row's sum in its last lane, two broadcasts carry it across
-// the rows to lane 63; the order is fixed, so the result is too.
+// The value of another lane of the row of 16, by a DPP control; 0 where a lane has none.
 template <int CTRL, int ROWS>
 __device__ __forceinline__ float dpp_shift(float v)
 {
     return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xf, true));
-}
-__device__ __forceinline__ float wave_sum(float v)
-{
-    v += dpp_shift<0x111, 0xf>(v);
-    v += dpp_shift<0x112, 0xf>(v);
-    v += dpp_shift<0x114, 0xf>(v);
-    v += dpp_shift<0x118, 0xf>(v);
-    v += dpp_shift<0x142, 0xa>(v);
-    v += dpp_shift<0x143, 0xc>(v);
-    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 
 // Division by a runtime constant d >= 1 for dividends below 2^31, as a
