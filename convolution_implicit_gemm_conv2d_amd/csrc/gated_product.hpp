@@ -25,7 +25,8 @@
 // 1180 TFLOP/s on normal data at a clock near 2.0 GHz, 1820 on zeros), or for
 // short sums the epilogue's vector instructions (100352 rows, 256 -> 2 x 1024:
 // 175 us, 87 of them products), or for few rows the weights' stream (one row,
-// 2048 -> 2 x 8192: 12 us, 5.6 TB/s).
+// 2048 -> 2 x 8192: 15.2 us, 4.4 TB/s, with weights that no cache holds; 11.8
+// where the memory-side cache has them from the call before).
 //
 // dg and du are rounded to T once, as operands of the products that follow
 // (their column sums, the bias gradients, are taken before); sums are fp32.

@@ -355,7 +355,8 @@ int conv_arm_launch_events(void *start, void *stop);
  * execution and error reporting are as above; `rows` may be 0 (nothing is
  * read, parameter gradients become zero).  Tensors are dense; pointers need
  * the alignment of their elements only, and 16-byte alignment with row
- * lengths that are multiples of 8 (bf16) is the fast case.  Accumulation,
+ * lengths that are multiples of 8 (bf16) is the fast case.  An output must not
+ * overlap an input or another output (but see conv_grad_clip).  Accumulation,
  * statistics and activations are in fp32 (the squares of conv_grad_norm in
  * fp64); each output is rounded once.
  */
