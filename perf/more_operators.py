@@ -1,0 +1,624 @@
+"""Cases that measure the operators of a selective block and its training: the
+short causal convolution, the selective state space scan, and the AdamW step
+over many tensors.
+
+``run`` computes one pass: with ``own`` false in elementary torch operations
+in 32 bits, with ``own`` true through the package.  ``exact`` gives the same
+outputs in 64 bits from the definitions.
+"""
+from __future__ import annotations
+
+import math
+import random
+
+import torch
+
+own = False
+
+BF16, F32 = "bf16", "fp32"
+TYPES = {BF16: torch.bfloat16, F32: torch.float32}
+BETAS, ADAM_EPS, DECAY, RATE, STEP, CLIP_EPS = (0.9, 0.95), 1e-8, 0.1, 3e-4, 20, 1e-6
+BLOCK = 128  # elements that share a scale of an 8-bit state
+# What a list of parameters is made of: types of the parameter, its gradient, and its copy for the forward pass.
+KINDS = {"fp32": ((F32, F32, None),), "bf16": ((BF16, BF16, None),), "master": ((F32, BF16, BF16),),
+         "mixed": ((BF16, BF16, None), (F32, F32, None), (F32, BF16, BF16))}
+
+
+def listed():
+    return [
+        # Four prompts through the short convolution, x one half of a projection.
+        dict(name="conv_prompt", op="conv", form="prompt", rows=4 * 4096, seqs=4, packed=False, channels=4096, taps=4,
+             dtype=BF16, act="silu", initial=False),
+        # Its training step over packed sequences of very different lengths, odd sizes, states from before.
+        dict(name="conv_train_packed", op="conv", form="train", rows=20011, seqs=13, packed=True, channels=1544, taps=4,
+             dtype=BF16, act="silu", initial=True),
+        # A token each of 64 running requests.
+        dict(name="conv_tokens", op="conv", form="token", rows=64, seqs=96, packed=False, channels=4096, taps=4,
+             dtype=BF16, act="silu", initial=True),
+        # The same prompts through the scan, gated.
+        dict(name="scan_prompt", op="scan", form="prompt", rows=4 * 4096, seqs=4, packed=False, channels=4096, state=16,
+             groups=1, dtype=BF16, gate=True, initial=False),
+        # One long prompt of a narrow model: few channels, many rows, the request goes on from a state.
+        dict(name="scan_long", op="scan", form="prompt", rows=16384, seqs=1, packed=False, channels=1024, state=16,
+             groups=1, dtype=BF16, gate=True, initial=True),
+        # A training step of a middle model.
+        dict(name="scan_train", op="scan", form="train", rows=8 * 2048, seqs=8, packed=False, channels=2048, state=16,
+             groups=1, dtype=BF16, gate=True, initial=False),
+        # An fp32 training step over packed sequences, two groups, no size a multiple of a tile.
+        dict(name="scan_train_fp32", op="scan", form="train", rows=3001, seqs=9, packed=True, channels=1000, state=24,
+             groups=2, dtype=F32, gate=True, initial=True),
+        # A token each of 64 running requests.
+        dict(name="scan_tokens", op="scan", form="token", rows=64, seqs=96, packed=False, channels=4096, state=16,
+             groups=1, dtype=BF16, gate=True, initial=True),
+        # One request's token: latency.
+        dict(name="scan_token", op="scan", form="token", rows=1, seqs=4, packed=False, channels=2048, state=16,
+             groups=1, dtype=BF16, gate=True, initial=True),
+        # The parameters of a few convolution layers: launches count.
+        dict(name="adamw_layers", op="adamw", tensors=12, total=700_001, spread=6.0, kind="fp32", bits=32, clip=False),
+        # A whole model with fp32 weights and states, clipped by a norm in hand.
+        dict(name="adamw_model", op="adamw", tensors=290, total=250_000_003, spread=9.0, kind="mixed", bits=32, clip=True),
+        # The same list with 8-bit states, which are read out afterwards as for a checkpoint.
+        dict(name="adamw_8bit", op="adamw", tensors=290, total=250_000_003, spread=9.0, kind="mixed", bits=8, clip=True),
+    ]
+
+
+def _log(rng, lo, hi):
+    return max(lo, min(hi, round(math.exp(rng.uniform(math.log(lo), math.log(hi))))))
+
+
+def draw(rng):
+    op = rng.choice(("conv", "conv", "scan", "scan", "scan", "adamw"))
+    if op == "adamw":
+        tensors = _log(rng, 1, 600)
+        return dict(op=op, tensors=tensors, total=max(tensors, _log(rng, 1000, 250_000_000)), spread=rng.uniform(1.0, 10.0),
+                    kind=rng.choice(tuple(KINDS)), bits=rng.choice((32, 8)), clip=rng.random() < 0.5)
+    form = rng.choice(("prompt", "train", "token"))
+    dtype = rng.choice((BF16, BF16, F32))
+    if form == "token":
+        rows, channels = _log(rng, 1, 512), _log(rng, 16, 8192)
+        seqs, packed = rows + _log(rng, 1, 64), False
+    else:
+        while True:
+            rows, channels = _log(rng, 1, 16384), _log(rng, 16, 8192)
+            if rows * channels <= 16384 * (4096 if op == "conv" or form == "prompt" else 2048):
+                break
+        seqs, packed = _log(rng, 1, min(rows, 64)), rng.random() < 0.6
+        if not packed:
+            rows = rows // seqs * seqs
+    if rng.random() < 0.6:
+        channels = -(-channels // 8) * 8
+    case = dict(op=op, form=form, rows=rows, seqs=seqs, packed=packed, channels=channels, dtype=dtype,
+                initial=form == "token" or rng.random() < 0.5)
+    if op == "conv":
+        return case | dict(taps=rng.choice((2, 3, 4, 4, 4, 6, 8)), act=rng.choice(("none", "silu")))
+    state = rng.choice((8, 16, 16, 16, 32))
+    if dtype == F32 or rng.random() < 0.3:
+        state = _log(rng, 1, 64)
+    state = max(1, min(state, 16384 * 4096 * 16 // (rows * channels) // (1 if form == "prompt" else 2), 64))
+    groups = rng.choice((1, 1, 2, 4))
+    case["channels"] = -(-channels // groups) * groups
+    return case | dict(state=state, groups=groups, gate=rng.random() < 0.7)
+
+
+# ------------------------------------------------------------------ inputs --
+
+def _lengths(case):
+    """Lengths of the packed sequences: log-uniform, some of them empty, a few rows behind the last."""
+    rows, n = case["rows"], case["seqs"]
+    r = random.Random(rows * 1_000_003 + n)
+    w = [math.exp(r.uniform(0.0, 6.0)) if i % 5 != 3 else 0.0 for i in range(n)]
+    left, whole = rows - min(rows % 7, rows // 8), sum(w)
+    got = [int(left * v / whole) for v in w]
+    got[0] += left - sum(got)
+    return got
+
+
+def _spans(case):
+    """First row and row past the last of every sequence."""
+    if not case["packed"]:
+        one = case["rows"] // case["seqs"]
+        return [(i * one, (i + 1) * one) for i in range(case["seqs"])]
+    spans, at = [], 0
+    for n in _lengths(case):
+        spans.append((at, at + n))
+        at += n
+    return spans
+
+
+def _sizes(case):
+    """Element counts of a list of parameters: log-uniform, at least one each."""
+    n, total = case["tensors"], case["total"]
+    r = random.Random(n * 1_000_003 + total)
+    w = [math.exp(r.uniform(0.0, case["spread"])) for _ in range(n)]
+    left, whole = total - n, sum(w)
+    sizes = [1 + int(left * v / whole) for v in w]
+    sizes[0] += total - sum(sizes)
+    return sizes
+
+
+class _Maker:
+    def __init__(self, seed, dtype):
+        self.gen = torch.Generator(device="cuda").manual_seed(seed)
+        self.dtype = dtype
+
+    def __call__(self, *shape, std=1.0, mean=0.0, dtype=None):
+        t = torch.empty(shape, device="cuda").normal_(mean, std, generator=self.gen)
+        return t.to(dtype or self.dtype)
+
+    def uniform(self, *shape):
+        return torch.empty(shape, device="cuda").uniform_(generator=self.gen)
+
+
+def prepare(case, seed):
+    if case["op"] == "adamw":
+        return _prepare_adamw(case, seed)
+    make = _Maker(seed, TYPES[case["dtype"]])
+    s, rows, d, token = {"case": case}, case["rows"], case["channels"], case["form"] == "token"
+    # A batch of prompts has its own dimension; packed sequences and tokens are rows.
+    lead = (case["seqs"], rows // case["seqs"]) if not case["packed"] and not token else (rows,)
+    proj = make(*lead, 2 * d)  # the input projection: x and the gate side by side
+    s["x"] = proj[..., :d]
+    if case["packed"]:
+        ends = [0] + [e for _, e in _spans(case)]
+        s["starts"] = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    if token:  # a slot of the state's pool for each running request
+        s["slots"] = torch.randperm(case["seqs"], generator=make.gen, device="cuda")[:rows].to(torch.int32)
+    if case["op"] == "conv":
+        k = case["taps"]
+        s["w"], s["b"] = make(d, k, std=k ** -0.5), make(d, std=0.1)
+        if case["initial"]:
+            s["initial"] = make(case["seqs"], k - 1, d)
+    else:
+        n, g = case["state"], case["groups"]
+        if case["gate"]:
+            s["z"] = proj[..., d:]
+        # B, C and the rank of delta come out of one projection.
+        rank = -(-d // 16)
+        bc = make(*lead, rank + 2 * g * n)
+        s["B"], s["C"] = (bc[..., rank + i * g * n:rank + (i + 1) * g * n].unflatten(-1, (g, n)) for i in (0, 1))
+        s["delta"] = make(*lead, d, std=0.5)
+        # steps between 0.001 and 0.1 behind the softplus
+        step = torch.exp(make.uniform(d) * math.log(100.0) + math.log(1e-3))
+        s["delta_bias"] = step + torch.log(-torch.expm1(-step))
+        s["A"] = -torch.arange(1, n + 1, device="cuda", dtype=torch.float32) * torch.exp(make(d, n, std=0.1, dtype=torch.float32))
+        s["D"] = make(d, std=0.1, mean=1.0, dtype=torch.float32)
+        if case["initial"]:
+            s["initial"] = make(case["seqs"], d, n, std=0.5, dtype=torch.float32)
+    if case["form"] == "train":
+        s["dy"] = make(*lead, d)
+    return s
+
+
+def _prepare_adamw(case, seed):
+    make, kinds, sizes = _Maker(seed, torch.float32), KINDS[case["kind"]], _sizes(case)
+    s = {"case": case, "groups": []}
+    lists = {k: [None] * len(sizes) for k in ("p", "g", "m", "v", "m_scale", "v_scale", "copy")}
+    for j, (tp, tg, tc) in enumerate(kinds):
+        # One flat buffer for each kind, each tensor from a multiple of 256 bytes on.
+        mine, at, starts = range(j, len(sizes), len(kinds)), 0, []
+        for i in mine:
+            starts.append(at)
+            at += -(-sizes[i] // BLOCK) * BLOCK
+        real = torch.zeros(at, dtype=torch.bool, device="cuda")
+        for i, a in zip(mine, starts):
+            real[a:a + sizes[i]] = True
+        f = {"p": make(at, std=0.02) * real, "g": make(at, std=0.01) * real, "m": make(at, std=0.003) * real,
+             "v": (make(at, std=0.01) * real).square()}
+        f["p"], f["g"] = f["p"].to(TYPES[tp]), f["g"].to(TYPES[tg])
+        f["copy"] = f["p"].to(TYPES[tc]) if tc else None
+        if case["bits"] == 8:
+            f["m"], f["m_scale"], f["v"], f["v_scale"] = _encode(f["m"], f["v"])
+        s["groups"].append(f)
+        for key, flat in f.items():
+            if flat is None:
+                continue
+            per = BLOCK if key.endswith("scale") else 1
+            for i, a in zip(mine, starts):
+                lists[key][i] = flat[a // per:a // per + -(-sizes[i] // per)]
+    s |= {"params": lists["p"], "grads": lists["g"], "copies": lists["copy"] if any(k[2] for k in kinds) else None}
+    s["state"] = {k: lists[k] for k in (("m", "v", "m_scale", "v_scale") if case["bits"] == 8 else ("m", "v"))}
+    if case["bits"] == 8:  # where a checkpoint reads the states out
+        s["values"] = [{k: torch.empty_like(f[k], dtype=torch.float32) for k in ("m", "v")} for f in s["groups"]]
+        s["out"] = {k: [None] * len(sizes) for k in ("m", "v")}
+        for j, f in enumerate(s["values"]):
+            at = 0
+            for i in range(j, len(sizes), len(kinds)):
+                for k in ("m", "v"):
+                    s["out"][k][i] = f[k][at:at + sizes[i]]
+                at += -(-sizes[i] // BLOCK) * BLOCK
+    if case["clip"]:
+        s["norm"] = torch.stack([f["g"].double().square().sum() for f in s["groups"]]).sum().sqrt().float()
+    return s
+
+
+# -------------------------------------------------------------- plain form --
+
+def _silu(v):
+    """Value and derivative."""
+    p = 1 / (1 + torch.exp(-v))
+    return v * p, p * (1 + v * (1 - p))
+
+
+def _rows(t, tail):
+    """One dimension of rows in front of the last ``tail`` dimensions, in 32 bits."""
+    return t.reshape(-1, *t.shape[t.dim() - tail:]).float()
+
+
+def _firsts(s, case):
+    """Which row begins a sequence, by its number of rows before it in the sequence: [rows], far for rows in none."""
+    dev, rows = s["x"].device, case["rows"]
+    r = torch.arange(rows, device=dev)
+    if not case["packed"]:
+        one = rows // case["seqs"]
+        return r % one, r // one, r >= 0
+    st = s["starts"].long()
+    # the last sequence that begins at or before a row is its own
+    seq = torch.searchsorted(st[:-1].contiguous(), r, right=True) - 1
+    return r - st[seq], seq, r < st[-1]
+
+
+def _plain_conv(s):
+    case, out = s["case"], s["x"].dtype
+    k, d, w = case["taps"], case["channels"], s["w"].float()
+    x = _rows(s["x"], 1)
+    before = s["initial"].float() if "initial" in s else None
+    if case["form"] == "token":
+        at = s["slots"].long()
+        win = torch.cat([before[at], x[:, None]], 1)  # [rows, taps, channels]
+        pre = (win * w.t()).sum(1) + s["b"].float()
+        s["initial"][at] = win[:, 1:].to(out)
+        return {"y": (_silu(pre)[0] if case["act"] == "silu" else pre).to(out), "state": s["initial"]}
+    at, seq, real = _firsts(s, case)
+
+    def tap(j):
+        """Each row's input j rows before it."""
+        v = torch.nn.functional.pad(x, (0, 0, j, 0))[:len(x)] * (at >= j)[:, None]
+        if before is not None and j:
+            v = v + before[seq, (k - 1 - j + at).clamp(max=k - 2)] * (at < j)[:, None]
+        return v * real[:, None]
+
+    pre = s["b"].float() + sum(w[:, k - 1 - j] * tap(j) for j in range(k))
+    v, g = _silu(pre) if case["act"] == "silu" else (pre, torch.ones_like(pre))
+    r = {"y": (v * real[:, None]).to(out).view(s["x"].shape)}
+    # the last rows of each sequence, with what was before it
+    dev = x.device
+    spans = torch.tensor(_spans(case), device=dev)
+    pos = spans[:, 1:] - (k - 1) + torch.arange(k - 1, device=dev)  # [seqs, taps - 1]
+    inside = pos >= spans[:, :1]
+    last = x[pos.clamp(0, len(x) - 1)] * inside[..., None]
+    if before is not None:
+        length = spans[:, 1] - spans[:, 0]
+        old = (torch.arange(k - 1, device=dev) + length[:, None]).clamp(max=k - 2)
+        last = last + before.gather(1, old[..., None].expand(-1, -1, d)) * (~inside)[..., None]
+    r["last"] = last.to(out)
+    if case["form"] == "prompt":
+        return r
+    dp = s["dy"].reshape(-1, d).float() * g * real[:, None]
+    dx = torch.zeros_like(x)
+    dw = torch.empty_like(w)
+    di = torch.zeros_like(before) if before is not None else None
+    for j in range(k):  # one tap at a time
+        e = dp * w[:, k - 1 - j]
+        dw[:, k - 1 - j] = (dp * tap(j)).sum(0)
+        dx[:len(x) - j] += (e * (at >= j)[:, None])[j:]
+        if di is not None and j:
+            early = ((at < j) & real).nonzero()[:, 0]
+            di.index_put_((seq[early], k - 1 - j + at[early]), e[early], accumulate=True)
+    r |= {"dx": dx.to(out).view(s["x"].shape), "dw": dw.to(out), "db": dp.sum(0).to(out)}
+    if di is not None:
+        r["dinitial"] = di.to(out)
+    return r
+
+
+def _recur(a, b):
+    """h[t] = a[t] h[t - 1] + b[t] along the first dimension, from zero: blocks of rows side by side, then what each
+    block inherits."""
+    t, q = a.shape[0], max(1, math.isqrt(a.shape[0]))
+    pad = -t % q
+    if pad:
+        zero = a.new_zeros((pad, *a.shape[1:]))
+        a, b = torch.cat([a, zero]), torch.cat([b, zero])
+    a, h = a.view(-1, q, *a.shape[1:]).clone(), b.reshape(-1, q, *b.shape[1:]).clone()
+    for i in range(1, q):
+        h[:, i] += a[:, i] * h[:, i - 1]
+        a[:, i] *= a[:, i - 1]  # the product of the block's factors so far
+    for c in range(1, h.shape[0]):
+        h[c] += a[c] * h[c - 1, -1]
+    return h.view(-1, *h.shape[2:])[:t]
+
+
+def _plain_scan(s):
+    case, out = s["case"], s["x"].dtype
+    d, n, g = case["channels"], case["state"], case["groups"]
+    x, raw = _rows(s["x"], 1), _rows(s["delta"], 1) + s["delta_bias"]
+    delta = raw.clamp(min=0) + torch.log1p(torch.exp(-raw.abs()))
+    spread = lambda t: t.repeat_interleave(d // g, 1)  # noqa: E731  a group's values for each of its channels
+    B, C = (_rows(s[k], 2) for k in ("B", "C"))
+    a = torch.exp(delta[..., None] * s["A"])
+    b = (delta * x)[..., None] * spread(B)
+    z = _rows(s["z"], 1) if case["gate"] else None
+    first = s["initial"] if "initial" in s else None
+    if case["form"] == "token":
+        at = s["slots"].long()
+        h = a * first[at] + b
+        first[at] = h
+        y = (h * spread(C)).sum(-1) + s["D"] * x
+        return {"y": (y * _silu(z)[0] if case["gate"] else y).to(out), "state": first}
+    at, seq, real = _firsts(s, case)
+    begins = (at == 0) & real
+    rows = begins.nonzero()[:, 0]
+    # A sequence's first row takes the state from before as a part of what it adds.
+    b = b * real[:, None, None]
+    if first is not None:
+        b[rows] += a[rows] * first[seq[rows]]
+    keep = a * (real & ~begins)[:, None, None]
+    h = _recur(keep, b)
+    y = (h * spread(C)).sum(-1) + s["D"] * x
+    last = first.clone() if first is not None else torch.zeros(case["seqs"], d, n, device=x.device)
+    ends = torch.tensor([(i, e - 1) for i, (f, e) in enumerate(_spans(case)) if e > f], device=x.device)
+    last[ends[:, 0]] = h[ends[:, 1]]
+    zv, zd = _silu(z) if case["gate"] else (torch.ones_like(y), None)
+    r = {"y": (y * zv * real[:, None]).to(out).view(s["x"].shape), "last": last}
+    if case["form"] == "prompt":
+        return r
+    dy = s["dy"].reshape(-1, d).float() * real[:, None]
+    if case["gate"]:
+        r["dz"] = (dy * y * zd).to(out).view(s["x"].shape)
+        dy = dy * zv
+    follow = torch.cat([keep[1:], torch.zeros_like(keep[:1])])
+    del keep
+    dh = _recur(follow.flip(0), (dy[..., None] * spread(C)).flip(0)).flip(0)
+    del follow
+    before = torch.cat([torch.zeros_like(h[:1]), h[:-1]])
+    before[rows] = first[seq[rows]] if first is not None else 0.0
+    q = dh * a * before
+    del before
+    r["dA"] = (delta[..., None] * q).sum(0)
+    dd = (q * s["A"]).sum(-1)
+    if first is not None:
+        di = torch.zeros_like(first)
+        di[seq[rows]] = (dh * a)[rows]
+        r["dinitial"] = di
+    del q, a
+    w = (dh * spread(B)).sum(-1)  # what delta x and x delta get
+    dd = dd + w * x
+    dd = dd / (1 + torch.exp(-raw))
+    r["ddelta"] = dd.to(out).view(s["x"].shape)
+    r["ddelta_bias"] = (dd * real[:, None]).sum(0)
+    r["dx"] = (w * delta + s["D"] * dy).to(out).view(s["x"].shape)
+    r["dD"] = (dy * x).sum(0)
+    r["dB"] = (dh * (delta * x)[..., None]).view(-1, g, d // g, n).sum(2).to(out).view(s["B"].shape)
+    r["dC"] = (h * dy[..., None]).view(-1, g, d // g, n).sum(2).to(out).view(s["C"].shape)
+    return r
+
+
+def _border(v, k, c):
+    """Whether ``v`` lies above the border between code ``c`` and the next."""
+    return v > (c + 0.5).square() * k
+
+
+def _encode(m, v):
+    """8-bit states of 128 elements each: m is the scale times a signed code's square, the root of v the scale times
+    an unsigned code's square; the scales fit the largest.  A positive v keeps a code of 1 at least; where the largest is below 2^-100, all codes are 0."""
+    m, v = m.view(-1, BLOCK), v.view(-1, BLOCK)
+    top_m, top_v = m.abs().amax(1, keepdim=True), v.amax(1, keepdim=True)
+    tiny = 2.0 ** -100
+    km = torch.where(top_m < tiny, 0.0, top_m * (1 / 16129))
+    kv = torch.where(top_v < tiny, 0.0, torch.sqrt(top_v) * (1 / 65025))
+
+    def code(above, guess, most):
+        c = guess.nan_to_num(0.0).round().clamp(0, most)
+        c = c + (above(c) & (c < most))
+        return c - (~above(c - 1) & (c > 0)).float()
+
+    cm = code(lambda c: _border(m.abs(), km, c), torch.sqrt(m.abs() / km), 127)
+    cv = code(lambda c: v > ((c + 0.5).square() * kv).square(), torch.sqrt(torch.sqrt(v) / kv), 255)
+    cm, cv = torch.where(km > 0, cm, 0.0), torch.where(kv > 0, torch.where(v > 0, cv.clamp(min=1), cv), 0.0)
+    cm = torch.where(m < 0, -cm, cm)
+    return cm.to(torch.int8).view(-1), km.view(-1), cv.to(torch.uint8).view(-1), kv.view(-1)
+
+
+def _decode(f):
+    m = f["m"].view(-1, BLOCK).float()
+    m = m * m.abs() * f["m_scale"][:, None]
+    r = f["v"].view(-1, BLOCK).float().square() * f["v_scale"][:, None]
+    return m.view(-1), (r * r).view(-1)
+
+
+def _plain_adamw(s):
+    case = s["case"]
+    c = (1.0 / (s["norm"] + CLIP_EPS)).clamp(max=1.0) if case["clip"] else None
+    for f in s["groups"]:
+        g = f["g"].float()
+        if c is not None:
+            g = g * c
+        m, v = _decode(f) if case["bits"] == 8 else (f["m"], f["v"])
+        m = m * BETAS[0] + g * (1 - BETAS[0])
+        v = v * BETAS[1] + g * (1 - BETAS[1]) * g
+        step = m * (RATE / (1 - BETAS[0] ** STEP)) / (torch.sqrt(v) * (1 - BETAS[1] ** STEP) ** -0.5 + ADAM_EPS)
+        p = f["p"].float() * (1 - RATE * DECAY) - step
+        f["p"].copy_(p)
+        if f["copy"] is not None:
+            f["copy"].copy_(p)
+        if case["bits"] == 8:
+            for k, t in zip(("m", "m_scale", "v", "v_scale"), _encode(m, v)):
+                f[k].copy_(t)
+        else:
+            f["m"].copy_(m)
+            f["v"].copy_(v)
+    if case["bits"] == 8:
+        for f, o in zip(s["groups"], s["values"]):
+            m, v = _decode(f)
+            o["m"].copy_(m)
+            o["v"].copy_(v)
+    return _updated(s)
+
+
+def _updated(s):
+    """The buffers that a step has written; states of 8 bits as the values they stand for."""
+    read = s["values"] if s["case"]["bits"] == 8 else s["groups"]
+    return [{"p": f["p"], "copy": f["copy"], "m": o["m"], "v": o["v"]} for f, o in zip(s["groups"], read)]
+
+
+# --------------------------------------------------------------- one pass --
+
+def run(state):
+    s, case = state, state["case"]
+    if not own:
+        return {"conv": _plain_conv, "scan": _plain_scan, "adamw": _plain_adamw}[case["op"]](s)
+    import convolution_implicit_gemm_conv2d_amd as cm
+
+    if case["op"] == "adamw":
+        cm.adamw_step(s["params"], s["grads"], s["state"], STEP, RATE, betas=BETAS, eps=ADAM_EPS, weight_decay=DECAY,
+                      norm=s.get("norm"), max_norm=1.0, norm_eps=CLIP_EPS, copies=s["copies"])
+        if case["bits"] == 8:
+            cm.adamw_moments(s["state"], out=s["out"])
+        return _updated(s)
+    if case["op"] == "conv":
+        if case["form"] == "token":
+            y = cm.causal_conv_step(s["x"], s["w"], s["initial"], s["b"], activation=case["act"], slots=s["slots"])
+            return {"y": y, "state": s["initial"]}
+        how = dict(activation=case["act"], starts=s.get("starts"), initial=s.get("initial"))
+        last = torch.empty(case["seqs"], case["taps"] - 1, case["channels"], dtype=s["x"].dtype, device=s["x"].device)
+        r = {"y": cm.causal_conv(s["x"], s["w"], s["b"], last=last, **how), "last": last}
+        if case["form"] == "train":
+            d = cm.causal_conv_grad(s["dy"], s["x"], s["w"], s["b"], **how)
+            r |= {"dx": d["x"], "dw": d["weight"], "db": d["bias"]}
+            if "initial" in s:
+                r["dinitial"] = d["initial"]
+        return r
+    how = dict(D=s["D"], z=s.get("z"), delta_bias=s["delta_bias"], softplus=True, gate_activation="silu")
+    if case["form"] == "token":
+        y = cm.selective_step(s["x"], s["delta"], s["A"], s["B"], s["C"], s["initial"], slots=s["slots"], **how)
+        return {"y": y, "state": s["initial"]}
+    how |= dict(starts=s.get("starts"), initial=s.get("initial"))
+    last = torch.empty(case["seqs"], case["channels"], case["state"], dtype=torch.float32, device=s["x"].device)
+    kept = cm.selective_scan_saved(s["x"], s["A"]) if case["form"] == "train" else None
+    y = cm.selective_scan(s["x"], s["delta"], s["A"], s["B"], s["C"], last=last, saved=kept, **how)
+    r = {"y": y, "last": last}
+    if case["form"] == "train":
+        d = cm.selective_scan_grad(s["dy"], s["x"], s["delta"], s["A"], s["B"], s["C"], saved=kept, **how)
+        r |= {"d" + k: v for k, v in d.items() if v is not None}
+    return r
+
+
+def work(case):
+    if case["op"] == "adamw":
+        size = {BF16: 2, F32: 4, None: 0}
+        n, kinds = _sizes(case), KINDS[case["kind"]]
+        total = 0
+        for i, count in enumerate(n):
+            tp, tg, tc = kinds[i % len(kinds)]
+            total += count * (2 * size[tp] + size[tg] + size[tc] + 2 * 8 * case["bits"] // 32)
+            if case["bits"] == 8:  # and the states read out
+                total += count * 10
+        return {"bytes": total, "flops": 15 * case["total"]}
+    e = 2 if case["dtype"] == BF16 else 4
+    rows, d, seqs = case["rows"], case["channels"], case["seqs"]
+    train, token = case["form"] == "train", case["form"] == "token"
+    if case["op"] == "conv":
+        k = case["taps"]
+        values = 2 * rows * d + (k + 1) * d + 2 * (rows if token else seqs) * (k - 1) * d
+        flops = 2 * k * rows * d
+        if train:
+            values, flops = values + 2 * rows * d + (k + 1) * d, 3 * flops
+        return {"bytes": e * values, "flops": flops}
+    n, g = case["state"], case["groups"]
+    values = rows * d * (4 if case["gate"] else 3) + 2 * rows * g * n
+    states = (1 + case["initial"]) * (rows if token else seqs) * d * n
+    flops = 7 * rows * d * n
+    if train:
+        values, flops = values + values, 20 * rows * d * n  # dy is read, a gradient of each input written
+        states += case["initial"] * seqs * d * n
+    return {"bytes": e * values + 4 * states, "flops": flops}
+
+
+# ----------------------------------------------------------------- 64 bits --
+
+def _each(parts, like, spans, tail):
+    """Sequences' results put back where they belong, zeros elsewhere."""
+    out = torch.zeros((like.shape[:-1].numel(), *tail), dtype=torch.float64, device=like.device)
+    pieces, at = [], 0
+    for p, (f, e) in zip(parts, spans):
+        pieces += [out[at:f], p]
+        at = e
+    return torch.cat(pieces + [out[at:]])
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    if case["op"] == "adamw":
+        return _exact_adamw(s)
+    token, d = case["form"] == "token", case["channels"]
+    leaf = {k: s[k].double().requires_grad_(case["form"] == "train")
+            for k in ("x", "w", "b", "delta", "A", "B", "C", "D", "z", "delta_bias", "initial") if k in s}
+    flat = {k: v.reshape(case["rows"], *v.shape[v.dim() - (2 if k in "BC" else 1):])
+            for k, v in leaf.items() if k in ("x", "delta", "B", "C", "z")}
+    spans = [(i, i + 1) for i in range(case["rows"])] if token else _spans(case)
+    slot = s["slots"].tolist() if token else range(len(spans))
+    if case["op"] == "conv":
+        ys, last = [], []
+        none = torch.zeros(case["taps"] - 1, d, dtype=torch.float64, device="cuda")
+        for (f, e), i in zip(spans, slot):
+            line = torch.cat([leaf["initial"][i] if "initial" in leaf else none, flat["x"][f:e]])
+            last.append(line[line.shape[0] - (case["taps"] - 1):])
+            pre = (line.unfold(0, case["taps"], 1) * leaf["w"]).sum(-1) + leaf["b"] if e > f else line[:0]
+            ys.append(torch.nn.functional.silu(pre) if case["act"] == "silu" else pre)
+    else:
+        heads = d // case["groups"]
+        delta = torch.nn.functional.softplus(flat["delta"] + leaf["delta_bias"], threshold=1e9)
+        a = torch.exp(delta.unsqueeze(-1) * leaf["A"])
+        b = (delta * flat["x"]).unsqueeze(-1) * flat["B"].repeat_interleave(heads, 1)
+        none = torch.zeros(d, case["state"], dtype=torch.float64, device="cuda")
+        first = [leaf["initial"][i] if "initial" in leaf else none for i in slot]
+        if token or not case["packed"]:  # all sequences one row at a time
+            one = spans[0][1]
+            h, hs = torch.stack(first), []
+            for at, bt in zip(a.view(-1, one, d, case["state"]).unbind(1), b.view(-1, one, d, case["state"]).unbind(1)):
+                h = at * h + bt
+                hs.append(h)
+            last, hs = h, torch.stack(hs, 1).view(-1, d, case["state"])
+        else:
+            rows_a, rows_b, hs, last = a.unbind(0), b.unbind(0), [], []
+            for (f, e), h in zip(spans, first):
+                for t in range(f, e):
+                    h = rows_a[t] * h + rows_b[t]
+                    hs.append(h)
+                last.append(h)
+            hs += [none] * (case["rows"] - len(hs))
+            hs = torch.stack(hs)
+        y = (hs * flat["C"].repeat_interleave(heads, 1)).sum(-1) + leaf["D"] * flat["x"]
+        y = y * torch.nn.functional.silu(flat["z"]) if case["gate"] else y
+        ys = [y[f:e] for f, e in spans]
+    y = _each(ys, s["x"], spans, (d,)).view(s["x"].shape)
+    last = torch.stack(list(last))
+    if token:
+        state = leaf["initial"].clone()
+        state[s["slots"].long()] = last
+        return {"y": y, "state": state}
+    r = {"y": y, "last": last}
+    if case["form"] == "train":
+        names = list(leaf)
+        got = torch.autograd.grad(y, [leaf[k] for k in names], s["dy"].double())
+        r |= {"d" + k: v for k, v in zip(names, got)}
+    return {k: v.detach() for k, v in r.items()}
+
+
+def _exact_adamw(s):
+    case, out = s["case"], []
+    c = min(1.0, 1.0 / (float(s["norm"]) + CLIP_EPS)) if case["clip"] else 1.0
+    for f in s["groups"]:
+        g = f["g"].double() * c
+        if case["bits"] == 8:
+            m = f["m"].double() * f["m"].double().abs() * f["m_scale"].double().repeat_interleave(BLOCK)
+            v = (f["v"].double() ** 2 * f["v_scale"].double().repeat_interleave(BLOCK)) ** 2
+        else:
+            m, v = f["m"].double(), f["v"].double()
+        m, v = torch.lerp(g, m, BETAS[0]), torch.lerp(g * g, v, BETAS[1])
+        p = f["p"].double()
+        mean, var = m / (1 - BETAS[0] ** STEP), v / (1 - BETAS[1] ** STEP)
+        p = p - RATE * (mean / (var ** 0.5 + ADAM_EPS) + DECAY * p)
+        # Codes next to a border go either way: 8-bit states have no value in 64 bits.
+        eight = case["bits"] == 8
+        out.append({"p": p, "copy": p if f["copy"] is not None else None, "m": None if eight else m, "v": None if eight else v})
+    return out
