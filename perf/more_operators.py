@@ -218,7 +218,7 @@ def _prepare_adamw(case, seed):
     s |= {"params": lists["p"], "grads": lists["g"], "copies": lists["copy"] if any(k[2] for k in kinds) else None}
     s["state"] = {k: lists[k] for k in (("m", "v", "m_scale", "v_scale") if case["bits"] == 8 else ("m", "v"))}
     if case["bits"] == 8:  # where a checkpoint reads the states out
-        s["values"] = [{k: torch.empty_like(f[k], dtype=torch.float32) for k in ("m", "v")} for f in s["groups"]]
+        s["values"] = [{k: torch.zeros_like(f[k], dtype=torch.float32) for k in ("m", "v")} for f in s["groups"]]
         s["out"] = {k: [None] * len(sizes) for k in ("m", "v")}
         for j, f in enumerate(s["values"]):
             at = 0
