@@ -7,7 +7,9 @@ stream.  The low-level functions carry the C names and arguments;
 ``conv2d_transposed`` derive the sizes from tensor shapes and allocate the
 output (and the weight gradient's workspace, when none is given).  The
 operators around a convolution (gated feed-forward, block norms, gradient
-clipping) are in ``block`` and exported here.
+clipping) are in ``block``, those along a sequence (short causal convolution,
+selective scan) in ``sequence``, the AdamW step in ``optimizer``; all are
+exported here.
 """
 from __future__ import annotations
 
@@ -447,4 +449,9 @@ def conv2d_weight_grad(x, dy, w_shape, stride=1, padding=0, dilation=1, groups=1
 from .block import *  # noqa: E402,F401,F403  (uses the helpers above)
 from .block import __all__ as _block_all  # noqa: E402
 
-__all__ += _block_all
+from .sequence import *  # noqa: E402,F401,F403
+from .sequence import __all__ as _sequence_all  # noqa: E402
+from .optimizer import *  # noqa: E402,F401,F403
+from .optimizer import __all__ as _optimizer_all  # noqa: E402
+
+__all__ += _block_all + _sequence_all + _optimizer_all

@@ -14,6 +14,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)),
 _I = ctypes.c_int
 _L = ctypes.c_longlong
 _P = ctypes.c_void_p
+_D = ctypes.c_double
 
 # Name -> (restype, argtypes), mirroring include/convmi.h.
 _GEOM = [_I] * 16  # N C H W C_out KH KW sh sw ph pw dh dw groups layout dtype
@@ -49,6 +50,21 @@ SIGNATURES = {
     "conv_grad_norm": (_I, [_P, _P, _P, _I, _P, _P, ctypes.c_size_t, _P]),
     "conv_grad_clip": (_I, [_P, _P, _P, _P, _I, ctypes.c_float, ctypes.c_float, _P, _P, ctypes.c_size_t, _P]),
     "conv_grad_workspace_size": (_I, [_I, ctypes.POINTER(ctypes.c_size_t)]),
+    # x w bias starts initial y last, rows seqs C K x_stride act clear dtype
+    "conv_causal_fwd": (_I, [_P] * 7 + [_L, _I, _I, _I, _L, _I, _I, _I, _P]),
+    "conv_causal_bwd": (_I, [_P] * 12 + [ctypes.c_size_t, _L, _I, _I, _I, _L, _I, _I, _I, _P]),
+    "conv_causal_bwd_workspace_size": (_I, [_L, _I, _I, _I, ctypes.POINTER(ctypes.c_size_t)]),
+    "conv_causal_step": (_I, [_P] * 6 + [_L, _I, _I, _I, _L, _I, _I, _I, _P]),
+    # ..., rows seqs channels N groups, five strides, softplus act clear dtype
+    "conv_scan_fwd": (_I, [_P] * 14 + [ctypes.c_size_t, _L, _I, _I, _I, _I] + [_L] * 5 + [_I] * 4 + [_P]),
+    "conv_scan_bwd": (_I, [_P] * 23 + [ctypes.c_size_t, _L, _I, _I, _I, _I] + [_L] * 5 + [_I] * 4 + [_P]),
+    "conv_scan_saved_size": (_I, [_L, _I, _I, ctypes.POINTER(ctypes.c_size_t)]),
+    "conv_scan_fwd_workspace_size": (_I, [_L, _I, _I, _I, _I, _I, ctypes.POINTER(ctypes.c_size_t)]),
+    "conv_scan_bwd_workspace_size": (_I, [_L, _I, _I, _I, _I, _I, _I, ctypes.POINTER(ctypes.c_size_t)]),
+    "conv_scan_step": (_I, [_P] * 11 + [_L, _I, _I, _I, _I] + [_L] * 5 + [_I] * 4 + [_P]),
+    # host arrays; n bits lr beta1 beta2 eps weight_decay step lr_dev step_dev norm max_norm norm_eps
+    "conv_adamw": (_I, [_P] * 11 + [_I, _I] + [_D] * 5 + [_L, _P, _P, _P, _D, _D, _P]),
+    "conv_adamw_moments": (_I, [_P] * 7 + [_I, _P]),
     "conv_path_name": (ctypes.c_char_p, [_I]),
     "conv_last_error": (ctypes.c_char_p, []),
     "conv_arm_launch_events": (_I, [_P, _P]),

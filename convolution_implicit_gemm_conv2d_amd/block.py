@@ -131,7 +131,10 @@ def conv_grad_clip(grads, outs, counts, dtypes, n, max_norm, eps, norm, workspac
 
 _ABI = ("conv_gated_fwd_ex", "conv_gated_fwd_workspace_size", "conv_gated_bwd",
         "conv_gated_bwd_workspace_size", "conv_block_norm_fwd", "conv_block_norm_bwd",
-        "conv_block_norm_bwd_workspace_size", "conv_grad_norm", "conv_grad_clip", "conv_grad_workspace_size")
+        "conv_block_norm_bwd_workspace_size", "conv_grad_norm", "conv_grad_clip", "conv_grad_workspace_size",
+        "conv_causal_fwd", "conv_causal_bwd", "conv_causal_bwd_workspace_size", "conv_causal_step", "conv_scan_fwd",
+        "conv_scan_bwd", "conv_scan_step", "conv_scan_saved_size", "conv_scan_fwd_workspace_size",
+        "conv_scan_bwd_workspace_size", "conv_adamw", "conv_adamw_moments")
 
 
 @functools.lru_cache(maxsize=None)

@@ -1,0 +1,417 @@
+// AdamW over a list of tensors, with states in 32 or in 8 bits.
+//
+//   c = min(1, max_norm / (norm + norm_eps)),  g' = c g,
+//   m' = b1 m + (1 - b1) g',   v' = b2 v + (1 - b2) g'^2,
+//   p' = p (1 - lr w) - lr / (1 - b1^t) m' / (sqrt(v') / sqrt(1 - b2^t) + eps).
+//
+// A stream over memory: every parameter, gradient and state is read once and
+// what changes is written once (fp32 throughout: 28 bytes an element; bf16 with
+// 8-bit states: 10).  Clipping by a norm in hand costs a factor here, where
+// clip_gradients is a pass of its own.  One launch takes a table of up to 48
+// tensors as its argument and deals chunks of them out to its workgroups.
+//
+// 8 bits: 128 elements, on 16 lanes, share a scale.  m is the scale times q |q|
+// and the root of v the scale times q^2: steps next to the largest value are
+// 1.6 % and 3.1 % and values down to 6e-5 (of the root of v 1.5e-5) of it still have a code of
+// their own, without a table.  A value next to a border is compared with it
+// exactly, so codes do not depend on the roundings of the hardware's root and
+// reciprocal, and the arithmetic up to them has a fixed order of roundings, no
+// multiply-add contracted.
+#include "kernels.hpp"
+
+#include <algorithm>
+#include <cmath>
+
+namespace convmi {
+namespace {
+
+constexpr int kThreads = 256, kE = 8;  // elements of a lane at once
+constexpr float kTiny = 0x1p-100f;     // blocks below it hold zeros
+constexpr int kMostM = 127, kMostV = 255;
+
+template <int N>
+struct Table {
+    void *p[N], *m[N], *v[N], *copy[N];
+    const void* g[N];
+    float *ms[N], *vs[N];
+    uint64_t count[N];        // elements * 8 + (1: p bf16) + (2: g bf16) + (4: copy bf16)
+    uint32_t begin[N + 1];    // first chunk of each tensor
+    int n;
+    uint32_t chunk;           // elements in a chunk, a multiple of 2048
+};
+constexpr int kTensors = 48;
+static_assert(sizeof(Table<kTensors>) + 128 <= 4096, "the table is a kernel argument");
+
+struct Rates {
+    double lr, log_b1, log_b2;         // for device values
+    float keep, rate, root, eps;       // 1 - lr w, lr / (1 - b1^t), (1 - b2^t)^-1/2
+    float b1, c1, b2, c2, max_norm, norm_eps;
+    double weight_decay;
+    long long step;
+    const float *lr_dev, *norm;
+    const long long* step_dev;
+};
+
+template <int N>
+__device__ __forceinline__ int find(const Table<N>& t, uint32_t c)
+{
+    int lo = 0, hi = t.n;  // begin[lo] <= c < begin[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (t.begin[mid] <= c) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+// kE elements from the i-th on; past n zeros.
+__device__ __forceinline__ void load_e(const void* at, bool bf16, uint64_t i, int have, float* v)
+{
+    if (have >= kE) {
+        if (bf16) {
+            const uint4 w = load16_any(static_cast<const bf16_t*>(at) + i);
+            const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                v[2 * k] = __uint_as_float(q[k] << 16);
+                v[2 * k + 1] = __uint_as_float(q[k] & 0xffff0000u);
+            }
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint4 w = load16_any(static_cast<const float*>(at) + i + 4 * h);
+                v[4 * h] = __uint_as_float(w.x);
+                v[4 * h + 1] = __uint_as_float(w.y);
+                v[4 * h + 2] = __uint_as_float(w.z);
+                v[4 * h + 3] = __uint_as_float(w.w);
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < kE; ++k) {
+        v[k] = 0.f;
+        if (k < have) v[k] = bf16 ? load_f(static_cast<const bf16_t*>(at) + i + k) : load_f(static_cast<const float*>(at) + i + k);
+    }
+}
+__device__ __forceinline__ void store_e(void* at, bool bf16, uint64_t i, int have, const float* v)
+{
+    if (have >= kE) {
+        if (bf16) {
+            store16_any(static_cast<bf16_t*>(at) + i, make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                store16_any(static_cast<float*>(at) + i + 4 * h, make_uint4(__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]),
+                                                                           __float_as_uint(v[4 * h + 2]), __float_as_uint(v[4 * h + 3])));
+        }
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < kE; ++k)
+        if (k < have) {
+            if (bf16) store_f(static_cast<bf16_t*>(at) + i + k, v[k]);
+            else store_f(static_cast<float*>(at) + i + k, v[k]);
+        }
+}
+
+typedef uint32_t u2_any __attribute__((ext_vector_type(2), aligned(1)));
+__device__ __forceinline__ void load_codes(const void* at, uint64_t i, int have, uint32_t* q)
+{
+    const uint8_t* p = static_cast<const uint8_t*>(at) + i;
+    q[0] = q[1] = 0;
+    if (have >= kE) {
+        const u2_any w = *reinterpret_cast<const u2_any*>(p);
+        q[0] = w.x;
+        q[1] = w.y;
+    } else {
+#pragma unroll
+        for (int k = 0; k < kE; ++k)
+            if (k < have) q[k >> 2] |= static_cast<uint32_t>(p[k]) << (8 * (k & 3));
+    }
+}
+__device__ __forceinline__ void store_codes(void* at, uint64_t i, int have, const uint32_t* q)
+{
+    uint8_t* p = static_cast<uint8_t*>(at) + i;
+    if (have >= kE) {
+        u2_any w;
+        w.x = q[0];
+        w.y = q[1];
+        *reinterpret_cast<u2_any*>(p) = w;
+    } else {
+#pragma unroll
+        for (int k = 0; k < kE; ++k)
+            if (k < have) p[k] = static_cast<uint8_t>(q[k >> 2] >> (8 * (k & 3)));
+    }
+}
+
+// The 16 lanes of a block.
+__device__ __forceinline__ uint32_t block_max(uint32_t v)
+{
+#define CONVMI_MAX(CTRL) v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xf, 0xf, false)))
+    CONVMI_MAX(0x128);
+    CONVMI_MAX(0x124);
+    CONVMI_MAX(0x122);
+    CONVMI_MAX(0x121);
+#undef CONVMI_MAX
+    return v;
+}
+
+#pragma clang fp contract(off)
+
+__device__ __forceinline__ float m_of(uint32_t byte, float scale)
+{
+    const float q = static_cast<float>(static_cast<int8_t>(byte));
+    return q * fabsf(q) * scale;
+}
+__device__ __forceinline__ float v_of(uint32_t byte, float scale)
+{
+    const float q = static_cast<float>(byte), r = q * q * scale;
+    return r * r;
+}
+__device__ __forceinline__ void decode(const uint32_t* qm, const uint32_t* qv, float km, float kv, float* m, float* v)
+{
+#pragma unroll
+    for (int k = 0; k < kE; ++k) {
+        m[k] = m_of((qm[k >> 2] >> (8 * (k & 3))) & 255u, km);
+        v[k] = v_of((qv[k >> 2] >> (8 * (k & 3))) & 255u, kv);
+    }
+}
+
+// Codes of a block's m and v, and its scales.
+__device__ __forceinline__ void encode(const float* m, const float* v, uint32_t* qm, uint32_t* qv, float& km, float& kv)
+{
+    uint32_t top_m = 0, top_v = 0;  // as bits: a NaN is above everything
+#pragma unroll
+    for (int k = 0; k < kE; ++k) {
+        top_m = max(top_m, __float_as_uint(m[k]) & 0x7fffffffu);
+        top_v = max(top_v, __float_as_uint(v[k]) & 0x7fffffffu);
+    }
+    const float sm = __uint_as_float(block_max(top_m)), sv = __uint_as_float(block_max(top_v));
+    km = sm < kTiny ? 0.f : sm * (1.0f / 16129.0f);
+    kv = sv < kTiny ? 0.f : __builtin_sqrtf(sv) * (1.0f / 65025.0f);
+    // The hardware's root takes denormal values for 0: small blocks' v are lifted.
+    const bool small = sv < 0x1p-40f;
+    const float lift = small ? 0x1p64f : 1.0f;
+    // No scale, or one that is no number: all codes are 0.
+    const float im = km > 0.f ? __builtin_amdgcn_rcpf(km) : 0.f, iv = kv > 0.f ? __builtin_amdgcn_rcpf(kv) * (small ? 0x1p-32f : 1.0f) : 0.f;
+    qm[0] = qm[1] = qv[0] = qv[1] = 0;
+#pragma unroll
+    for (int k = 0; k < kE; ++k) {
+        // The guess is off by 2e-4 at most (two roundings of the reciprocal and
+        // the root each, at codes up to 255), so only values within 1e-3 of a
+        // border are compared with it.
+        const float a = fabsf(m[k]), t = __builtin_amdgcn_sqrtf(a * im), r = __builtin_rintf(t);
+        float c = __builtin_fminf(r, static_cast<float>(kMostM));
+        if (fabsf(t - r) > 0.499f) {
+            const float up = c + 0.5f, down = c - 0.5f;
+            if (a > up * up * km && c < kMostM) c += 1.0f;
+            else if (c > 0.f && !(a > down * down * km)) c -= 1.0f;
+        }
+        const int q = static_cast<int>(c);
+        qm[k >> 2] |= (static_cast<uint32_t>(m[k] < 0.f ? -q : q) & 255u) << (8 * (k & 3));
+        const float tv = __builtin_amdgcn_sqrtf(__builtin_amdgcn_sqrtf(v[k] * lift) * iv), rv = __builtin_rintf(tv);
+        float d = __builtin_fminf(rv, static_cast<float>(kMostV));
+        if (fabsf(tv - rv) > 0.499f) {
+            const float up = (d + 0.5f) * (d + 0.5f) * kv, down = (d - 0.5f) * (d - 0.5f) * kv;
+            if (v[k] > up * up && d < kMostV) d += 1.0f;
+            else if (d > 0.f && !(v[k] > down * down)) d -= 1.0f;
+        }
+        const uint32_t w = static_cast<uint32_t>(d);
+        qv[k >> 2] |= (w == 0 && v[k] > 0.f && kv > 0.f ? 1u : w) << (8 * (k & 3));
+    }
+}
+
+// m', v' and p' of one element; a fixed order of roundings up to m' and v'.
+__device__ __forceinline__ void update(float& p, float g, float& m, float& v, float clip, const Rates& r)
+{
+    g = g * clip;
+    m = m * r.b1 + g * r.c1;
+    v = v * r.b2 + g * r.c2 * g;
+    const bool small = v < 0x1p-64f;  // the hardware's root takes denormal values for 0
+    const float d = __builtin_amdgcn_sqrtf(small ? v * 0x1p64f : v) * (small ? 0x1p-32f : 1.0f) * r.root + r.eps;
+    p = p * r.keep - m * r.rate * __builtin_amdgcn_rcpf(d);
+}
+
+template <int BITS, int N>
+__global__ __launch_bounds__(kThreads) void adamw_kernel(Table<N> t, Rates r)
+{
+    __shared__ float late[3];
+    if (r.lr_dev || r.step_dev) {
+        if (threadIdx.x == 0) {
+            const double lr = r.lr_dev ? static_cast<double>(*r.lr_dev) : r.lr;
+            const double step = static_cast<double>(r.step_dev ? *r.step_dev : r.step);
+            late[0] = static_cast<float>(1.0 - lr * r.weight_decay);
+            late[1] = static_cast<float>(lr / (1.0 - exp(step * r.log_b1)));
+            late[2] = static_cast<float>(1.0 / sqrt(1.0 - exp(step * r.log_b2)));
+        }
+        __syncthreads();
+        r.keep = late[0];
+        r.rate = late[1];
+        r.root = late[2];
+    }
+    float clip = 1.0f;
+    if (r.norm) {
+        clip = r.max_norm / (*r.norm + r.norm_eps);
+        clip = clip > 1.0f ? 1.0f : clip;  // NaN stays
+    }
+    for (uint32_t c = blockIdx.x; c < t.begin[t.n]; c += gridDim.x) {
+        const int k = find(t, c);
+        const uint64_t count = t.count[k] >> 3, first = static_cast<uint64_t>(c - t.begin[k]) * t.chunk;
+        const uint32_t n = static_cast<uint32_t>(count - first < t.chunk ? count - first : t.chunk);
+        const bool pb = t.count[k] & 1, gb = t.count[k] & 2, cb = t.count[k] & 4;
+        // All lanes of a block of 128 go through its step together.
+        for (uint32_t at = threadIdx.x * kE; (at & ~static_cast<uint32_t>(kAdamBlock - 1)) < n; at += kThreads * kE) {
+            const int have = at < n ? static_cast<int>(n - at < kE ? n - at : kE) : 0;
+            const uint64_t i = first + at;
+            float p[kE], g[kE], m[kE], v[kE];
+            uint32_t qm[2], qv[2];
+            float km = 0.f, kv = 0.f;
+            load_e(t.p[k], pb, i, have, p);
+            load_e(t.g[k], gb, i, have, g);
+            if constexpr (BITS == 8) {
+                load_codes(t.m[k], i, have, qm);
+                load_codes(t.v[k], i, have, qv);
+                km = t.ms[k][i / kAdamBlock];
+                kv = t.vs[k][i / kAdamBlock];
+                decode(qm, qv, km, kv, m, v);
+            } else {
+                load_e(t.m[k], false, i, have, m);
+                load_e(t.v[k], false, i, have, v);
+            }
+#pragma unroll
+            for (int e = 0; e < kE; ++e) update(p[e], g[e], m[e], v[e], clip, r);
+            store_e(t.p[k], pb, i, have, p);
+            if (t.copy[k]) store_e(t.copy[k], cb, i, have, p);
+            if constexpr (BITS == 8) {
+#pragma unroll
+                for (int e = 0; e < kE; ++e)
+                    if (e >= have) m[e] = v[e] = 0.f;
+                encode(m, v, qm, qv, km, kv);
+                store_codes(t.m[k], i, have, qm);
+                store_codes(t.v[k], i, have, qv);
+                if ((threadIdx.x & 15) == 0) {
+                    t.ms[k][i / kAdamBlock] = km;
+                    t.vs[k][i / kAdamBlock] = kv;
+                }
+            } else {
+                store_e(t.m[k], false, i, have, m);
+                store_e(t.v[k], false, i, have, v);
+            }
+        }
+    }
+}
+
+// p: m's values, copy: v's values.
+template <int N>
+__global__ __launch_bounds__(kThreads) void moments_kernel(Table<N> t)
+{
+    for (uint32_t c = blockIdx.x; c < t.begin[t.n]; c += gridDim.x) {
+        const int k = find(t, c);
+        const uint64_t count = t.count[k] >> 3, first = static_cast<uint64_t>(c - t.begin[k]) * t.chunk;
+        const uint32_t n = static_cast<uint32_t>(count - first < t.chunk ? count - first : t.chunk);
+        for (uint32_t at = threadIdx.x * kE; at < n; at += kThreads * kE) {
+            const int have = static_cast<int>(n - at < kE ? n - at : kE);
+            const uint64_t i = first + at;
+            uint32_t qm[2], qv[2];
+            float m[kE], v[kE];
+            load_codes(t.m[k], i, have, qm);
+            load_codes(t.v[k], i, have, qv);
+            decode(qm, qv, t.ms[k][i / kAdamBlock], t.vs[k][i / kAdamBlock], m, v);
+            store_e(t.p[k], false, i, have, m);
+            store_e(t.copy[k], false, i, have, v);
+        }
+    }
+}
+
+constexpr int kMaxBlocks = 2048;
+
+// One list, N tensors a launch: `go` launches one table.
+template <int N, typename Go>
+hipError_t each_table(const AdamList& l, float* const* m_out, float* const* v_out, Go go)
+{
+    size_t total = 0;
+    for (int i = 0; i < l.n; ++i) total += l.counts[i];
+    // Elements in a chunk: about one a workgroup for small lists, at most 32768.
+    uint32_t chunk = kThreads * kE;
+    while (chunk < 32768 && total / chunk > kMaxBlocks) chunk *= 2;
+    int left = 0;
+    for (int i = 0; i < l.n; ++i) left += l.counts[i] != 0;
+    hipError_t e = hipSuccess;
+    CallEvents events;
+    for (int i = 0; left > 0 && e == hipSuccess;) {
+        Table<N> t;
+        t.n = 0;
+        t.chunk = chunk;
+        uint64_t chunks = 0;
+        for (; i < l.n && t.n < N; ++i) {
+            if (l.counts[i] == 0) continue;
+            const uint64_t more = (l.counts[i] + chunk - 1) / chunk;
+            if (t.n > 0 && chunks + more > UINT32_MAX) break;
+            t.m[t.n] = l.m[i];
+            t.v[t.n] = l.v[i];
+            t.ms[t.n] = l.m_scales ? l.m_scales[i] : nullptr;
+            t.vs[t.n] = l.v_scales ? l.v_scales[i] : nullptr;
+            t.count[t.n] = static_cast<uint64_t>(l.counts[i]) * 8;
+            if (m_out) {
+                t.p[t.n] = m_out[i];
+                t.copy[t.n] = v_out[i];
+                t.g[t.n] = nullptr;
+            } else {
+                t.p[t.n] = l.params[i];
+                t.g[t.n] = l.grads[i];
+                t.copy[t.n] = l.copies ? l.copies[i] : nullptr;
+                t.count[t.n] += (l.param_dtypes[i] == 1 ? 1 : 0) + (l.grad_dtypes[i] == 1 ? 2 : 0) + (t.copy[t.n] && l.copy_dtypes[i] == 1 ? 4 : 0);
+            }
+            t.begin[t.n++] = static_cast<uint32_t>(chunks);
+            chunks += more;
+            --left;
+        }
+        t.begin[t.n] = static_cast<uint32_t>(chunks);
+        events.next(left == 0);
+        e = go(t, dim3(static_cast<unsigned>(std::min<uint64_t>(chunks, kMaxBlocks))));
+    }
+    return e;
+}
+
+}  // namespace
+
+hipError_t launch_adamw(const AdamList& l, const AdamRates& a, hipStream_t s)
+{
+    Rates r{};
+    r.lr = a.lr;
+    r.weight_decay = a.weight_decay;
+    r.step = a.step;
+    r.log_b1 = std::log(a.beta1);
+    r.log_b2 = std::log(a.beta2);
+    const double t = static_cast<double>(a.step);
+    r.keep = static_cast<float>(1.0 - a.lr * a.weight_decay);
+    r.rate = static_cast<float>(a.lr / (1.0 - std::pow(a.beta1, t)));
+    r.root = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(a.beta2, t)));
+    r.eps = static_cast<float>(a.eps);
+    r.b1 = static_cast<float>(a.beta1);
+    r.c1 = static_cast<float>(1.0 - a.beta1);
+    r.b2 = static_cast<float>(a.beta2);
+    r.c2 = static_cast<float>(1.0 - a.beta2);
+    r.max_norm = static_cast<float>(a.max_norm);
+    r.norm_eps = static_cast<float>(a.norm_eps);
+    r.lr_dev = a.lr_dev;
+    r.step_dev = a.step_dev;
+    r.norm = a.norm;
+    auto run = [&](auto small) {
+        constexpr int N = decltype(small)::value;
+        auto kernel = l.bits == 8 ? adamw_kernel<8, N> : adamw_kernel<32, N>;
+        return each_table<N>(l, nullptr, nullptr, [&](const Table<N>& t, dim3 grid) { return launch(kernel, grid, dim3(kThreads), 0, s, t, r); });
+    };
+    return l.n <= 12 ? run(std::integral_constant<int, 12>{}) : run(std::integral_constant<int, kTensors>{});
+}
+
+hipError_t launch_adamw_moments(const AdamList& l, float* const* m_out, float* const* v_out, hipStream_t s)
+{
+    auto run = [&](auto small) {
+        constexpr int N = decltype(small)::value;
+        return each_table<N>(l, m_out, v_out, [&](const Table<N>& t, dim3 grid) { return launch(moments_kernel<N>, grid, dim3(kThreads), 0, s, t); });
+    };
+    return l.n <= 12 ? run(std::integral_constant<int, 12>{}) : run(std::integral_constant<int, kTensors>{});
+}
+
+}  // namespace convmi

@@ -1,67 +1,19 @@
 // C ABI of the operators around a convolution: argument checks and launches of
 // the gated feed-forward layer, the block norms and gradient clipping.  Every
 // check runs on the host before anything is launched.
-#include "act.hpp"
-#include "convmi.h"
-#include "kernels.hpp"
+#include "checks.hpp"
 
-#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <memory>
 #include <new>
 
+using namespace convmi::checks;
 using convmi::fail;
 
 static_assert(convmi::kActs == CONV_ACT_TANH + 1, "the activations of the header");
 
 namespace {
-
-constexpr int kMaxWidth = 1 << 20;  // channels of a row
-
-bool off(const void* p, size_t align) { return (reinterpret_cast<uintptr_t>(p) & (align - 1)) != 0; }
-
-int check_dtype(const char* op, int dtype)
-{
-    if (dtype != CONV_F32 && dtype != CONV_BF16)
-        return fail(CONV_ERR_INVALID_ARG, "%s: dtype must be CONV_F32 or CONV_BF16, got %d", op, dtype);
-    return CONV_OK;
-}
-
-int check_sizes(const char* op, long long rows, long long C, const char* name)
-{
-    if (rows < 0 || C < 1)
-        return fail(CONV_ERR_INVALID_ARG, "%s: rows must be >= 0 and %s >= 1 (got %lld, %lld)", op, name, rows, C);
-    if (rows > INT32_MAX || C > kMaxWidth)
-        return fail(CONV_ERR_OVERFLOW, "%s: rows must be below 2^31 and %s at most 2^20 (got %lld, %lld)", op, name, rows, C);
-    return CONV_OK;
-}
-
-int check_aligned(const char* op, std::initializer_list<const void*> tensors, size_t align)
-{
-    for (const void* p : tensors)
-        if (off(p, align))
-            return fail(CONV_ERR_INVALID_ARG, "%s: a tensor is not aligned to its %zu-byte elements", op, align);
-    return CONV_OK;
-}
-
-int check_workspace(const char* op, const void* workspace, size_t bytes, size_t need)
-{
-    if (bytes < need || (need > 0 && (!workspace || off(workspace, 16))))
-        return fail(CONV_ERR_INVALID_ARG, "%s: needs a 16-byte aligned workspace of %zu bytes (got %zu)", op, need, bytes);
-    return CONV_OK;
-}
-
-int launched(hipError_t e, const char* op)
-{
-    return e == hipSuccess ? CONV_OK : fail(CONV_ERR_HIP, "%s: launch failed: %s", op, hipGetErrorString(e));
-}
-
-int check_act(const char* op, int act)
-{
-    if (act < 0 || act >= convmi::kActs) return fail(CONV_ERR_INVALID_ARG, "%s: %d is not a conv_act_t", op, act);
-    return CONV_OK;
-}
 
 int check_gated(const char* op, long long rows, int C, int F, int act, int dtype)
 {
@@ -94,12 +46,6 @@ int check_norm(const char* op, const convmi::NormArgs& a, long long rows, int C,
                               a.dz, a.ds, a.dpost_w, a.dpost_b, a.dpre_w, a.dpre_b}, dtype == CONV_F32 ? 4 : 2);
 }
 
-// The memory of one tensor of a list.
-struct Span {
-    uintptr_t at, end;
-    bool written;
-};
-
 // Clipping writes a list's outputs in any order, many workgroups at a time: none
 // may overlap another output, or a gradient but the one it replaces.  A list of
 // 600 tensors takes 15 us.
@@ -122,14 +68,7 @@ int check_apart(const char* op, const void* const* grads, void* const* outs, con
         s[m++] = Span{to, to + bytes, true};
         if (from != to) s[m++] = Span{from, from + bytes, false};
     }
-    std::sort(s, s + m, [](const Span& a, const Span& b) { return a.at < b.at; });
-    uintptr_t any = 0, written = 0;  // how far the spans up to here reach
-    for (int i = 0; i < m; ++i) {
-        if (s[i].at < (s[i].written ? any : written))
-            return fail(CONV_ERR_INVALID_ARG, "%s: an output overlaps another output or another gradient", op);
-        any = std::max(any, s[i].end);
-        if (s[i].written) written = std::max(written, s[i].end);
-    }
+    if (!spans_apart(s, m)) return fail(CONV_ERR_INVALID_ARG, "%s: an output overlaps another output or another gradient", op);
     return CONV_OK;
 }
 

@@ -149,4 +149,71 @@ size_t clip_workspace(int n);
 hipError_t launch_clip(const void* const* src, void* const* dst, const size_t* counts, const int* dtypes, int n,
                        float max_norm, float eps, float* norm, void* workspace, hipStream_t s);
 
+// Short causal convolution along a sequence (see conv_causal_fwd /
+// conv_causal_bwd / conv_causal_step).
+constexpr int kCausalTaps = 8;         // taps at most
+struct CausalArgs {
+    const void *x, *w, *bias, *initial, *dy, *dlast;
+    const int *starts, *slots;
+    void *y, *last, *state, *dx, *dinitial;
+    float *part_w, *part_b;            // gradient: partial sums
+    int64_t rows, len, xs;             // len: rows of each sequence, without starts; xs: elements from one row of x to the next
+    int per;                           // rows of a range
+    int seqs, C, K, act, clear;
+};
+size_t causal_bwd_workspace(int64_t rows, int C, int K);
+hipError_t launch_causal_fwd(CausalArgs a, int dtype, hipStream_t s);
+hipError_t launch_causal_bwd(CausalArgs a, void* dw, void* db, int dtype, void* workspace, hipStream_t s);
+hipError_t launch_causal_step(const CausalArgs& a, int count, int dtype, hipStream_t s);
+
+// Selective state space scan (see conv_scan_fwd / conv_scan_bwd / conv_scan_step).
+constexpr int kScanTile = 16;          // rows between two states kept for the gradient
+constexpr int kScanStates = 64;        // states of a channel at most
+struct ScanArgs {
+    const void *x, *delta, *B, *C, *z, *dy;
+    const float *A, *D, *bias, *initial, *dlast;
+    const int *starts, *slots;
+    void *y, *dx, *ddelta, *dB, *dC, *dz;
+    float *last, *saved, *dinitial;
+    // workspace
+    float *ends, *sums;                // a piece's state at its end (or its gradient's at its begin), and sum of d
+    float *part_bc, *part_a, *part_d, *part_bias;
+    int64_t rows, len;                 // len: rows of each sequence, without starts
+    int64_t xs, ds, zs, bs, cs;        // elements from one row to the next
+    int64_t piece_rows;
+    int seqs, channels, n, groups, per_group;
+    int blocks;                        // workgroups of a group's channels
+    int pieces;                        // 0: a workgroup a sequence
+    int softplus, act, clear;          // clear: rows of no sequence become zeros
+};
+struct ScanGrads {
+    float *dA, *dD, *dbias;
+};
+size_t scan_saved(int64_t rows, int channels, int n);
+// `packed`: the sequences' rows are known to the device alone.
+size_t scan_fwd_workspace(const ScanArgs& a, bool packed);
+size_t scan_bwd_workspace(const ScanArgs& a, bool packed, bool saved);
+hipError_t launch_scan_fwd(ScanArgs a, int dtype, void* workspace, hipStream_t s);
+hipError_t launch_scan_bwd(ScanArgs a, const ScanGrads& g, int dtype, void* workspace, hipStream_t s);
+hipError_t launch_scan_step(const ScanArgs& a, float* state, int count, int dtype, hipStream_t s);
+
+// AdamW over a list of tensors (see conv_adamw).
+struct AdamList {
+    void *const *params, *const *m, *const *v, *const *copies;
+    const void* const* grads;
+    float *const *m_scales, *const *v_scales;
+    const size_t* counts;
+    const int *param_dtypes, *grad_dtypes, *copy_dtypes;
+    int n, bits;
+};
+struct AdamRates {
+    double lr, beta1, beta2, eps, weight_decay, max_norm, norm_eps;
+    long long step;
+    const float *lr_dev, *norm;
+    const long long* step_dev;
+};
+constexpr int kAdamBlock = 128;        // elements that share a scale of 8-bit states
+hipError_t launch_adamw(const AdamList& l, const AdamRates& r, hipStream_t s);
+hipError_t launch_adamw_moments(const AdamList& l, float* const* m_out, float* const* v_out, hipStream_t s);
+
 }  // namespace convmi

@@ -1,0 +1,365 @@
+// Gradient of the selective scan, for one type: included by the sources that
+// build it for bf16 and for fp32.
+//
+// With G[t] the gradient of h[t] (from y[t] and from h[t + 1]):
+//   G[t] = C[t] dy[t] + a[t + 1] G[t + 1],   q[t] = a[t] G[t] h[t - 1],
+//   dA = sum_t d q,   dd = sum_n A q + x sum_n B G,   dx = d sum_n B G + D dy,
+//   dB = sum_channels d x G,   dC = sum_channels dy h,
+// dy being the gradient behind the gate, dz = dout y act'(z).
+//
+// A tile's states come again from the state in front of it (the forward pass
+// keeps one every 16 rows, 4 bytes a state of a row; going back by dividing by a
+// would not be stable) and stay in registers, factors too, so a tile costs one
+// exp2 a state and row.  Then the tile goes backwards.  About 20 issue slots a
+// state and row, four of them the sums over channels of dB and dC, which are
+// merged over a wave's lanes in pairs, over the workgroup's waves in LDS and
+// over workgroups by a kernel of their own: no atomics, so a fixed order.
+#pragma once
+
+#include "scan.hpp"
+
+namespace convmi {
+namespace scan {
+
+constexpr int pow2_of(int v)
+{
+    int p = 1;
+    while (p < v) p *= 2;
+    return p;
+}
+constexpr float kLn2 = 0.69314718055994531f;
+
+// What the pieces behind a share give to the gradient of its last state.
+template <int GR, int NS>
+__device__ __forceinline__ void inherit_back(const ScanArgs& a, const Lanes<GR, NS>& l, const float* A, int item, int64_t end, float* g)
+{
+    const int64_t states = static_cast<int64_t>(a.channels) * a.n;
+    float passed = 0.f;
+    for (int q = item + 1; q < a.pieces; ++q) {
+        float e[NS];
+        l.read(a, a.ends + q * states, e);
+        const float sum = a.sums[static_cast<int64_t>(q) * a.channels + l.c];
+#pragma unroll
+        for (int j = 0; j < NS; ++j) g[j] = __builtin_fmaf(exp2_hw(A[j] * passed), e[j], g[j]);
+        passed += sum;
+        if (end <= (q + 1) * a.piece_rows) break;  // the sequence ends in that piece
+    }
+}
+
+// The gradient that a piece passes on to the row before it, from nothing behind
+// it, for the pieces in front.
+template <typename T, int GR, int NS>
+__global__ __launch_bounds__(kThreads) void back_kernel(ScanArgs a)
+{
+    typedef Lanes<GR, NS> L;
+    constexpr int CH = L::CH, R = L::R, NP = L::NP;
+    __shared__ float2 lds_d[kWaves][kTile][CH];
+    __shared__ float lds_b[kWaves][kTile * NP], lds_c[kWaves][kTile * NP];
+    const uint32_t cb = static_cast<uint32_t>(a.groups) * a.blocks;
+    const int item = static_cast<int>(blockIdx.x / cb);
+    const L l(a, blockIdx.x % cb);
+    const Share share(a, item);
+    if (share.first >= share.last) return;
+    const int s = share.first;
+    const Span span = span_of(a, s);
+    if (span.begin >= share.begin) return;  // no sequence comes from the piece before
+    float2(*dd)[CH] = lds_d[l.wave];
+    float *sb = lds_b[l.wave], *sc = lds_c[l.wave];
+    float A[NS], g[NS];
+    l.read(a, a.A, A);
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+        A[j] *= kLog2e;
+        g[j] = 0.f;
+    }
+    const float bias = a.bias ? a.bias[l.c] : 0.f;
+    const int64_t states = static_cast<int64_t>(a.channels) * a.n;
+    if (span.end <= share.end && a.dlast) l.read(a, a.dlast + s * states, g);
+    int64_t at = span.end < share.end ? span.end : share.end;
+    float total = 0.f;
+    T dl[R], z[R], dy[R];
+    Shared<T, GR, NS> bc;
+    while (at > share.begin) {
+        int64_t row0 = (at - 1) & ~static_cast<int64_t>(kTile - 1);
+        const int rows = static_cast<int>(at - row0);
+        at = row0;
+        load_rows(l, a.delta, a.ds, row0, rows, dl);
+        load_rows(l, a.dy, a.channels, row0, rows, dy);
+        if (a.z) load_rows(l, a.z, a.zs, row0, rows, z);
+        bc.load(a, l, row0, rows);
+        float d[R], dv[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int r = i * GR + l.row;
+            d[i] = load_f(&dl[i]) + bias;
+            if (a.softplus) d[i] = softplus<false>(d[i]).v;
+            if (r >= rows) d[i] = 0.f;
+            dv[i] = load_f(&dy[i]);
+        }
+        if (a.z)
+            with_act(a.act, [&](auto kind) __attribute__((always_inline)) {
+#pragma unroll
+                for (int i = 0; i < R; ++i) dv[i] *= act_value<kind()>(load_f(&z[i]));
+            });
+        wave_fence();
+#pragma unroll
+        for (int i = 0; i < R; ++i) dd[i * GR + l.row][l.ch] = make_float2(d[i], i * GR + l.row < rows ? dv[i] : 0.f);
+        bc.put(l, sb, sc);
+        wave_fence();
+#pragma unroll
+        for (int r = kTile - 1; r >= 0; --r) {
+            const float2 v = dd[r][l.ch];
+            const float* c = sc + r * NP + l.n0;
+            total += v.x;
+#pragma unroll
+            for (int j = 0; j < NS; ++j) g[j] = __builtin_fmaf(c[j], v.y, g[j]) * exp2_hw(v.x * A[j]);
+        }
+    }
+    l.write(a, a.ends + item * states, g);
+    if (l.grp == 0 && l.on) a.sums[static_cast<int64_t>(item) * a.channels + l.c] = total;
+}
+
+template <typename T, int GR, int NS>
+__global__ __launch_bounds__(kThreads) void bwd_kernel(ScanArgs a)
+{
+    typedef Lanes<GR, NS> L;
+    constexpr int CH = L::CH, R = L::R, NP = L::NP;
+    constexpr int V = pow2_of(2 * NS);                                   // values of dB and dC a row, padded
+    constexpr int RB = CH / V < 1 ? 1 : CH / V > GR ? GR : CH / V;       // rows merged at once
+    constexpr int K = V * RB, KEPT = K > CH ? K / CH : 1;
+    __shared__ float4 lds_d[kWaves][kTile][CH];
+    __shared__ float lds_b[kWaves][kTile * NP], lds_c[kWaves][kTile * NP];
+    __shared__ float lds_part[2][kWaves][kTile * 2 * NP];
+
+    const uint32_t cb = static_cast<uint32_t>(a.groups) * a.blocks, block = blockIdx.x % cb;
+    const int item = static_cast<int>(blockIdx.x / cb);
+    const L l(a, block);
+    const Share share(a, item);
+    float4(*dd)[CH] = lds_d[l.wave];
+    float *sb = lds_b[l.wave], *sc = lds_c[l.wave];
+    int mine = 0;  // which of the merged values this lane holds
+#pragma unroll
+    for (int b = 1, to = CH / 2; b < CH; b <<= 1, to >>= 1) mine += (l.ch & b) ? to : 0;
+
+    float A[NS], g[NS], dA[NS];
+    l.read(a, a.A, A);
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+        A[j] *= kLog2e;
+        dA[j] = 0.f;
+    }
+    const float bias = a.bias ? a.bias[l.c] : 0.f, skip = a.D ? a.D[l.c] : 0.f;
+    const int64_t states = static_cast<int64_t>(a.channels) * a.n;
+    float dskip = 0.f, dbias = 0.f;
+    int turn = 0;
+
+    for (int s = share.last - 1; s >= share.first; --s) {
+        const Span span = span_of(a, s);
+#pragma unroll
+        for (int j = 0; j < NS; ++j) g[j] = 0.f;
+        if (span.end <= share.end) {
+            if (a.dlast) l.read(a, a.dlast + s * states, g);
+        } else {
+            inherit_back(a, l, A, item, span.end, g);
+        }
+        const int64_t begin = span.begin > share.begin ? span.begin : share.begin;
+        int64_t at = span.end < share.end ? span.end : share.end;
+        T x[R], dl[R], z[R], dy[R];
+        float entry[NS];
+        Shared<T, GR, NS> bc;
+        auto begin_of = [&](int64_t to) {
+            const int64_t v = (to - 1) & ~static_cast<int64_t>(kTile - 1);
+            return v > begin ? v : begin;
+        };
+        auto fetch = [&](int64_t to) __attribute__((always_inline)) {
+            const int64_t row0 = begin_of(to);
+            const int rows = static_cast<int>(to - row0);
+            load_rows(l, a.x, a.xs, row0, rows, x);
+            load_rows(l, a.delta, a.ds, row0, rows, dl);
+            load_rows(l, a.dy, a.channels, row0, rows, dy);
+            if (a.z) load_rows(l, a.z, a.zs, row0, rows, z);
+            bc.load(a, l, row0, rows);
+            if (row0 > span.begin) l.read(a, a.saved + row0 / kTile * states, entry);
+            else if (a.initial) l.read(a, a.initial + s * states, entry);
+            else
+#pragma unroll
+                for (int j = 0; j < NS; ++j) entry[j] = 0.f;
+        };
+        if (at > begin) fetch(at);
+        while (at > begin) {
+            const int64_t row0 = begin_of(at);
+            const int rows = static_cast<int>(at - row0);
+            at = row0;
+            // ------------------------------------------ the tile's rows --
+            float xf[R], d[R], sig[R], dv[R], dz[R];
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int r = i * GR + l.row;
+                xf[i] = load_f(&x[i]);
+                dz[i] = dv[i] = load_f(&dy[i]);
+                const float raw = load_f(&dl[i]) + bias;
+                const Step p = a.softplus ? softplus<true>(raw) : Step{raw, 1.0f};
+                d[i] = r < rows ? p.v : 0.f;  // a row that is not there changes nothing
+                sig[i] = p.d;
+            }
+            if (a.z)
+                with_act(a.act, [&](auto kind) __attribute__((always_inline)) {
+#pragma unroll
+                    for (int i = 0; i < R; ++i) {
+                        const ActPair p = act_pair<kind()>(load_f(&z[i]));
+                        dz[i] = dv[i] * p.d;
+                        dv[i] *= p.v;
+                    }
+                });
+            wave_fence();
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const bool there = i * GR + l.row < rows;
+                dd[i * GR + l.row][l.ch] = make_float4(d[i], d[i] * xf[i], there ? dv[i] : 0.f, 0.f);
+            }
+            bc.put(l, sb, sc);
+            wave_fence();
+            float first[NS];
+#pragma unroll
+            for (int j = 0; j < NS; ++j) first[j] = entry[j];
+            if (at > begin) fetch(at);
+            // ------------------------------------------- states again --
+            float hs[kTile][NS], as[kTile][NS];
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                float v[GR];
+#pragma unroll
+                for (int r = 0; r < GR; ++r) {
+                    const int t = i * GR + r;
+                    const float2 w = *reinterpret_cast<const float2*>(&dd[t][l.ch]);
+                    const float *b = sb + t * NP + l.n0, *c = sc + t * NP + l.n0;
+                    v[r] = 0.f;
+#pragma unroll
+                    for (int j = 0; j < NS; ++j) {
+                        as[t][j] = exp2_hw(w.x * A[j]);
+                        hs[t][j] = __builtin_fmaf(as[t][j], t ? hs[t ? t - 1 : 0][j] : first[j], w.y * b[j]);
+                        v[r] = __builtin_fmaf(hs[t][j], c[j], v[r]);
+                    }
+                }
+                merge_all<32, CH, GR>(v);
+                dz[i] *= __builtin_fmaf(skip, xf[i], v[0]);
+            }
+            // ------------------------------------------------- and back --
+            float* part = lds_part[turn][l.wave];
+            float da[NS], ddelta[R], dx[R];
+#pragma unroll
+            for (int j = 0; j < NS; ++j) da[j] = 0.f;
+#pragma unroll
+            for (int i = R - 1; i >= 0; --i) {
+                float w[GR], u[GR], m[K];
+#pragma unroll
+                for (int r = GR - 1; r >= 0; --r) {
+                    const int t = i * GR + r, in = r % RB;
+                    const float4 v = dd[t][l.ch];
+                    const float *b = sb + t * NP + l.n0, *c = sc + t * NP + l.n0;
+                    w[r] = u[r] = 0.f;
+#pragma unroll
+                    for (int j = 0; j < NS; ++j) {
+                        const float e = __builtin_fmaf(c[j], v.z, g[j]);
+                        m[in * V + j] = e * v.y;
+                        m[in * V + NS + j] = v.z * hs[t][j];
+                        w[r] = __builtin_fmaf(e, b[j], w[r]);
+                        g[j] = e * as[t][j];
+                        const float q = g[j] * (t ? hs[t ? t - 1 : 0][j] : first[j]);
+                        u[r] = __builtin_fmaf(A[j], q, u[r]);
+                        da[j] = __builtin_fmaf(v.x, q, da[j]);
+                    }
+#pragma unroll
+                    for (int j = 2 * NS; j < V; ++j) m[in * V + j] = 0.f;
+                    if (in == 0) {
+                        merge_all<CH / 2, 1, K>(m);
+#pragma unroll
+                        for (int k = 0; k < KEPT; ++k) {
+                            const int at_v = mine + k * CH, row = t + at_v / V, val = at_v % V;
+                            if (at_v < K && val < 2 * NS)
+                                part[row * 2 * NP + (val < NS ? l.n0 + val : NP + l.n0 + val - NS)] = m[k];
+                        }
+                    }
+                }
+                merge_all<32, CH, GR>(w);
+                merge_all<32, CH, GR>(u);
+                ddelta[i] = (u[0] * kLn2 + w[0] * xf[i]) * sig[i];
+                dx[i] = __builtin_fmaf(w[0], d[i], skip * dv[i]);
+                if (i * GR + l.row < rows) {
+                    dskip = __builtin_fmaf(dv[i], xf[i], dskip);
+                    dbias += ddelta[i];
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < NS; ++j) dA[j] += da[j];
+            if (a.dx) store_rows<T>(l, a.dx, a.channels, row0, rows, dx);
+            if (a.ddelta) store_rows<T>(l, a.ddelta, a.channels, row0, rows, ddelta);
+            if (a.dz) store_rows<T>(l, a.dz, a.channels, row0, rows, dz);
+            // The workgroup's sum of dB and dC; the other half of the buffer
+            // is the next tile's, so one barrier a tile is enough.
+            __syncthreads();
+            float* out = a.part_bc + (static_cast<int64_t>(block) * a.rows + row0) * 2 * a.n;
+            for (int e = threadIdx.x; e < rows * 2 * NP; e += kThreads) {
+                const int row = e / (2 * NP), in = e % (2 * NP), n = in % NP;
+                if (n < a.n) {
+                    const float* p = &lds_part[turn][0][e];
+                    out[(row * 2 + in / NP) * a.n + n] = (p[0] + p[kTile * 2 * NP]) + (p[2 * kTile * 2 * NP] + p[3 * kTile * 2 * NP]);
+                }
+            }
+            turn ^= 1;
+        }
+        if (a.dinitial && span.begin >= share.begin) l.write(a, a.dinitial + s * states, g);
+    }
+    l.write(a, a.part_a + item * states, dA);
+#pragma unroll
+    for (int dist = 32; dist >= CH; dist >>= 1) {
+        dskip += __shfl_xor(dskip, dist);
+        dbias += __shfl_xor(dbias, dist);
+    }
+    if (l.grp == 0 && l.on) {
+        a.part_d[static_cast<int64_t>(item) * a.channels + l.c] = dskip;
+        a.part_bias[static_cast<int64_t>(item) * a.channels + l.c] = dbias;
+    }
+    if (a.clear && a.starts) {  // rows of no sequence
+        auto clear = [&](int64_t from, int64_t to) {
+            if (a.dx) clear_rows<T>(l, a.dx, a.channels, from, to);
+            if (a.ddelta) clear_rows<T>(l, a.ddelta, a.channels, from, to);
+            if (a.dz) clear_rows<T>(l, a.dz, a.channels, from, to);
+        };
+        if (item == 0) clear(0, span_of(a, 0).begin);
+        if (share.end_of_all) clear(span_of(a, a.seqs - 1).end, a.rows);
+    }
+}
+
+// dB and dC: the sums over the workgroups of a group's channels, in order.
+template <typename T>
+__global__ __launch_bounds__(256) void sum_bc_kernel(ScanArgs a)
+{
+    const int64_t one = a.rows * 2 * a.n, at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    const int group = blockIdx.y;
+    if (at >= one) return;
+    const int64_t row = at / (2 * a.n);
+    const int in = static_cast<int>(at - row * 2 * a.n), n = in % a.n;
+    void* to = in < a.n ? a.dB : a.dC;
+    if (!to) return;
+    bool there = true;
+    if (a.starts) there = row >= span_of(a, 0).begin && row < span_of(a, a.seqs - 1).end;
+    float v = 0.f;
+    if (there) {
+        const float* p = a.part_bc + static_cast<int64_t>(group) * a.blocks * one + at;
+        constexpr int kBatch = 8;
+        for (int b = 0; b < a.blocks; b += kBatch) {
+            float t[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) t[i] = b + i < a.blocks ? p[(b + i) * one] : 0.f;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) v += t[i];
+        }
+    } else if (!a.clear) {
+        return;
+    }
+    store_f(static_cast<T*>(to) + (row * a.groups + group) * a.n + n, v);
+}
+
+}  // namespace scan
+}  // namespace convmi

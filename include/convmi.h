@@ -519,6 +519,195 @@ int conv_grad_clip(const void *const *grads, void *const *outs,
  * only. */
 int conv_grad_workspace_size(int n, size_t *bytes);
 
+/* ------------------------------------------------------------------------
+ * Operators along a sequence: the short causal convolution and the selective
+ * state space scan, on channels-last rows (prompts, tokens, packed sequences).
+ *
+ * Sequences.  `rows` rows hold `seqs` sequences one after another: all of
+ * rows / seqs rows (starts NULL; seqs then divides rows), or sequence s of
+ * rows starts[s] up to starts[s + 1], `starts` being seqs + 1 non-decreasing
+ * int32 values on the device (empty sequences are allowed; values are not
+ * checked, but no row outside the tensors is touched).  Rows in front of the
+ * first sequence or behind the last one belong to none: their outputs are left
+ * as they were, or with `clear` != 0 become zeros.
+ * Strides.  The rows of x, delta, z, B and C may lie apart (a part of a wider
+ * projection): x_stride and its like count elements from one row to the next,
+ * at least the row's own and below 2^24.  All other tensors are dense.
+ * Ownership, execution, error reporting, alignment and the rounding of outputs
+ * are as above.  An output that overlaps an input or another output is refused
+ * (CONV_ERR_INVALID_ARG).  Sizes of a sequence's dimension: rows below 2^31, channels
+ * at most 2^20 (CONV_ERR_OVERFLOW).
+ */
+
+/*
+ * Short causal convolution of each channel, with an activation:
+ *   y[t] = act(bias + sum_{k < K} w[k] x[t - K + 1 + k]),
+ * rows before a sequence's first row taken from `initial`, zeros without it.
+ *   x [rows, C], w [C, K] (a depthwise conv1d weight), bias [C] or NULL,
+ *   2 <= K <= 8;  y [rows, C].
+ *   initial : [seqs, K - 1, C] or NULL.  last : [seqs, K - 1, C] that receives
+ *   the last K - 1 rows of each sequence with those before it, or NULL.
+ */
+int conv_causal_fwd(const void *x, const void *w, const void *bias,
+                    const int *starts, const void *initial, void *y,
+                    void *last, long long rows, int seqs, int C, int K,
+                    long long x_stride, int act, int clear, int dtype,
+                    void *stream);
+
+/*
+ * Gradient of conv_causal_fwd from dy [rows, C] and dlast [seqs, K - 1, C]
+ * (the gradient of `last`, NULL for zeros): dx [rows, C], dw [C, K], dbias
+ * [C], dinitial [seqs, K - 1, C]; any may be NULL.  The outputs before the
+ * activation are computed again.
+ *   workspace : 16-byte aligned, at least conv_causal_bwd_workspace_size bytes.
+ */
+int conv_causal_bwd(const void *dy, const void *dlast, const void *x,
+                    const void *w, const void *bias, const int *starts,
+                    const void *initial, void *dx, void *dw, void *dbias,
+                    void *dinitial, void *workspace, size_t workspace_bytes,
+                    long long rows, int seqs, int C, int K, long long x_stride,
+                    int act, int clear, int dtype, void *stream);
+
+/* Workspace bytes of conv_causal_bwd.  Host only. */
+int conv_causal_bwd_workspace_size(long long rows, int C, int K, int dtype,
+                                   size_t *bytes);
+
+/*
+ * One row each of many sequences: the K - 1 rows before row r lie in
+ * state[slots[r]], which moves on by the row.
+ *   x, y [rows, C];  state [count, K - 1, C], updated in place;
+ *   slots : rows int32 values on the device, or NULL for slots[r] = r.
+ *   A slot outside [0, count) marks a row without a sequence: its output is
+ *   left as it was (zeros with `clear`).  Rows of the same slot are taken in
+ *   their order, as consecutive rows of one sequence.
+ */
+int conv_causal_step(const void *x, const void *w, const void *bias,
+                     void *state, const int *slots, void *y, long long rows,
+                     int count, int C, int K, long long x_stride, int act,
+                     int clear, int dtype, void *stream);
+
+/*
+ * Selective state space scan: for every channel c with n < N states, along
+ * each sequence,
+ *   d[t] = softplus(delta[t] + delta_bias)   (softplus 0: without it),
+ *   h[t, n] = exp(d[t] A[n]) h[t - 1, n] + d[t] B[t, n] x[t],
+ *   y[t] = (sum_n C[t, n] h[t, n] + D x[t]) * act(z[t]),
+ * h before the first row from `initial`, zeros without it.
+ *   x, delta, z, y [rows, channels]; z NULL: no gate (act unused).
+ *   B, C [rows, groups, N]: `groups` divides channels, consecutive
+ *   channels / groups channels share a group.
+ *   A [channels, N], D, delta_bias [channels] (or NULL): fp32, finite.
+ *   initial, last : fp32 [seqs, channels, N], the state before each sequence
+ *   and the one behind it; either may be NULL.
+ *   saved : receives states for conv_scan_bwd, conv_scan_saved_size bytes; NULL
+ *   to keep nothing.
+ *   workspace : 16-byte aligned, at least conv_scan_fwd_workspace_size bytes.
+ * 1 <= N <= 64.  dtype: of x, delta, z, B, C and y.  States and sums are fp32.
+ */
+int conv_scan_fwd(const void *x, const void *delta, const float *A,
+                  const void *B, const void *C, const float *D, const void *z,
+                  const float *delta_bias, const int *starts,
+                  const float *initial, void *y, float *last, float *saved,
+                  void *workspace, size_t workspace_bytes, long long rows,
+                  int seqs, int channels, int N, int groups,
+                  long long x_stride, long long delta_stride,
+                  long long z_stride, long long B_stride, long long C_stride,
+                  int softplus, int act, int clear, int dtype, void *stream);
+
+/*
+ * Gradient of conv_scan_fwd from dy [rows, channels] and dlast (the gradient
+ * of `last`, NULL for zeros), with the forward call's inputs:
+ *   dx, ddelta, dz [rows, channels], dB, dC [rows, groups, N] (dtype);
+ *   dA [channels, N], dD, ddelta_bias [channels], dinitial [seqs, channels, N]
+ *   (fp32); any may be NULL (dz needs z).
+ *   saved : as conv_scan_fwd wrote it for the same inputs, or NULL: the states
+ *   are computed again.
+ *   workspace : 16-byte aligned, at least conv_scan_bwd_workspace_size bytes
+ *   for this call's choice of `saved`.
+ */
+int conv_scan_bwd(const void *dy, const float *dlast, const void *x,
+                  const void *delta, const float *A, const void *B,
+                  const void *C, const float *D, const void *z,
+                  const float *delta_bias, const int *starts,
+                  const float *initial, const float *saved, void *dx,
+                  void *ddelta, float *dA, void *dB, void *dC, float *dD,
+                  void *dz, float *ddelta_bias, float *dinitial,
+                  void *workspace, size_t workspace_bytes, long long rows,
+                  int seqs, int channels, int N, int groups,
+                  long long x_stride, long long delta_stride,
+                  long long z_stride, long long B_stride, long long C_stride,
+                  int softplus, int act, int clear, int dtype, void *stream);
+
+/* Bytes of `saved`, and of the workspaces; packed: 1 if the call has starts;
+ * saved: 1 if conv_scan_bwd is given it.  Host only. */
+int conv_scan_saved_size(long long rows, int channels, int N, size_t *bytes);
+int conv_scan_fwd_workspace_size(long long rows, int seqs, int channels, int N,
+                                 int groups, int packed, size_t *bytes);
+int conv_scan_bwd_workspace_size(long long rows, int seqs, int channels, int N,
+                                 int groups, int packed, int saved,
+                                 size_t *bytes);
+
+/*
+ * One row each of many sequences: row r's state is state[slots[r]] (fp32
+ * [count, channels, N]), updated in place; slots as in conv_causal_step, the
+ * rest as in conv_scan_fwd.
+ */
+int conv_scan_step(const void *x, const void *delta, const float *A,
+                   const void *B, const void *C, const float *D,
+                   const void *z, const float *delta_bias, float *state,
+                   const int *slots, void *y, long long rows, int count,
+                   int channels, int N, int groups, long long x_stride,
+                   long long delta_stride, long long z_stride,
+                   long long B_stride, long long C_stride, int softplus,
+                   int act, int clear, int dtype, void *stream);
+
+/* ------------------------------------------------------------------------
+ * AdamW over a list of parameters, in one pass over their memory:
+ *   c = min(1, max_norm / (norm + norm_eps))  (1 without `norm`),  g' = c g,
+ *   m' = beta1 m + (1 - beta1) g',  v' = beta2 v + (1 - beta2) g'^2,
+ *   p' = p (1 - lr weight_decay)
+ *        - lr / (1 - beta1^step) m' / (sqrt(v' / (1 - beta2^step)) + eps).
+ * p, m and v are replaced.  Host arrays of n entries, read before the call
+ * returns:
+ *   params, grads : device pointers; counts: elements (0: skipped);
+ *   param_dtypes, grad_dtypes : conv_dtype_t.
+ *   copies, copy_dtypes : where p' is written once more, rounded to its type
+ *   (weights for the forward pass beside fp32 parameters); NULL, or a NULL
+ *   entry, for none.
+ *   m, v : with bits 32 fp32 arrays of counts[i] elements.  With bits 8 one
+ *   byte an element and a scale for each block of 128 elements (m_scales,
+ *   v_scales: fp32 arrays of ceil(counts[i] / 128)):
+ *     m = scale * q * |q|, q the signed byte;  v = (scale * q^2)^2, q the
+ *     unsigned byte.
+ *   A block's scale fits its largest value to the largest byte, values go to
+ *   the nearest byte on the line of q (borders at (q + 1/2)^2 times the scale;
+ *   a positive v to 1 at least), and blocks whose largest value is below
+ *   2^-100 hold zeros.  p' is computed before m' and v' are rounded.
+ *   norm : one fp32 value on the device (conv_grad_norm's), or NULL.
+ *   lr_dev, step_dev : one fp32 and one int64 value on the device that replace
+ *   lr and step where not NULL (for a captured graph); step counts from 1.
+ * 0 <= beta < 1, 2^-126 <= eps, weight_decay >= 0, max_norm >= 0, norm_eps >=
+ * 0, all finite.  Errors: CONV_ERR_INVALID_ARG (a null or misaligned pointer, a
+ * value out of range, what is written overlapping anything else),
+ * CONV_ERR_OVERFLOW (a count of 2^38 or more), CONV_ERR_HIP.
+ */
+int conv_adamw(void *const *params, const void *const *grads, void *const *m,
+               void *const *v, float *const *m_scales, float *const *v_scales,
+               void *const *copies, const size_t *counts,
+               const int *param_dtypes, const int *grad_dtypes,
+               const int *copy_dtypes, int n, int bits, double lr,
+               double beta1, double beta2, double eps, double weight_decay,
+               long long step, const float *lr_dev, const long long *step_dev,
+               const float *norm, double max_norm, double norm_eps,
+               void *stream);
+
+/* The values that 8-bit states stand for, as fp32 arrays m_out[i], v_out[i]. */
+int conv_adamw_moments(const void *const *m, const void *const *v,
+                       const float *const *m_scales,
+                       const float *const *v_scales, float *const *m_out,
+                       float *const *v_out, const size_t *counts, int n,
+                       void *stream);
+
 /* Message describing the last failure on the calling thread ("" if none). */
 const char *conv_last_error(void);
 
