@@ -15,29 +15,42 @@ size_t up(size_t n) { return (n + 15) & ~size_t(15); }
 // Workgroups that one range of rows gives with GR groups of lanes.
 int64_t blocks_of(const ScanArgs& a, int gr) { return (a.per_group + kWaves * (64 / gr) - 1) / (kWaves * (64 / gr)); }
 
-// Groups of lanes and states of a lane: four groups hold up to 16 states, the
-// fewest instructions a row (its LDS reads and merges are shared by four
-// states).  Pieces of the rows where the sequences alone leave the device
-// empty, or where their lengths are the device's own knowledge.
+// Groups of lanes, states of a lane, and pieces of the rows.
+//
+// Few groups cost the fewest instructions: a row's LDS reads and merges are
+// shared by more states of a lane.  But one wave on a SIMD cannot fill it (an exp2
+// with four multiply-adds takes 31 cycles there, 23 with two waves, 20 with eight), so with
+// less than two waves for each SIMD twice the groups are better (4 x 4096 rows of 4096
+// channels, 16 states: 395 us with 4 groups, 376 with 8), and the gradient, whose
+// 256 registers leave room for two waves in any case, always takes them (8 x 2048 rows of
+// 2048 channels, forward and gradient: 832 us and 788).  With less than one wave for each SIMD
+// the rows are cut into pieces, which cost a pass more over them (16384 rows of 1024
+// channels: 146 us in pieces, 280 in whole).  So are packed rows always: their
+// lengths are the device's own knowledge, and one long sequence among short ones
+// would otherwise keep a few waves busy alone.
 struct Plan {
     int gr, ns;
 };
-Plan plan(ScanArgs& a, bool packed)
+constexpr int64_t kSimds = 1024;
+int64_t waves_of(const ScanArgs& a, int gr) { return static_cast<int64_t>(a.groups) * blocks_of(a, gr) * kWaves; }  // of a range of rows
+
+Plan plan(ScanArgs& a, bool packed, bool gradient)
 {
+    const int few = a.n <= 16 ? 4 : a.n <= 32 ? 8 : 16, many = few == 4 ? 8 : few;
+    const bool whole = a.rows == 0 || (!packed && a.seqs * waves_of(a, many) >= kSimds);
     Plan p;
-    p.gr = a.n <= 16 ? 4 : a.n <= 32 ? 8 : 16;
+    p.gr = gradient || (whole && a.seqs * waves_of(a, few) < 2 * kSimds) ? many : few;
     p.ns = (a.n + p.gr - 1) / p.gr;
     a.blocks = static_cast<int>(blocks_of(a, p.gr));
-    const int64_t one = static_cast<int64_t>(a.groups) * a.blocks * kWaves;  // waves of a range of rows
-    constexpr int64_t kFill = 2048;                                        // two waves for each SIMD
-    const int64_t want = std::min<int64_t>((kFill + one - 1) / one, (a.rows + 63) / 64);
     a.pieces = 0;
     a.piece_rows = 0;
-    if (a.rows > 0 && (packed || (a.seqs < want && one * a.seqs < kFill / 2))) {
-        const int64_t rows = (a.rows + want - 1) / want;
-        a.piece_rows = (rows + kTile - 1) / kTile * kTile;
-        a.pieces = static_cast<int>((a.rows + a.piece_rows - 1) / a.piece_rows);
-    }
+    if (whole) return p;
+    // two waves for each SIMD, 64 rows in a piece at least
+    const int64_t want = std::max<int64_t>(1, std::min<int64_t>((2 * kSimds + waves_of(a, p.gr) - 1) / waves_of(a, p.gr), a.rows / 64));
+    if (!packed && want <= a.seqs) return p;
+    const int64_t rows = (a.rows + want - 1) / want;
+    a.piece_rows = (rows + kTile - 1) / kTile * kTile;
+    a.pieces = static_cast<int>((a.rows + a.piece_rows - 1) / a.piece_rows);
     return p;
 }
 
@@ -64,14 +77,14 @@ size_t scan_saved(int64_t rows, int channels, int n)
 size_t scan_fwd_workspace(const ScanArgs& args, bool packed)
 {
     ScanArgs a = args;
-    plan(a, packed);
+    plan(a, packed, false);
     return ends_bytes(a);
 }
 
 size_t scan_bwd_workspace(const ScanArgs& args, bool packed, bool saved)
 {
     ScanArgs a = args;
-    plan(a, packed);
+    plan(a, packed, true);
     const size_t cb = static_cast<size_t>(a.groups) * a.blocks, n = items(a);
     return (saved ? 0 : up(scan_saved(a.rows, a.channels, a.n))) + ends_bytes(a) + up(cb * a.rows * 2 * a.n * 4) +
            up(n * a.channels * a.n * 4) + 2 * up(n * a.channels * 4);
@@ -80,7 +93,7 @@ size_t scan_bwd_workspace(const ScanArgs& args, bool packed, bool saved)
 hipError_t launch_scan_fwd(ScanArgs a, int dtype, void* workspace, hipStream_t s)
 {
     if (a.seqs == 0) return hipSuccess;
-    const Plan p = plan(a, a.starts != nullptr);
+    const Plan p = plan(a, a.starts != nullptr, false);
     const bool passes = a.pieces > 1;
     if (passes) take_ends(a, static_cast<char*>(workspace));
     auto go = dtype ? scan_kernels_bf16 : scan_kernels_f32;
@@ -95,7 +108,7 @@ hipError_t launch_scan_fwd(ScanArgs a, int dtype, void* workspace, hipStream_t s
 
 hipError_t launch_scan_bwd(ScanArgs a, const ScanGrads& g, int dtype, void* workspace, hipStream_t s)
 {
-    const Plan p = plan(a, a.starts != nullptr);
+    const Plan p = plan(a, a.starts != nullptr, true);
     const bool passes = a.pieces > 1, again = !a.saved;
     char* at = static_cast<char*>(workspace);
     if (again) {

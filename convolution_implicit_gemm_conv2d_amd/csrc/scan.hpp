@@ -22,16 +22,18 @@ constexpr int kTile = kScanTile;
 
 // ---------------------------------------------------------- lane exchange --
 
-template <int CTRL, int BANKS>
-__device__ __forceinline__ float dpp_over(float old, float v)
+template <int CTRL>
+__device__ __forceinline__ float dpp_of(float v)
 {
-    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, old), __builtin_bit_cast(int, v), CTRL, 0xf, BANKS, false));
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
 }
 
-// Lanes whose bit DIST is 0 receive u of themselves and of their partner (the
-// lane at distance DIST), the others v: two sums over a pair of lanes for the
-// price of one.  Log2 of a span such steps sum as many values over its lanes.
-template <int DIST>
+// Lanes whose bit DIST is 0 receive u of themselves and of a partner whose bit
+// is 1, the others v: two sums over a pair of lanes for the price of one.  Log2
+// of a span such steps sum as many values over its lanes.  The partner is the
+// lane at distance DIST; of 4, the mirrored lane of eight, which is as good
+// where the steps below follow (MIRROR).
+template <int DIST, bool MIRROR>
 __device__ __forceinline__ float merge(float u, float v)
 {
     if constexpr (DIST == 32) {
@@ -40,14 +42,15 @@ __device__ __forceinline__ float merge(float u, float v)
     } else if constexpr (DIST == 16) {
         const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(u), __float_as_uint(v), false, false);
         return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-    } else if constexpr (DIST == 8) {  // row_ror:8
-        return dpp_over<0x128, 0x3>(v, u) + dpp_over<0x128, 0xc>(u, v);
-    } else if constexpr (DIST == 4) {  // row_shl:4, row_shr:4
-        return dpp_over<0x104, 0x5>(v, u) + dpp_over<0x114, 0xa>(u, v);
     } else {
         const bool high = (threadIdx.x & DIST) != 0;
         const float mine = high ? v : u, other = high ? u : v;
-        return mine + dpp_over<DIST == 2 ? 0x4e : 0xb1, 0xf>(other, other);  // quad_perm
+        if constexpr (DIST == 8) return mine + dpp_of<0x128>(other);              // row_ror:8
+        else if constexpr (DIST == 4 && MIRROR) return mine + dpp_of<0x141>(other);  // row_half_mirror
+        else if constexpr (DIST == 4) {  // row_shr:4, row_shl:4: all lanes take part in both
+            const float below = dpp_of<0x114>(other), above = dpp_of<0x104>(other);
+            return mine + (high ? below : above);
+        } else return mine + dpp_of<DIST == 2 ? 0x4e : 0xb1>(other);                // quad_perm
     }
 }
 
@@ -59,11 +62,11 @@ __device__ __forceinline__ void merge_all(float* v)
 {
     if constexpr (FIRST >= LAST) {
         if constexpr (K == 1) {
-            v[0] = merge<FIRST>(v[0], v[0]);
+            v[0] = merge<FIRST, LAST == 1>(v[0], v[0]);
             merge_all<FIRST / 2, LAST, 1>(v);
         } else {
 #pragma unroll
-            for (int i = 0; i < K / 2; ++i) v[i] = merge<FIRST>(v[2 * i], v[2 * i + 1]);
+            for (int i = 0; i < K / 2; ++i) v[i] = merge<FIRST, LAST == 1>(v[2 * i], v[2 * i + 1]);
             merge_all<FIRST / 2, LAST, K / 2>(v);
         }
     }
@@ -162,69 +165,132 @@ struct Lanes {
     }
 };
 
-// B and C of a tile, in flight to the wave's LDS.  Addresses are a base that
-// the wave shares and a 32-bit offset of the lane (the strides are below 2^24).
+// A tile: up to kTile rows, between two multiples of kTile, of a sequence and a
+// share.  The rows of the first one of [begin, end), and of the last one; 0 where
+// there are none.
+__device__ __forceinline__ int rows_from(int begin, int end)
+{
+    const int left = end - begin, room = kTile - (begin & (kTile - 1));
+    return left < room ? left : room;
+}
+__device__ __forceinline__ int rows_to(int begin, int end)
+{
+    const int left = end - begin, room = end > begin ? ((end - 1) & (kTile - 1)) + 1 : 0;
+    return left < room ? left : room;
+}
+
+// One value through a buffer resource; offsets past its end read 0 and write
+// nothing, which is all that rows, channels and states that do not exist need.
+__device__ __forceinline__ float fetch(rsrc_t r, uint32_t at, float)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0));
+}
+__device__ __forceinline__ bf16_t fetch(rsrc_t r, uint32_t at, bf16_t) { return __builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0); }
+__device__ __forceinline__ void put(rsrc_t r, uint32_t at, float v, float) { __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(int, v), r, at, 0, 0); }
+__device__ __forceinline__ void put(rsrc_t r, uint32_t at, float v, bf16_t) { __builtin_amdgcn_raw_buffer_store_b16(f_to_bf16(v), r, at, 0, 0); }
+
+// This lane's values of a tensor of rows: rows l.row, l.row + GR, ... of a tile.
+// The tensor is walked tile by tile: `at` is the next tile's first row (going
+// up) or the one behind its last (going down).
+template <typename T, int GR, int NS>
+struct Rows {
+    typedef Lanes<GR, NS> L;
+    const char* at;
+    uint32_t stride, off;  // bytes
+    __device__ Rows(const L& l, const void* p, int64_t elements, int row0)
+        : at(static_cast<const char*>(p) + row0 * elements * static_cast<int64_t>(sizeof(T))), stride(static_cast<uint32_t>(elements) * sizeof(T))
+    {
+        off = l.on ? static_cast<uint32_t>(l.row) * stride + static_cast<uint32_t>(l.c) * static_cast<uint32_t>(sizeof(T)) : kOutside;
+    }
+    template <bool UP>
+    __device__ rsrc_t tile(int rows)
+    {
+        const uint32_t bytes = static_cast<uint32_t>(rows) * stride;
+        if (!UP) at -= bytes;
+        const rsrc_t r = make_rsrc(at, bytes);
+        if (UP) at += bytes;
+        return r;
+    }
+    template <bool UP>
+    __device__ void load(int rows, T* v)
+    {
+        const rsrc_t r = tile<UP>(rows);
+#pragma unroll
+        for (int i = 0; i < L::R; ++i) v[i] = fetch(r, off + i * GR * stride, T());
+    }
+    template <bool UP>
+    __device__ void store(int rows, const float* v)
+    {
+        const rsrc_t r = tile<UP>(rows);
+#pragma unroll
+        for (int i = 0; i < L::R; ++i) put(r, off + i * GR * stride, v[i], T());
+    }
+};
+
+// B and C of a tile, in flight to the wave's LDS.
 template <typename T, int GR, int NS>
 struct Shared {
     typedef Lanes<GR, NS> L;
-    T b[L::LOADS], c[L::LOADS];
+    const char *at_b, *at_c;  // walked as Rows are
+    uint32_t bs, cs, ob, oc;  // bytes
+    int at;                   // this lane's place in a tile; -1 for lanes that do not take part
 
-    __device__ void load(const ScanArgs& a, const L& l, int64_t row0, int rows)
+    __device__ Shared(const ScanArgs& a, const L& l, int row0)
+        : at_b(static_cast<const char*>(a.B) + (row0 * a.bs + static_cast<int64_t>(l.group) * a.n) * static_cast<int64_t>(sizeof(T))),
+          at_c(static_cast<const char*>(a.C) + (row0 * a.cs + static_cast<int64_t>(l.group) * a.n) * static_cast<int64_t>(sizeof(T))), bs(static_cast<uint32_t>(a.bs) * sizeof(T)),
+          cs(static_cast<uint32_t>(a.cs) * sizeof(T))
     {
-        const T* pb = static_cast<const T*>(a.B) + row0 * a.bs + static_cast<int64_t>(l.group) * a.n;
-        const T* pc = static_cast<const T*>(a.C) + row0 * a.cs + static_cast<int64_t>(l.group) * a.n;
         const int r = l.lane / L::NP, n = l.lane % L::NP;
-        const uint32_t ob = static_cast<uint32_t>(r) * static_cast<uint32_t>(a.bs) + n, oc = static_cast<uint32_t>(r) * static_cast<uint32_t>(a.cs) + n;
-        const int have = r < L::ROWS && n < a.n ? rows - r : 0;
+        at = r < L::ROWS ? r * L::NP + n : -1;
+        const bool on = at >= 0 && n < a.n;
+        ob = on ? r * bs + n * static_cast<uint32_t>(sizeof(T)) : kOutside;
+        oc = on ? r * cs + n * static_cast<uint32_t>(sizeof(T)) : kOutside;
+    }
+    template <bool UP>
+    __device__ void load(int rows, T* b, T* c)
+    {
+        const uint32_t nb = static_cast<uint32_t>(rows) * bs, nc = static_cast<uint32_t>(rows) * cs;
+        if (!UP) at_b -= nb, at_c -= nc;
+        const rsrc_t rb = make_rsrc(at_b, nb), rc = make_rsrc(at_c, nc);
+        if (UP) at_b += nb, at_c += nc;
 #pragma unroll
         for (int i = 0; i < L::LOADS; ++i) {
-            b[i] = c[i] = T(0);
-            if (i * L::ROWS < have) {
-                b[i] = pb[ob];
-                c[i] = pc[oc];
-            }
-            pb += L::ROWS * a.bs;
-            pc += L::ROWS * a.cs;
+            b[i] = fetch(rb, ob + i * L::ROWS * bs, T());
+            c[i] = fetch(rc, oc + i * L::ROWS * cs, T());
         }
     }
-    __device__ void put(const L& l, float* to_b, float* to_c) const
+    __device__ void put(const T* b, const T* c, float* to_b, float* to_c) const
     {
-        const int at = l.lane;  // row * NP + state
+        if (at < 0) return;
 #pragma unroll
         for (int i = 0; i < L::LOADS; ++i)
-            if (at < L::ROWS * L::NP && at + i * L::ROWS * L::NP < kTile * L::NP) {
+            if ((i + 1) * L::ROWS <= kTile || at + i * L::ROWS * L::NP < kTile * L::NP) {
                 to_b[at + i * L::ROWS * L::NP] = load_f(&b[i]);
                 to_c[at + i * L::ROWS * L::NP] = load_f(&c[i]);
             }
     }
 };
 
-// This lane's values of a tensor of rows: rows l.row, l.row + GR, ... of a tile.
-template <typename T, int GR, int NS>
-__device__ __forceinline__ void load_rows(const Lanes<GR, NS>& l, const void* p, int64_t stride, int64_t row0, int rows, T* v)
+// What kGroup rows' work reads from LDS.  It is read a group ahead: the compiler
+// by itself reads just before the use and waits out the latency each time (scan of
+// 4 x 4096 rows of 4096 channels, 16 states: 391 us).
+constexpr int kGroup = 4;
+template <int NS, int G, typename D>
+struct Operands {
+    D d[G];
+    float b[G][NS], c[G][NS];
+};
+// LDS accesses do not cross this point, other instructions may.
+__device__ __forceinline__ void lds_stays() { __builtin_amdgcn_sched_barrier(0x47f); }
+
+// A barrier of the workgroup for what its waves have in LDS; loads and stores
+// of memory stay in flight.
+__device__ __forceinline__ void lds_barrier()
 {
-    const T* at = static_cast<const T*>(p) + row0 * stride;
-    const uint32_t off = static_cast<uint32_t>(l.row) * static_cast<uint32_t>(stride) + l.c;
-    const int have = l.on ? rows - l.row : 0;
-#pragma unroll
-    for (int i = 0; i < Lanes<GR, NS>::R; ++i) {
-        v[i] = T(0);
-        if (i * GR < have) v[i] = at[off];
-        at += GR * stride;
-    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    barrier_no_fence();
 }
-template <typename T, int GR, int NS>
-__device__ __forceinline__ void store_rows(const Lanes<GR, NS>& l, void* p, int64_t stride, int64_t row0, int rows, const float* v)
-{
-    T* at = static_cast<T*>(p) + row0 * stride;
-    const uint32_t off = static_cast<uint32_t>(l.row) * static_cast<uint32_t>(stride) + l.c;
-    const int have = l.on ? rows - l.row : 0;
-#pragma unroll
-    for (int i = 0; i < Lanes<GR, NS>::R; ++i) {
-        if (i * GR < have) store_f(at + off, v[i]);
-        at += GR * stride;
-    }
-}
+
 // Zeros in the rows [from, to).
 template <typename T, int GR, int NS>
 __device__ __forceinline__ void clear_rows(const Lanes<GR, NS>& l, void* p, int64_t stride, int64_t from, int64_t to)
@@ -233,31 +299,26 @@ __device__ __forceinline__ void clear_rows(const Lanes<GR, NS>& l, void* p, int6
         if (l.on) store_f(static_cast<T*>(p) + r * stride + l.c, 0.f);
 }
 
-// A tile ends at the next multiple of kTile rows, or with its sequence.
-__device__ __forceinline__ int64_t tile_end(int64_t at, int64_t end)
-{
-    const int64_t next = (at | (kTile - 1)) + 1;
-    return next < end ? next : end;
-}
-
 // ----------------------------------------------------------------- pieces --
 
-// The rows of a sequence.
+// The rows of a sequence (there are fewer than 2^31).
 struct Span {
-    int64_t begin, end;
+    int begin, end;
 };
 __device__ __forceinline__ Span span_of(const ScanArgs& a, int s)
 {
-    if (!a.starts) return {s * a.len, (s + 1) * a.len};
-    // whatever the offsets hold, the rows are the tensor's
-    int64_t b = a.starts[s], e = a.starts[s + 1];
-    b = b < 0 ? 0 : b > a.rows ? a.rows : b;
-    e = e < b ? b : e > a.rows ? a.rows : e;
+    if (!a.starts) return {static_cast<int>(s * a.len), static_cast<int>((s + 1) * a.len)};
+    // Whatever the offsets hold, the rows are the tensor's.  They are the same
+    // for all lanes, which the compiler does not see in what it loads.
+    const int rows = static_cast<int>(a.rows);
+    int b = __builtin_amdgcn_readfirstlane(a.starts[s]), e = __builtin_amdgcn_readfirstlane(a.starts[s + 1]);
+    b = b < 0 ? 0 : b > rows ? rows : b;
+    e = e < b ? b : e > rows ? rows : e;
     return {b, e};
 }
 
 // The first sequence that has rows from `row` on, or begins there or later.
-__device__ __forceinline__ int first_of(const ScanArgs& a, int64_t row)
+__device__ __forceinline__ int first_of(const ScanArgs& a, int row)
 {
     int lo = 0, hi = a.seqs;
     while (lo < hi) {
@@ -271,8 +332,7 @@ __device__ __forceinline__ int first_of(const ScanArgs& a, int64_t row)
 // A workgroup's share of the rows: one sequence, or a piece of all rows with
 // the sequences [first, last) that have rows in it (empty ones count where they lie).
 struct Share {
-    int64_t begin, end;
-    int first, last;
+    int begin, end, first, last;
     bool pieces, end_of_all;
 
     __device__ Share(const ScanArgs& a, int item) : pieces(a.pieces > 0)
@@ -286,8 +346,9 @@ struct Share {
             end_of_all = item + 1 == a.seqs;
             return;
         }
-        begin = static_cast<int64_t>(item) * a.piece_rows;
-        end = begin + a.piece_rows < a.rows ? begin + a.piece_rows : a.rows;
+        const int64_t from = static_cast<int64_t>(item) * a.piece_rows, to = from + a.piece_rows;
+        begin = static_cast<int>(from);
+        end = static_cast<int>(to < a.rows ? to : a.rows);
         end_of_all = item + 1 == a.pieces;
         first = first_of(a, begin);
         last = end_of_all ? a.seqs : first_of(a, end);

@@ -31,7 +31,7 @@ constexpr float kLn2 = 0.69314718055994531f;
 
 // What the pieces behind a share give to the gradient of its last state.
 template <int GR, int NS>
-__device__ __forceinline__ void inherit_back(const ScanArgs& a, const Lanes<GR, NS>& l, const float* A, int item, int64_t end, float* g)
+__device__ __forceinline__ void inherit_back(const ScanArgs& a, const Lanes<GR, NS>& l, const float* A, int item, int end, float* g)
 {
     const int64_t states = static_cast<int64_t>(a.channels) * a.n;
     float passed = 0.f;
@@ -75,25 +75,25 @@ __global__ __launch_bounds__(kThreads) void back_kernel(ScanArgs a)
     const float bias = a.bias ? a.bias[l.c] : 0.f;
     const int64_t states = static_cast<int64_t>(a.channels) * a.n;
     if (span.end <= share.end && a.dlast) l.read(a, a.dlast + s * states, g);
-    int64_t at = span.end < share.end ? span.end : share.end;
+    const int end = span.end < share.end ? span.end : share.end;
     float total = 0.f;
-    T dl[R], z[R], dy[R];
-    Shared<T, GR, NS> bc;
-    while (at > share.begin) {
-        int64_t row0 = (at - 1) & ~static_cast<int64_t>(kTile - 1);
-        const int rows = static_cast<int>(at - row0);
-        at = row0;
-        load_rows(l, a.delta, a.ds, row0, rows, dl);
-        load_rows(l, a.dy, a.channels, row0, rows, dy);
-        if (a.z) load_rows(l, a.z, a.zs, row0, rows, z);
-        bc.load(a, l, row0, rows);
+    T dl[R], z[R], dy[R], rb[L::LOADS], rc[L::LOADS];
+    Rows<T, GR, NS> rd(l, a.delta, a.ds, end), rz(l, a.z, a.zs, end), rg(l, a.dy, a.channels, end);
+    Shared<T, GR, NS> bc(a, l, end);
+    auto load = [&](int rows) __attribute__((always_inline)) {
+        rd.template load<false>(rows, dl);
+        rg.template load<false>(rows, dy);
+        rz.template load<false>(a.z ? rows : 0, z);
+        bc.template load<false>(rows, rb, rc);
+    };
+    load(rows_to(share.begin, end));
+    for (int to = end; to > share.begin;) {
+        const int rows = rows_to(share.begin, to);
         float d[R], dv[R];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const int r = i * GR + l.row;
             d[i] = load_f(&dl[i]) + bias;
             if (a.softplus) d[i] = softplus<false>(d[i]).v;
-            if (r >= rows) d[i] = 0.f;
             dv[i] = load_f(&dy[i]);
         }
         if (a.z)
@@ -103,9 +103,14 @@ __global__ __launch_bounds__(kThreads) void back_kernel(ScanArgs a)
             });
         wave_fence();
 #pragma unroll
-        for (int i = 0; i < R; ++i) dd[i * GR + l.row][l.ch] = make_float2(d[i], i * GR + l.row < rows ? dv[i] : 0.f);
-        bc.put(l, sb, sc);
+        for (int i = 0; i < R; ++i) {
+            const int r = i * GR + l.row;
+            dd[r][l.ch] = make_float2(r < rows ? d[i] : 0.f, r < rows ? dv[i] : 0.f);
+        }
+        bc.put(rb, rc, sb, sc);
         wave_fence();
+        to -= rows;
+        load(rows_to(share.begin, to));
 #pragma unroll
         for (int r = kTile - 1; r >= 0; --r) {
             const float2 v = dd[r][l.ch];
@@ -162,45 +167,39 @@ __global__ __launch_bounds__(kThreads) void bwd_kernel(ScanArgs a)
         } else {
             inherit_back(a, l, A, item, span.end, g);
         }
-        const int64_t begin = span.begin > share.begin ? span.begin : share.begin;
-        int64_t at = span.end < share.end ? span.end : share.end;
-        T x[R], dl[R], z[R], dy[R];
+        const int begin = span.begin > share.begin ? span.begin : share.begin;
+        const int end = span.end < share.end ? span.end : share.end;
+        T x[R], dl[R], z[R], dy[R], rb[L::LOADS], rc[L::LOADS];
         float entry[NS];
-        Shared<T, GR, NS> bc;
-        auto begin_of = [&](int64_t to) {
-            const int64_t v = (to - 1) & ~static_cast<int64_t>(kTile - 1);
-            return v > begin ? v : begin;
-        };
-        auto fetch = [&](int64_t to) __attribute__((always_inline)) {
-            const int64_t row0 = begin_of(to);
-            const int rows = static_cast<int>(to - row0);
-            load_rows(l, a.x, a.xs, row0, rows, x);
-            load_rows(l, a.delta, a.ds, row0, rows, dl);
-            load_rows(l, a.dy, a.channels, row0, rows, dy);
-            if (a.z) load_rows(l, a.z, a.zs, row0, rows, z);
-            bc.load(a, l, row0, rows);
-            if (row0 > span.begin) l.read(a, a.saved + row0 / kTile * states, entry);
-            else if (a.initial) l.read(a, a.initial + s * states, entry);
-            else
+        Rows<T, GR, NS> rx(l, a.x, a.xs, end), rd(l, a.delta, a.ds, end), rz(l, a.z, a.zs, end), rg(l, a.dy, a.channels, end);
+        Rows<T, GR, NS> wx(l, a.dx, a.channels, end), wd(l, a.ddelta, a.channels, end), wz(l, a.dz, a.channels, end);
+        Shared<T, GR, NS> bc(a, l, end);
+        auto load = [&](int to) __attribute__((always_inline)) {
+            const int n = rows_to(begin, to);
+            rx.template load<false>(n, x);
+            rd.template load<false>(n, dl);
+            rg.template load<false>(n, dy);
+            rz.template load<false>(a.z ? n : 0, z);
+            bc.template load<false>(n, rb, rc);
+            // the state in front of the tile; zeros where there is none
+            const float* from = to - n > span.begin ? a.saved + static_cast<int64_t>((to - n) / kTile) * states : a.initial ? a.initial + s * states : nullptr;
+            const rsrc_t r = make_rsrc(from, from && n > 0 ? static_cast<uint32_t>(states) * 4 : 0);
 #pragma unroll
-                for (int j = 0; j < NS; ++j) entry[j] = 0.f;
+            for (int j = 0; j < NS; ++j) entry[j] = scan::fetch(r, l.on && l.n0 + j < a.n ? (static_cast<uint32_t>(l.c) * a.n + l.n0 + j) * 4 : kOutside, 0.f);
         };
-        if (at > begin) fetch(at);
-        while (at > begin) {
-            const int64_t row0 = begin_of(at);
-            const int rows = static_cast<int>(at - row0);
-            at = row0;
+        if (begin < end) load(end);
+        for (int to = end; to > begin;) {
+            const int rows = rows_to(begin, to);
             // ------------------------------------------ the tile's rows --
             float xf[R], d[R], sig[R], dv[R], dz[R];
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                const int r = i * GR + l.row;
                 xf[i] = load_f(&x[i]);
                 dz[i] = dv[i] = load_f(&dy[i]);
                 const float raw = load_f(&dl[i]) + bias;
-                const Step p = a.softplus ? softplus<true>(raw) : Step{raw, 1.0f};
-                d[i] = r < rows ? p.v : 0.f;  // a row that is not there changes nothing
-                sig[i] = p.d;
+                const Step p = softplus<true>(raw);
+                d[i] = a.softplus ? p.v : raw;
+                sig[i] = a.softplus ? p.d : 1.0f;
             }
             if (a.z)
                 with_act(a.act, [&](auto kind) __attribute__((always_inline)) {
@@ -214,77 +213,102 @@ __global__ __launch_bounds__(kThreads) void bwd_kernel(ScanArgs a)
             wave_fence();
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                const bool there = i * GR + l.row < rows;
-                dd[i * GR + l.row][l.ch] = make_float4(d[i], d[i] * xf[i], there ? dv[i] : 0.f, 0.f);
+                // a row that is not there changes nothing, nor does a channel
+                const int r = i * GR + l.row;
+                const bool there = r < rows && l.on;
+                dd[r][l.ch] = make_float4(there ? d[i] : 0.f, there ? d[i] * xf[i] : 0.f, there ? dv[i] : 0.f, 0.f);
             }
-            bc.put(l, sb, sc);
+            bc.put(rb, rc, sb, sc);
             wave_fence();
             float first[NS];
 #pragma unroll
             for (int j = 0; j < NS; ++j) first[j] = entry[j];
-            if (at > begin) fetch(at);
+            to -= rows;
+            load(to);
             // ------------------------------------------- states again --
-            float hs[kTile][NS], as[kTile][NS];
+            constexpr int G = NS <= 2 ? kGroup : kGroup / 2, NG = kTile / G;  // rows whose operands are read at once
+            static_assert(NG % 2 == 0, "operands alternate");
+            typedef Operands<NS, G, float4> Ops;
+            Ops ops[2];
+            auto fetch = [&](Ops& o, int group) __attribute__((always_inline)) {
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-                float v[GR];
-#pragma unroll
-                for (int r = 0; r < GR; ++r) {
-                    const int t = i * GR + r;
-                    const float2 w = *reinterpret_cast<const float2*>(&dd[t][l.ch]);
-                    const float *b = sb + t * NP + l.n0, *c = sc + t * NP + l.n0;
-                    v[r] = 0.f;
+                for (int r = 0; r < G; ++r) {
+                    o.d[r] = dd[group * G + r][l.ch];
 #pragma unroll
                     for (int j = 0; j < NS; ++j) {
-                        as[t][j] = exp2_hw(w.x * A[j]);
-                        hs[t][j] = __builtin_fmaf(as[t][j], t ? hs[t ? t - 1 : 0][j] : first[j], w.y * b[j]);
-                        v[r] = __builtin_fmaf(hs[t][j], c[j], v[r]);
+                        o.b[r][j] = sb[(group * G + r) * NP + l.n0 + j];
+                        o.c[r][j] = sc[(group * G + r) * NP + l.n0 + j];
                     }
                 }
-                merge_all<32, CH, GR>(v);
-                dz[i] *= __builtin_fmaf(skip, xf[i], v[0]);
+            };
+            float hs[kTile][NS], as[kTile][NS], v[kTile];
+            fetch(ops[0], 0);
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+                fetch(ops[(i + 1) & 1], i + 1 < NG ? i + 1 : NG - 1);  // the last group is also the first one back
+                lds_stays();
+                const Ops& o = ops[i & 1];
+#pragma unroll
+                for (int r = 0; r < G; ++r) {
+                    const int k = i * G + r;
+                    v[k] = 0.f;
+#pragma unroll
+                    for (int j = 0; j < NS; ++j) {
+                        as[k][j] = exp2_hw(o.d[r].x * A[j]);
+                        hs[k][j] = __builtin_fmaf(as[k][j], k ? hs[k ? k - 1 : 0][j] : first[j], o.d[r].y * o.b[r][j]);
+                        v[k] = __builtin_fmaf(hs[k][j], o.c[r][j], v[k]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                merge_all<32, CH, GR>(v + i * GR);
+                dz[i] *= __builtin_fmaf(skip, xf[i], v[i * GR]);
             }
             // ------------------------------------------------- and back --
             float* part = lds_part[turn][l.wave];
-            float da[NS], ddelta[R], dx[R];
+            float da[NS], ddelta[R], dx[R], w[kTile], u[kTile], m[K];
 #pragma unroll
             for (int j = 0; j < NS; ++j) da[j] = 0.f;
 #pragma unroll
-            for (int i = R - 1; i >= 0; --i) {
-                float w[GR], u[GR], m[K];
+            for (int i = 0; i < NG; ++i) {
+                if (i + 1 < NG) fetch(ops[(i + 1) & 1], NG - 2 - i);
+                lds_stays();
+                const Ops& o = ops[i & 1];
 #pragma unroll
-                for (int r = GR - 1; r >= 0; --r) {
-                    const int t = i * GR + r, in = r % RB;
-                    const float4 v = dd[t][l.ch];
-                    const float *b = sb + t * NP + l.n0, *c = sc + t * NP + l.n0;
-                    w[r] = u[r] = 0.f;
+                for (int r = G - 1; r >= 0; --r) {
+                    const int k = (NG - 1 - i) * G + r, in = k % RB;
+                    w[k] = u[k] = 0.f;
 #pragma unroll
                     for (int j = 0; j < NS; ++j) {
-                        const float e = __builtin_fmaf(c[j], v.z, g[j]);
-                        m[in * V + j] = e * v.y;
-                        m[in * V + NS + j] = v.z * hs[t][j];
-                        w[r] = __builtin_fmaf(e, b[j], w[r]);
-                        g[j] = e * as[t][j];
-                        const float q = g[j] * (t ? hs[t ? t - 1 : 0][j] : first[j]);
-                        u[r] = __builtin_fmaf(A[j], q, u[r]);
-                        da[j] = __builtin_fmaf(v.x, q, da[j]);
+                        const float e = __builtin_fmaf(o.c[r][j], o.d[r].z, g[j]);
+                        m[in * V + j] = e * o.d[r].y;
+                        m[in * V + NS + j] = o.d[r].z * hs[k][j];
+                        w[k] = __builtin_fmaf(e, o.b[r][j], w[k]);
+                        g[j] = e * as[k][j];
+                        const float q = g[j] * (k ? hs[k ? k - 1 : 0][j] : first[j]);
+                        u[k] = __builtin_fmaf(A[j], q, u[k]);
+                        da[j] = __builtin_fmaf(o.d[r].x, q, da[j]);
                     }
 #pragma unroll
                     for (int j = 2 * NS; j < V; ++j) m[in * V + j] = 0.f;
                     if (in == 0) {
                         merge_all<CH / 2, 1, K>(m);
 #pragma unroll
-                        for (int k = 0; k < KEPT; ++k) {
-                            const int at_v = mine + k * CH, row = t + at_v / V, val = at_v % V;
+                        for (int q = 0; q < KEPT; ++q) {
+                            const int at_v = mine + q * CH, row = k + at_v / V, val = at_v % V;
                             if (at_v < K && val < 2 * NS)
-                                part[row * 2 * NP + (val < NS ? l.n0 + val : NP + l.n0 + val - NS)] = m[k];
+                                part[row * 2 * NP + (val < NS ? l.n0 + val : NP + l.n0 + val - NS)] = m[q];
                         }
                     }
                 }
-                merge_all<32, CH, GR>(w);
-                merge_all<32, CH, GR>(u);
-                ddelta[i] = (u[0] * kLn2 + w[0] * xf[i]) * sig[i];
-                dx[i] = __builtin_fmaf(w[0], d[i], skip * dv[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                merge_all<32, CH, GR>(w + i * GR);
+                merge_all<32, CH, GR>(u + i * GR);
+                ddelta[i] = (u[i * GR] * kLn2 + w[i * GR] * xf[i]) * sig[i];
+                dx[i] = __builtin_fmaf(w[i * GR], d[i], skip * dv[i]);
                 if (i * GR + l.row < rows) {
                     dskip = __builtin_fmaf(dv[i], xf[i], dskip);
                     dbias += ddelta[i];
@@ -292,16 +316,17 @@ __global__ __launch_bounds__(kThreads) void bwd_kernel(ScanArgs a)
             }
 #pragma unroll
             for (int j = 0; j < NS; ++j) dA[j] += da[j];
-            if (a.dx) store_rows<T>(l, a.dx, a.channels, row0, rows, dx);
-            if (a.ddelta) store_rows<T>(l, a.ddelta, a.channels, row0, rows, ddelta);
-            if (a.dz) store_rows<T>(l, a.dz, a.channels, row0, rows, dz);
+            wx.template store<false>(a.dx ? rows : 0, dx);
+            wd.template store<false>(a.ddelta ? rows : 0, ddelta);
+            wz.template store<false>(a.dz ? rows : 0, dz);
             // The workgroup's sum of dB and dC; the other half of the buffer
             // is the next tile's, so one barrier a tile is enough.
-            __syncthreads();
-            float* out = a.part_bc + (static_cast<int64_t>(block) * a.rows + row0) * 2 * a.n;
-            for (int e = threadIdx.x; e < rows * 2 * NP; e += kThreads) {
-                const int row = e / (2 * NP), in = e % (2 * NP), n = in % NP;
-                if (n < a.n) {
+            lds_barrier();
+            float* out = a.part_bc + (static_cast<int64_t>(block) * a.rows + to) * 2 * a.n;
+#pragma unroll
+            for (int q = 0; q < (kTile * 2 * NP + kThreads - 1) / kThreads; ++q) {
+                const int e = threadIdx.x + q * kThreads, row = e / (2 * NP), in = e % (2 * NP), n = in % NP;
+                if (row < rows && n < a.n) {
                     const float* p = &lds_part[turn][0][e];
                     out[(row * 2 + in / NP) * a.n + n] = (p[0] + p[kTile * 2 * NP]) + (p[2 * kTile * 2 * NP] + p[3 * kTile * 2 * NP]);
                 }

@@ -15,7 +15,7 @@ namespace scan {
 // The state that the pieces before a share leave to its first sequence: what
 // each of them ends with, faded by the pieces between.
 template <int GR, int NS>
-__device__ __forceinline__ void inherit(const ScanArgs& a, const Lanes<GR, NS>& l, const float* A, int item, int64_t begin, float* h)
+__device__ __forceinline__ void inherit(const ScanArgs& a, const Lanes<GR, NS>& l, const float* A, int item, int begin, float* h)
 {
     const int64_t states = static_cast<int64_t>(a.channels) * a.n;
     float passed = 0.f;
@@ -26,28 +26,28 @@ __device__ __forceinline__ void inherit(const ScanArgs& a, const Lanes<GR, NS>& 
 #pragma unroll
         for (int j = 0; j < NS; ++j) h[j] = __builtin_fmaf(exp2_hw(A[j] * passed), e[j], h[j]);
         passed += sum;
-        if (begin >= q * a.piece_rows) break;  // the sequence begins in that piece
+        if (begin >= static_cast<int64_t>(q) * a.piece_rows) break;  // the sequence begins in that piece
     }
 }
 
 // kStates: states for the gradient's tiles alone; kEnds: the state at the end of
 // a piece from nothing before it, for the pieces behind it.
 enum Want { kOutputs, kStates, kEnds };
+constexpr int kAhead = 2;
 
 template <typename T, int GR, int NS, int WANT>
 __global__ __launch_bounds__(kThreads) void fwd_kernel(ScanArgs a)
 {
     typedef Lanes<GR, NS> L;
     constexpr int CH = L::CH, R = L::R, NP = L::NP;
-    __shared__ float2 lds_d[kWaves][kTile][CH];
-    __shared__ float lds_b[kWaves][kTile * NP], lds_c[kWaves][kTile * NP];
+    // two tiles: while one is worked on, the next one is prepared
+    __shared__ float2 lds_d[kWaves][2][kTile][CH];
+    __shared__ float lds_b[kWaves][2][kTile * NP], lds_c[kWaves][2][kTile * NP];
 
     const uint32_t cb = static_cast<uint32_t>(a.groups) * a.blocks;
     const int item = static_cast<int>(blockIdx.x / cb);
     const L l(a, blockIdx.x % cb);
     const Share share(a, item);
-    float2(*dd)[CH] = lds_d[l.wave];
-    float *sb = lds_b[l.wave], *sc = lds_c[l.wave];
 
     float A[NS], h[NS];
     l.read(a, a.A, A);
@@ -67,70 +67,125 @@ __global__ __launch_bounds__(kThreads) void fwd_kernel(ScanArgs a)
         } else if (WANT != kEnds) {
             inherit(a, l, A, item, span.begin, h);
         }
-        int64_t at = span.begin > share.begin ? span.begin : share.begin;
-        const int64_t end = span.end < share.end ? span.end : share.end;
+        const int begin = span.begin > share.begin ? span.begin : share.begin, end = span.end < share.end ? span.end : share.end;
         float total = 0.f;  // sum of d
-        T x[R], dl[R], z[R];
-        Shared<T, GR, NS> bc;
-        auto fetch = [&](int64_t row0) __attribute__((always_inline)) {
-            const int rows = static_cast<int>(tile_end(row0, end) - row0);
-            load_rows(l, a.x, a.xs, row0, rows, x);
-            load_rows(l, a.delta, a.ds, row0, rows, dl);
-            if (gate) load_rows(l, a.z, a.zs, row0, rows, z);
-            bc.load(a, l, row0, rows);
+        Rows<T, GR, NS> rx(l, a.x, a.xs, begin), rd(l, a.delta, a.ds, begin), rz(l, a.z, a.zs, begin), ry(l, a.y, a.channels, begin);
+        // Loads run kAhead tiles ahead of the work, each tile's in registers of
+        // its own.
+        struct Raw {
+            T x[R], dl[R], z[R], b[L::LOADS], c[L::LOADS];
         };
-        if (at < end) fetch(at);
-        while (at < end) {
-            const int64_t row0 = at;
-            at = tile_end(at, end);
-            const int rows = static_cast<int>(at - row0);
-            float xf[R], zf[R], y[R];
+        Shared<T, GR, NS> bc(a, l, begin);
+        Raw raw[kAhead];
+        // Without a condition: a wait for one tile's loads can then leave the
+        // later ones in flight (past the end they are of no rows).
+        int ahead = begin;
+        auto load_next = [&](Raw& w) __attribute__((always_inline)) {
+            const int n = rows_from(ahead, end);
+            rx.template load<true>(n, w.x);
+            rd.template load<true>(n, w.dl);
+            rz.template load<true>(gate ? n : 0, w.z);
+            bc.template load<true>(n, w.b, w.c);
+            ahead += n;
+        };
+        // A tile's steps and inputs, from registers to LDS.
+        struct Ready {
+            float x[R], z[R], d[R];
+        };
+        auto prepare = [&](const Raw& w, int rows, Ready& v) __attribute__((always_inline)) {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                const int r = i * GR + l.row;
-                xf[i] = load_f(&x[i]);
-                zf[i] = gate ? load_f(&z[i]) : 0.f;
-                float d = load_f(&dl[i]) + bias;
-                if (a.softplus) d = softplus<false>(d).v;
-                if (r >= rows) d = 0.f;  // a row that is not there changes nothing
-                dd[r][l.ch] = make_float2(d, d * xf[i]);
+                v.x[i] = load_f(&w.x[i]);
+                v.z[i] = load_f(&w.z[i]);
+                const float t = load_f(&w.dl[i]) + bias, p = softplus<false>(t).v;
+                v.d[i] = a.softplus ? p : t;
+                if (i * GR + l.row >= rows) v.d[i] = 0.f;  // a row that is not there changes nothing
             }
-            bc.put(l, sb, sc);
-            wave_fence();
-            if (WANT != kEnds && a.saved && row0 > span.begin && (row0 & (kTile - 1)) == 0) l.write(a, a.saved + row0 / kTile * states, h);
-            if (at < end) fetch(at);  // the next tile's loads run beside this tile's work
+        };
+        auto put_tile = [&](const Raw& w, const Ready& v, int turn) __attribute__((always_inline)) {
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-                y[i] = 0.f;
-                if (i * GR < rows) {
-                    float v[GR];
+            for (int i = 0; i < R; ++i) lds_d[l.wave][turn][i * GR + l.row][l.ch] = make_float2(v.d[i], v.d[i] * v.x[i]);
+            bc.put(w.b, w.c, lds_b[l.wave][turn], lds_c[l.wave][turn]);
+        };
+        typedef Operands<NS, kGroup, float2> Ops;
+        Ops ops[2];
+        auto fetch = [&](Ops& o, int turn, int row) __attribute__((always_inline)) {
 #pragma unroll
-                    for (int r = 0; r < GR; ++r) {
-                        const float2 d = dd[i * GR + r][l.ch];
-                        const float *b = sb + (i * GR + r) * NP + l.n0, *c = sc + (i * GR + r) * NP + l.n0;
-                        if (WANT == kEnds) total += d.x;
-                        v[r] = 0.f;
+            for (int r = 0; r < kGroup; ++r) {
+                o.d[r] = lds_d[l.wave][turn][row + r][l.ch];
 #pragma unroll
-                        for (int j = 0; j < NS; ++j) {
-                            h[j] = __builtin_fmaf(exp2_hw(d.x * A[j]), h[j], d.y * b[j]);
-                            if (WANT == kOutputs) v[r] = __builtin_fmaf(h[j], c[j], v[r]);
-                        }
-                    }
-                    if constexpr (WANT == kOutputs) {
-                        merge_all<32, CH, GR>(v);
-                        y[i] = __builtin_fmaf(skip, xf[i], v[0]);
-                    }
+                for (int j = 0; j < NS; ++j) {
+                    o.b[r][j] = lds_b[l.wave][turn][(row + r) * NP + l.n0 + j];
+                    if (WANT == kOutputs) o.c[r][j] = lds_c[l.wave][turn][(row + r) * NP + l.n0 + j];
                 }
             }
+        };
+        Ready now, next;
+        int at = begin, rows = 0;
+        if (begin < end) {
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) load_next(raw[k]);
+            rows = rows_from(at, end);
+            prepare(raw[0], rows, now);
             wave_fence();
+            put_tile(raw[0], now, 0);
+            load_next(raw[0]);
+            wave_fence();
+            fetch(ops[0], 0, 0);
+        }
+        // One tile, which is in LDS, and beside it the next one's preparation:
+        // dependent chains that cost little time of their own there.
+        auto work = [&](Raw& w, int turn) __attribute__((always_inline)) {
+            const int here = rows;
+            if (WANT != kEnds && a.saved && at > span.begin) l.write(a, a.saved + static_cast<int64_t>(at / kTile) * states, h);
+            at += rows;
+            rows = rows_from(at, end);
+            prepare(w, rows, next);
+            float v[kTile], y[R];
+#pragma unroll
+            for (int g = 0; g < kTile / kGroup; ++g) {
+                if (g + 1 < kTile / kGroup) {
+                    fetch(ops[(g + 1) & 1], turn, (g + 1) * kGroup);
+                } else {
+                    wave_fence();
+                    put_tile(w, next, turn ^ 1);
+                    load_next(w);
+                    wave_fence();
+                    fetch(ops[0], turn ^ 1, 0);
+                }
+                lds_stays();
+                const Ops& o = ops[g & 1];
+#pragma unroll
+                for (int r = 0; r < kGroup; ++r) {
+                    if (WANT == kEnds) total += o.d[r].x;
+                    float acc = 0.f;
+#pragma unroll
+                    for (int j = 0; j < NS; ++j) {
+                        h[j] = __builtin_fmaf(exp2_hw(o.d[r].x * A[j]), h[j], o.d[r].y * o.b[r][j]);
+                        if (WANT == kOutputs) acc = __builtin_fmaf(h[j], o.c[r][j], acc);
+                    }
+                    v[g * kGroup + r] = acc;
+                }
+            }
             if constexpr (WANT == kOutputs) {
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    merge_all<32, CH, GR>(v + i * GR);
+                    y[i] = __builtin_fmaf(skip, now.x[i], v[i * GR]);
+                }
                 if (gate)
                     with_act(a.act, [&](auto kind) __attribute__((always_inline)) {
 #pragma unroll
-                        for (int i = 0; i < R; ++i) y[i] *= act_value<kind()>(zf[i]);
+                        for (int i = 0; i < R; ++i) y[i] *= act_value<kind()>(now.z[i]);
                     });
-                store_rows<T>(l, a.y, a.channels, row0, rows, y);
+                ry.template store<true>(here, y);
             }
+            now = next;
+        };
+        static_assert(kAhead == 2 && kTile / kGroup % 2 == 0, "registers and LDS alternate");
+        while (at < end) {
+            work(raw[1], 0);
+            if (at < end) work(raw[0], 1);
         }
         if (WANT == kOutputs && a.last && span.end <= share.end) l.write(a, a.last + s * states, h);
         if (WANT == kEnds) {

@@ -23,8 +23,12 @@ hipError_t run_one(int run, const ScanArgs& a, int items, hipStream_t s)
     case kRunOutputs: return launch(fwd_kernel<T, GR, NS, kOutputs>, grid, threads, 0, s, a);
     case kRunStates: return launch(fwd_kernel<T, GR, NS, kStates>, grid, threads, 0, s, a);
     case kRunEnds: return launch(fwd_kernel<T, GR, NS, kEnds>, grid, threads, 0, s, a);
-    case kRunBack: return launch(back_kernel<T, GR, NS>, grid, threads, 0, s, a);
-    default: return launch(bwd_kernel<T, GR, NS>, grid, threads, 0, s, a);
+    case kRunBack:
+        if constexpr (GR > 4) return launch(back_kernel<T, GR, NS>, grid, threads, 0, s, a);
+        else return hipErrorInvalidConfiguration;  // the gradient has eight groups at least
+    default:
+        if constexpr (GR > 4) return launch(bwd_kernel<T, GR, NS>, grid, threads, 0, s, a);
+        else return hipErrorInvalidConfiguration;
     }
 }
 
@@ -34,7 +38,7 @@ hipError_t run_of(int run, int gr, int ns, const ScanArgs& a, int items, hipStre
 #define CONVMI_SCAN(GR, NS) \
     if (gr == GR && ns == NS) return run_one<T, GR, NS>(run, a, items, s);
     CONVMI_SCAN(4, 1) CONVMI_SCAN(4, 2) CONVMI_SCAN(4, 3) CONVMI_SCAN(4, 4)
-    CONVMI_SCAN(8, 3) CONVMI_SCAN(8, 4) CONVMI_SCAN(16, 3) CONVMI_SCAN(16, 4)
+    CONVMI_SCAN(8, 1) CONVMI_SCAN(8, 2) CONVMI_SCAN(8, 3) CONVMI_SCAN(8, 4) CONVMI_SCAN(16, 3) CONVMI_SCAN(16, 4)
 #undef CONVMI_SCAN
     return hipErrorInvalidConfiguration;
 }
