@@ -6,10 +6,11 @@
 // Gradient: dp = dy act'(p) (p again from x), dx[t] = sum_k w[k] dp[t + K - 1 - k]
 // over the rows of the sequence, dw[k] = sum_t dp[t] x[t - K + 1 + k], db = sum_t dp[t].
 //
-// A stream over memory: a lane takes kV neighbouring channels and walks down a
+// A stream over memory: a lane takes four neighbouring channels and walks down a
 // range of rows with the last K - 1 rows (in the gradient also the last K - 1
 // dp) in registers, so every value is loaded once but for the K - 1 rows around
-// a range.  Sequences may begin anywhere in a range.  The rows' ragged end
+// a range.  The next four rows' loads are out while four are worked on (72 -> 58
+// us for 4 x 4096 rows of 4096 channels, bf16: 4.7 TB/s).  Sequences may begin anywhere in a range.  The rows' ragged end
 // repeats channels of the lane before it.
 #include "act.hpp"
 #include "kernels.hpp"
@@ -23,36 +24,71 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kU = 4;  // rows loaded at once
 
+// V neighbouring values: as loaded, and in fp32.
+template <int N>
+struct Words {
+    typedef uint32_t any __attribute__((ext_vector_type(N), aligned(2)));
+};
+template <>
+struct Words<1> {
+    typedef uint32_t any __attribute__((aligned(2)));
+};
 template <typename T, int V>
 struct Vec {
+    static constexpr int N = V * static_cast<int>(sizeof(T)) / 4;  // dwords
+    uint32_t w[N];
+    __device__ __forceinline__ void load(const T* p)
+    {
+        const typename Words<N>::any t = *reinterpret_cast<const typename Words<N>::any*>(p);
+        if constexpr (N == 1) w[0] = t;
+        else
+#pragma unroll
+            for (int i = 0; i < N; ++i) w[i] = t[i];
+    }
+    __device__ __forceinline__ void open(float* v) const
+    {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = __uint_as_float(w[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                v[2 * i] = __uint_as_float(w[i] << 16);
+                v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        }
+    }
     static __device__ __forceinline__ void load(const T* p, float* v)
     {
-        if constexpr (V == 1) {
-            v[0] = load_f(p);
-        } else if constexpr (sizeof(T) == 4) {
-            const uint4 t = load16_any(p);
-            v[0] = __uint_as_float(t.x); v[1] = __uint_as_float(t.y); v[2] = __uint_as_float(t.z); v[3] = __uint_as_float(t.w);
-        } else {
-            typedef uint32_t u2 __attribute__((ext_vector_type(2), aligned(2)));
-            const u2 t = *reinterpret_cast<const u2*>(p);
-            v[0] = __uint_as_float(t.x << 16); v[1] = __uint_as_float(t.x & 0xffff0000u);
-            v[2] = __uint_as_float(t.y << 16); v[3] = __uint_as_float(t.y & 0xffff0000u);
-        }
+        Vec t;
+        t.load(p);
+        t.open(v);
     }
     static __device__ __forceinline__ void store(T* p, const float* v)
     {
-        if constexpr (V == 1) {
-            store_f(p, v[0]);
-        } else if constexpr (sizeof(T) == 4) {
-            store16_any(p, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
+        typename Words<N>::any t;
+        if constexpr (sizeof(T) == 4) {
+            if constexpr (N == 1) t = __float_as_uint(v[0]);
+            else
+#pragma unroll
+                for (int i = 0; i < N; ++i) t[i] = __float_as_uint(v[i]);
+        } else if constexpr (N == 1) {
+            t = pack_bf16x2(v[0], v[1]);
         } else {
-            typedef uint32_t u2 __attribute__((ext_vector_type(2), aligned(2)));
-            u2 t;
-            t.x = pack_bf16x2(v[0], v[1]);
-            t.y = pack_bf16x2(v[2], v[3]);
-            *reinterpret_cast<u2*>(p) = t;
+#pragma unroll
+            for (int i = 0; i < N; ++i) t[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
         }
+        *reinterpret_cast<typename Words<N>::any*>(p) = t;
     }
+};
+// A single value of bf16.
+template <>
+struct Vec<bf16_t, 1> {
+    bf16_t w;
+    __device__ __forceinline__ void load(const bf16_t* p) { w = *p; }
+    __device__ __forceinline__ void open(float* v) const { v[0] = bf16_to_f(w); }
+    static __device__ __forceinline__ void load(const bf16_t* p, float* v) { v[0] = load_f(p); }
+    static __device__ __forceinline__ void store(bf16_t* p, const float* v) { store_f(p, v[0]); }
 };
 
 struct Span {
@@ -148,11 +184,19 @@ __global__ __launch_bounds__(kThreads) void causal_fwd_kernel(CausalArgs a, int6
         float win[K - 1 + kU][V];
 #pragma unroll
         for (int k = 0; k < K - 1; ++k) t.before(a, s, span, row - span.begin - (K - 1) + k, win[k]);
+        // The next rows' loads run beside these rows' work; rows past the end
+        // are the last one again.
+        Vec<T, V> next[kU];
+        auto load = [&](int64_t from) __attribute__((always_inline)) {
+#pragma unroll
+            for (int u = 0; u < kU; ++u) next[u].load(t.x(a, from + u < end ? from + u : end - 1));
+        };
+        load(row);
         for (; row < end; row += kU) {
             const int n = static_cast<int>(end - row < kU ? end - row : kU);
 #pragma unroll
-            for (int u = 0; u < kU; ++u)
-                if (u < n) Vec<T, V>::load(t.x(a, row + u), win[K - 1 + u]);
+            for (int u = 0; u < kU; ++u) next[u].open(win[K - 1 + u]);
+            load(row + kU);
             float p[kU][V];
 #pragma unroll
             for (int u = 0; u < kU; ++u)
@@ -191,18 +235,26 @@ __global__ __launch_bounds__(kThreads) void causal_bwd_kernel(CausalArgs a, int6
     const T* dy = static_cast<const T*>(a.dy);
     const int before = K - 1;
 
-    // dp of `n` rows from `row` on: p again from the window, times dy.
-    auto slopes = [&](float (*win)[V], int64_t row, int n, float (*dp)[V]) __attribute__((always_inline)) {
-        float g[kU][V];
+    // Rows of x and dy, on their way; rows from `stop` on are the one before it.
+    Vec<T, V> next_x[kU], next_g[kU];
+    auto load = [&](int64_t row, int64_t stop) __attribute__((always_inline)) {
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) win[before + u][v] = g[u][v] = 0.f;
-            if (u < n) {
-                Vec<T, V>::load(t.x(a, row + u), win[before + u]);
-                Vec<T, V>::load(dy + (row + u) * a.C + t.c, g[u]);
-            }
+            const int64_t r = row + u < stop ? row + u : stop - 1;
+            next_x[u].load(t.x(a, r));
+            next_g[u].load(dy + r * a.C + t.c);
         }
+    };
+    // dp of the loaded rows, `n` of which are there: p again from the window,
+    // times dy.
+    auto take = [&](float (*win)[V], float (*g)[V]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            next_x[u].open(win[before + u]);
+            next_g[u].open(g[u]);
+        }
+    };
+    auto slopes = [&](float (*win)[V], float (*g)[V], int n, float (*dp)[V]) __attribute__((always_inline)) {
 #pragma unroll
         for (int u = 0; u < kU; ++u)
 #pragma unroll
@@ -242,8 +294,11 @@ __global__ __launch_bounds__(kThreads) void causal_bwd_kernel(CausalArgs a, int6
 #pragma unroll
         for (int row = 0; row < K - 1; row += kU) {
             const int n = static_cast<int>(len - row < 0 ? 0 : len - row < kU ? len - row : kU);
-            float dp[kU][V];
-            slopes(win, span.begin + row, n, dp);
+            float dp[kU][V], g[kU][V];
+            if (n == 0) break;
+            load(span.begin + row, span.begin + row + n);
+            take(win, g);
+            slopes(win, g, n, dp);
 #pragma unroll
             for (int u = 0; u < kU; ++u)
 #pragma unroll
@@ -289,10 +344,14 @@ __global__ __launch_bounds__(kThreads) void causal_bwd_kernel(CausalArgs a, int6
 #pragma unroll
             for (int v = 0; v < V; ++v) back[k][v] = 0.f;
         }
+        load(row, far);
         for (; row < end + before; row += kU) {
             const int n = static_cast<int>(far - row < 0 ? 0 : far - row < kU ? far - row : kU);
             const int own = static_cast<int>(end - row < 0 ? 0 : end - row < kU ? end - row : kU);
-            slopes(win, row, n, back + before);
+            float g[kU][V];
+            take(win, g);
+            load(row + kU, far);
+            slopes(win, g, n, back + before);
 #pragma unroll
             for (int u = 0; u < kU; ++u) {
                 if (u < own)
@@ -370,15 +429,20 @@ __global__ __launch_bounds__(kThreads) void causal_step_kernel(CausalArgs a, int
     });
 }
 
+// Channels of a lane: four, or one where there are fewer.  Two would leave room
+// for more waves, but are slower both ways (65 us for 58, 118 for 113).
 int vector_of(const CausalArgs& a) { return a.C >= 4 ? 4 : 1; }
 
-// Rows of a range: the fewer, the more lanes; the more, the fewer rows read
-// twice (and partial sums).  From 16 up to 128 as long as the device stays full.
+// Rows of a range: the fewest that leave no more lanes than the device holds at
+// four waves a SIMD.  Fewer rows are read twice and have more partial sums, more
+// leave SIMDs empty (4 x 4096 rows of 4096 channels: 61, 58 and 62 us with 32, 64
+// and 128 rows; training step of 20011 rows of 1544 channels: 130, 113 and 129 us
+// with 16, 32 and 64).
 void plan(CausalArgs& a)
 {
     const int64_t vecs = (a.C + vector_of(a) - 1) / vector_of(a);
-    a.per = 16;
-    while (a.per < 128 && a.rows / (2 * a.per) * vecs >= 256 * 1024) a.per *= 2;
+    a.per = 8;
+    while (a.per < 128 && (a.rows + a.per - 1) / a.per * vecs > 262144) a.per *= 2;
 }
 
 size_t up(size_t n) { return (n + 15) & ~size_t(15); }
@@ -405,10 +469,10 @@ size_t causal_bwd_workspace(int64_t rows, int C, int K)
     case 7: e = GO((KERNEL<T, V, 7>)); break;         \
     default: e = GO((KERNEL<T, V, 8>)); break;        \
     }
-#define CONVMI_CAUSAL(KERNEL, GO)                                                                          \
-    if (dtype) {                                                                                           \
+#define CONVMI_CAUSAL(KERNEL, GO)                                                                                 \
+    if (dtype) {                                                                                                  \
         if (vector_of(a) == 4) { CONVMI_TAPS(bf16_t, 4, KERNEL, GO) } else { CONVMI_TAPS(bf16_t, 1, KERNEL, GO) } \
-    } else {                                                                                               \
+    } else {                                                                                                      \
         if (vector_of(a) == 4) { CONVMI_TAPS(float, 4, KERNEL, GO) } else { CONVMI_TAPS(float, 1, KERNEL, GO) }   \
     }
 
