@@ -8,7 +8,7 @@
 // what changes is written once (fp32 throughout: 28 bytes an element; bf16 with
 // 8-bit states: 10).  Clipping by a norm in hand costs a factor here, where
 // clip_gradients is a pass of its own.  One launch takes a table of up to 48
-// tensors as its argument and deals chunks of them out to its workgroups.
+// tensors as its argument and has a workgroup for each chunk of 4096 elements.
 //
 // 8 bits: 128 elements, on 16 lanes, share a scale.  m is the scale times q |q|
 // and the root of v the scale times q^2: steps next to the largest value are
@@ -19,7 +19,6 @@
 // multiply-add contracted.
 #include "kernels.hpp"
 
-#include <algorithm>
 #include <cmath>
 
 namespace convmi {
@@ -29,6 +28,11 @@ constexpr int kThreads = 256, kE = 8;  // elements of a lane at once
 constexpr float kTiny = 0x1p-100f;     // blocks below it hold zeros
 constexpr int kMostM = 127, kMostV = 255;
 
+// Elements in a chunk.  Every chunk has a workgroup of its own, which the
+// device gives out as others end: 2048 workgroups that walk over chunks of 32768 took
+// 1427 us where this takes 1129.
+constexpr uint32_t kChunk = 4096;
+
 template <int N>
 struct Table {
     void *p[N], *m[N], *v[N], *copy[N];
@@ -37,7 +41,6 @@ struct Table {
     uint64_t count[N];        // elements * 8 + (1: p bf16) + (2: g bf16) + (4: copy bf16)
     uint32_t begin[N + 1];    // first chunk of each tensor
     int n;
-    uint32_t chunk;           // elements in a chunk, a multiple of 2048
 };
 constexpr int kTensors = 48;
 static_assert(sizeof(Table<kTensors>) + 128 <= 4096, "the table is a kernel argument");
@@ -63,51 +66,69 @@ __device__ __forceinline__ int find(const Table<N>& t, uint32_t c)
     return lo;
 }
 
-// kE elements from the i-th on; past n zeros.
+template <int N>
+struct Words {
+    typedef uint32_t any __attribute__((ext_vector_type(N), aligned(2)));
+};
+
+// E elements from the i-th on; past the `have`-th zeros.
+template <int E, bool STREAM>
 __device__ __forceinline__ void load_e(const void* at, bool bf16, uint64_t i, int have, float* v)
 {
-    if (have >= kE) {
+    if (have >= E) {
         if (bf16) {
-            const uint4 w = load16_any(static_cast<const bf16_t*>(at) + i);
-            const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+            typedef typename Words<E / 2>::any W;
+            const W* p = reinterpret_cast<const W*>(static_cast<const bf16_t*>(at) + i);
+            const W w = STREAM ? __builtin_nontemporal_load(p) : *p;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                v[2 * k] = __uint_as_float(q[k] << 16);
-                v[2 * k + 1] = __uint_as_float(q[k] & 0xffff0000u);
+            for (int k = 0; k < E / 2; ++k) {
+                v[2 * k] = __uint_as_float(w[k] << 16);
+                v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
             }
         } else {
+            typedef Words<4>::any W;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint4 w = load16_any(static_cast<const float*>(at) + i + 4 * h);
-                v[4 * h] = __uint_as_float(w.x);
-                v[4 * h + 1] = __uint_as_float(w.y);
-                v[4 * h + 2] = __uint_as_float(w.z);
-                v[4 * h + 3] = __uint_as_float(w.w);
+            for (int h = 0; h < E / 4; ++h) {
+                const W* p = reinterpret_cast<const W*>(static_cast<const float*>(at) + i + 4 * h);
+                const W w = STREAM ? __builtin_nontemporal_load(p) : *p;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[4 * h + k] = __uint_as_float(w[k]);
             }
         }
         return;
     }
 #pragma unroll
-    for (int k = 0; k < kE; ++k) {
+    for (int k = 0; k < E; ++k) {
         v[k] = 0.f;
         if (k < have) v[k] = bf16 ? load_f(static_cast<const bf16_t*>(at) + i + k) : load_f(static_cast<const float*>(at) + i + k);
     }
 }
+template <int E, bool STREAM>
 __device__ __forceinline__ void store_e(void* at, bool bf16, uint64_t i, int have, const float* v)
 {
-    if (have >= kE) {
+    if (have >= E) {
         if (bf16) {
-            store16_any(static_cast<bf16_t*>(at) + i, make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
-        } else {
+            typedef typename Words<E / 2>::any W;
+            W w;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                store16_any(static_cast<float*>(at) + i + 4 * h, make_uint4(__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]),
-                                                                           __float_as_uint(v[4 * h + 2]), __float_as_uint(v[4 * h + 3])));
+            for (int k = 0; k < E / 2; ++k) w[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+            W* p = reinterpret_cast<W*>(static_cast<bf16_t*>(at) + i);
+            if (STREAM) __builtin_nontemporal_store(w, p); else *p = w;
+        } else {
+            typedef Words<4>::any W;
+#pragma unroll
+            for (int h = 0; h < E / 4; ++h) {
+                W w;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[k] = __float_as_uint(v[4 * h + k]);
+                W* p = reinterpret_cast<W*>(static_cast<float*>(at) + i + 4 * h);
+                if (STREAM) __builtin_nontemporal_store(w, p); else *p = w;
+            }
         }
         return;
     }
 #pragma unroll
-    for (int k = 0; k < kE; ++k)
+    for (int k = 0; k < E; ++k)
         if (k < have) {
             if (bf16) store_f(static_cast<bf16_t*>(at) + i + k, v[k]);
             else store_f(static_cast<float*>(at) + i + k, v[k]);
@@ -194,6 +215,7 @@ __device__ __forceinline__ void encode(const float* m, const float* v, uint32_t*
     const float lift = small ? 0x1p64f : 1.0f;
     // No scale, or one that is no number: all codes are 0.
     const float im = km > 0.f ? __builtin_amdgcn_rcpf(km) : 0.f, iv = kv > 0.f ? __builtin_amdgcn_rcpf(kv) * (small ? 0x1p-32f : 1.0f) : 0.f;
+    const float most_m = km > 0.f && km < __builtin_inff() ? kMostM : 0.f, most_v = kv > 0.f && kv < __builtin_inff() ? kMostV : 0.f;
     qm[0] = qm[1] = qv[0] = qv[1] = 0;
 #pragma unroll
     for (int k = 0; k < kE; ++k) {
@@ -201,7 +223,7 @@ __device__ __forceinline__ void encode(const float* m, const float* v, uint32_t*
         // the root each, at codes up to 255), so only values within 1e-3 of a
         // border are compared with it.
         const float a = fabsf(m[k]), t = __builtin_amdgcn_sqrtf(a * im), r = __builtin_rintf(t);
-        float c = __builtin_fminf(r, static_cast<float>(kMostM));
+        float c = __builtin_fminf(r, most_m);
         if (fabsf(t - r) > 0.499f) {
             const float up = c + 0.5f, down = c - 0.5f;
             if (a > up * up * km && c < kMostM) c += 1.0f;
@@ -210,7 +232,7 @@ __device__ __forceinline__ void encode(const float* m, const float* v, uint32_t*
         const int q = static_cast<int>(c);
         qm[k >> 2] |= (static_cast<uint32_t>(m[k] < 0.f ? -q : q) & 255u) << (8 * (k & 3));
         const float tv = __builtin_amdgcn_sqrtf(__builtin_amdgcn_sqrtf(v[k] * lift) * iv), rv = __builtin_rintf(tv);
-        float d = __builtin_fminf(rv, static_cast<float>(kMostV));
+        float d = __builtin_fminf(rv, most_v);
         if (fabsf(tv - rv) > 0.499f) {
             const float up = (d + 0.5f) * (d + 0.5f) * kv, down = (d - 0.5f) * (d - 0.5f) * kv;
             if (v[k] > up * up && d < kMostV) d += 1.0f;
@@ -232,7 +254,7 @@ __device__ __forceinline__ void update(float& p, float g, float& m, float& v, fl
     p = p * r.keep - m * r.rate * __builtin_amdgcn_rcpf(d);
 }
 
-template <int BITS, int N>
+template <int BITS, int N, bool STREAM>
 __global__ __launch_bounds__(kThreads) void adamw_kernel(Table<N> t, Rates r)
 {
     __shared__ float late[3];
@@ -254,86 +276,104 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Table<N> t, Rates r)
         clip = r.max_norm / (*r.norm + r.norm_eps);
         clip = clip > 1.0f ? 1.0f : clip;  // NaN stays
     }
-    for (uint32_t c = blockIdx.x; c < t.begin[t.n]; c += gridDim.x) {
-        const int k = find(t, c);
-        const uint64_t count = t.count[k] >> 3, first = static_cast<uint64_t>(c - t.begin[k]) * t.chunk;
-        const uint32_t n = static_cast<uint32_t>(count - first < t.chunk ? count - first : t.chunk);
-        const bool pb = t.count[k] & 1, gb = t.count[k] & 2, cb = t.count[k] & 4;
+    const int k = find(t, blockIdx.x);
+    const uint64_t count = t.count[k] >> 3, first = static_cast<uint64_t>(blockIdx.x - t.begin[k]) * kChunk;
+    const uint32_t n = static_cast<uint32_t>(count - first < kChunk ? count - first : kChunk);
+    const bool pb = t.count[k] & 1, gb = t.count[k] & 2, cb = t.count[k] & 4;
+    if constexpr (BITS == 32) {
+        // Four elements a lane, whole lines a load, kU such groups in flight.
+        constexpr int E = 4, kU = 2;
+        for (uint32_t at = threadIdx.x * E; at < n; at += kThreads * E * kU) {
+            float p[kU][E], g[kU][E], m[kU][E], v[kU][E];
+            int have[kU];
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                const uint32_t in = at + u * kThreads * E;
+                const uint64_t i = first + in;
+                have[u] = in < n ? static_cast<int>(n - in < E ? n - in : E) : 0;
+                load_e<E, STREAM>(t.p[k], pb, i, have[u], p[u]);
+                load_e<E, STREAM>(t.g[k], gb, i, have[u], g[u]);
+                load_e<E, STREAM>(t.m[k], false, i, have[u], m[u]);
+                load_e<E, STREAM>(t.v[k], false, i, have[u], v[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                const uint64_t i = first + at + u * kThreads * E;
+#pragma unroll
+                for (int e = 0; e < E; ++e) update(p[u][e], g[u][e], m[u][e], v[u][e], clip, r);
+                store_e<E, STREAM>(t.p[k], pb, i, have[u], p[u]);
+                if (t.copy[k]) store_e<E, STREAM>(t.copy[k], cb, i, have[u], p[u]);
+                store_e<E, STREAM>(t.m[k], false, i, have[u], m[u]);
+                store_e<E, STREAM>(t.v[k], false, i, have[u], v[u]);
+            }
+        }
+    } else {
         // All lanes of a block of 128 go through its step together.
         for (uint32_t at = threadIdx.x * kE; (at & ~static_cast<uint32_t>(kAdamBlock - 1)) < n; at += kThreads * kE) {
             const int have = at < n ? static_cast<int>(n - at < kE ? n - at : kE) : 0;
             const uint64_t i = first + at;
             float p[kE], g[kE], m[kE], v[kE];
             uint32_t qm[2], qv[2];
-            float km = 0.f, kv = 0.f;
-            load_e(t.p[k], pb, i, have, p);
-            load_e(t.g[k], gb, i, have, g);
-            if constexpr (BITS == 8) {
-                load_codes(t.m[k], i, have, qm);
-                load_codes(t.v[k], i, have, qv);
-                km = t.ms[k][i / kAdamBlock];
-                kv = t.vs[k][i / kAdamBlock];
-                decode(qm, qv, km, kv, m, v);
-            } else {
-                load_e(t.m[k], false, i, have, m);
-                load_e(t.v[k], false, i, have, v);
-            }
+            load_e<kE, STREAM>(t.p[k], pb, i, have, p);
+            load_e<kE, STREAM>(t.g[k], gb, i, have, g);
+            load_codes(t.m[k], i, have, qm);
+            load_codes(t.v[k], i, have, qv);
+            float km = t.ms[k][i / kAdamBlock], kv = t.vs[k][i / kAdamBlock];
+            decode(qm, qv, km, kv, m, v);
 #pragma unroll
             for (int e = 0; e < kE; ++e) update(p[e], g[e], m[e], v[e], clip, r);
-            store_e(t.p[k], pb, i, have, p);
-            if (t.copy[k]) store_e(t.copy[k], cb, i, have, p);
-            if constexpr (BITS == 8) {
+            store_e<kE, STREAM>(t.p[k], pb, i, have, p);
+            if (t.copy[k]) store_e<kE, STREAM>(t.copy[k], cb, i, have, p);
 #pragma unroll
-                for (int e = 0; e < kE; ++e)
-                    if (e >= have) m[e] = v[e] = 0.f;
-                encode(m, v, qm, qv, km, kv);
-                store_codes(t.m[k], i, have, qm);
-                store_codes(t.v[k], i, have, qv);
-                if ((threadIdx.x & 15) == 0) {
-                    t.ms[k][i / kAdamBlock] = km;
-                    t.vs[k][i / kAdamBlock] = kv;
-                }
-            } else {
-                store_e(t.m[k], false, i, have, m);
-                store_e(t.v[k], false, i, have, v);
+            for (int e = 0; e < kE; ++e)
+                if (e >= have) m[e] = v[e] = 0.f;
+            encode(m, v, qm, qv, km, kv);
+            store_codes(t.m[k], i, have, qm);
+            store_codes(t.v[k], i, have, qv);
+            if ((threadIdx.x & 15) == 0) {
+                t.ms[k][i / kAdamBlock] = km;
+                t.vs[k][i / kAdamBlock] = kv;
             }
         }
     }
 }
 
 // p: m's values, copy: v's values.
-template <int N>
+template <int N, bool STREAM>
 __global__ __launch_bounds__(kThreads) void moments_kernel(Table<N> t)
 {
-    for (uint32_t c = blockIdx.x; c < t.begin[t.n]; c += gridDim.x) {
-        const int k = find(t, c);
-        const uint64_t count = t.count[k] >> 3, first = static_cast<uint64_t>(c - t.begin[k]) * t.chunk;
-        const uint32_t n = static_cast<uint32_t>(count - first < t.chunk ? count - first : t.chunk);
-        for (uint32_t at = threadIdx.x * kE; at < n; at += kThreads * kE) {
-            const int have = static_cast<int>(n - at < kE ? n - at : kE);
-            const uint64_t i = first + at;
-            uint32_t qm[2], qv[2];
-            float m[kE], v[kE];
-            load_codes(t.m[k], i, have, qm);
-            load_codes(t.v[k], i, have, qv);
-            decode(qm, qv, t.ms[k][i / kAdamBlock], t.vs[k][i / kAdamBlock], m, v);
-            store_e(t.p[k], false, i, have, m);
-            store_e(t.copy[k], false, i, have, v);
-        }
+    const int k = find(t, blockIdx.x);
+    const uint64_t count = t.count[k] >> 3, first = static_cast<uint64_t>(blockIdx.x - t.begin[k]) * kChunk;
+    const uint32_t n = static_cast<uint32_t>(count - first < kChunk ? count - first : kChunk);
+    for (uint32_t at = threadIdx.x * kE; at < n; at += kThreads * kE) {
+        const int have = static_cast<int>(n - at < kE ? n - at : kE);
+        const uint64_t i = first + at;
+        uint32_t qm[2], qv[2];
+        float m[kE], v[kE];
+        load_codes(t.m[k], i, have, qm);
+        load_codes(t.v[k], i, have, qv);
+        decode(qm, qv, t.ms[k][i / kAdamBlock], t.vs[k][i / kAdamBlock], m, v);
+        store_e<kE, STREAM>(t.p[k], false, i, have, m);
+        store_e<kE, STREAM>(t.copy[k], false, i, have, v);
     }
 }
 
-constexpr int kMaxBlocks = 2048;
+// Lists whose step moves more than half of the memory-side cache go past it both
+// ways: nothing in it would be there at the next step (250 M elements, 32-bit
+// states: 1247 us with ordinary accesses, 1251 with streaming stores, 1129 with
+// streaming loads too).
+constexpr size_t kStreamBytes = size_t(128) << 20;
+bool streams(const AdamList& l)
+{
+    size_t bytes = 0;
+    for (int i = 0; i < l.n; ++i) bytes += l.counts[i] * (l.bits == 8 ? 12 : 28);
+    return bytes > kStreamBytes;
+}
 
 // One list, N tensors a launch: `go` launches one table.
 template <int N, typename Go>
 hipError_t each_table(const AdamList& l, float* const* m_out, float* const* v_out, Go go)
 {
-    size_t total = 0;
-    for (int i = 0; i < l.n; ++i) total += l.counts[i];
-    // Elements in a chunk: about one a workgroup for small lists, at most 32768.
-    uint32_t chunk = kThreads * kE;
-    while (chunk < 32768 && total / chunk > kMaxBlocks) chunk *= 2;
     int left = 0;
     for (int i = 0; i < l.n; ++i) left += l.counts[i] != 0;
     hipError_t e = hipSuccess;
@@ -341,12 +381,11 @@ hipError_t each_table(const AdamList& l, float* const* m_out, float* const* v_ou
     for (int i = 0; left > 0 && e == hipSuccess;) {
         Table<N> t;
         t.n = 0;
-        t.chunk = chunk;
         uint64_t chunks = 0;
         for (; i < l.n && t.n < N; ++i) {
             if (l.counts[i] == 0) continue;
-            const uint64_t more = (l.counts[i] + chunk - 1) / chunk;
-            if (t.n > 0 && chunks + more > UINT32_MAX) break;
+            const uint64_t more = (l.counts[i] + kChunk - 1) / kChunk;
+            if (t.n > 0 && chunks + more > INT32_MAX) break;
             t.m[t.n] = l.m[i];
             t.v[t.n] = l.v[i];
             t.ms[t.n] = l.m_scales ? l.m_scales[i] : nullptr;
@@ -368,7 +407,7 @@ hipError_t each_table(const AdamList& l, float* const* m_out, float* const* v_ou
         }
         t.begin[t.n] = static_cast<uint32_t>(chunks);
         events.next(left == 0);
-        e = go(t, dim3(static_cast<unsigned>(std::min<uint64_t>(chunks, kMaxBlocks))));
+        e = go(t, dim3(static_cast<unsigned>(chunks)));
     }
     return e;
 }
@@ -397,9 +436,10 @@ hipError_t launch_adamw(const AdamList& l, const AdamRates& a, hipStream_t s)
     r.lr_dev = a.lr_dev;
     r.step_dev = a.step_dev;
     r.norm = a.norm;
+    const bool stream = streams(l);
     auto run = [&](auto small) {
         constexpr int N = decltype(small)::value;
-        auto kernel = l.bits == 8 ? adamw_kernel<8, N> : adamw_kernel<32, N>;
+        auto kernel = l.bits == 8 ? (stream ? adamw_kernel<8, N, true> : adamw_kernel<8, N, false>) : stream ? adamw_kernel<32, N, true> : adamw_kernel<32, N, false>;
         return each_table<N>(l, nullptr, nullptr, [&](const Table<N>& t, dim3 grid) { return launch(kernel, grid, dim3(kThreads), 0, s, t, r); });
     };
     return l.n <= 12 ? run(std::integral_constant<int, 12>{}) : run(std::integral_constant<int, kTensors>{});
@@ -407,9 +447,10 @@ hipError_t launch_adamw(const AdamList& l, const AdamRates& a, hipStream_t s)
 
 hipError_t launch_adamw_moments(const AdamList& l, float* const* m_out, float* const* v_out, hipStream_t s)
 {
+    const bool stream = streams(l);
     auto run = [&](auto small) {
         constexpr int N = decltype(small)::value;
-        return each_table<N>(l, m_out, v_out, [&](const Table<N>& t, dim3 grid) { return launch(moments_kernel<N>, grid, dim3(kThreads), 0, s, t); });
+        return each_table<N>(l, m_out, v_out, [&](const Table<N>& t, dim3 grid) { return launch(stream ? moments_kernel<N, true> : moments_kernel<N, false>, grid, dim3(kThreads), 0, s, t); });
     };
     return l.n <= 12 ? run(std::integral_constant<int, 12>{}) : run(std::integral_constant<int, kTensors>{});
 }

@@ -137,6 +137,9 @@ def test_not_finite_gradients_show(bits):
     assert torch.isnan(p[[3, 500]]).all() and torch.isfinite(p[[4, 499, 999]]).all()
     values = state if bits == 32 else cm.adamw_moments(state)
     assert torch.isnan(values["m"][0][3]) and not torch.isfinite(values["m"][0][500])
+    if bits == 8:  # a block with such a value holds no numbers, nor codes
+        assert torch.isnan(values["m"][0][:128]).all() and torch.isnan(values["m"][0][384:512]).all()
+        assert (state["m"][0][:128] == 0).all() and (state["m"][0][384:512] == 0).all()
     assert torch.isfinite(values["m"][0][256:384]).all()
 
 
