@@ -8,7 +8,7 @@
 // what changes is written once (fp32 throughout: 28 bytes an element; bf16 with
 // 8-bit states: 10).  Clipping by a norm in hand costs a factor here, where
 // clip_gradients is a pass of its own.  One launch takes a table of up to 48
-// tensors as its argument and has a workgroup for each chunk of 4096 elements.
+// tensors as its argument and has a workgroup for each chunk of them.
 //
 // 8 bits: 128 elements, on 16 lanes, share a scale.  m is the scale times q |q|
 // and the root of v the scale times q^2: steps next to the largest value are
@@ -28,10 +28,12 @@ constexpr int kThreads = 256, kE = 8;  // elements of a lane at once
 constexpr float kTiny = 0x1p-100f;     // blocks below it hold zeros
 constexpr int kMostM = 127, kMostV = 255;
 
-// Elements in a chunk.  Every chunk has a workgroup of its own, which the
-// device gives out as others end: 2048 workgroups that walk over chunks of 32768 took
-// 1427 us where this takes 1129.
-constexpr uint32_t kChunk = 4096;
+// Elements in a chunk: one vector for each lane of a workgroup, four elements
+// with 32-bit states (whole lines a load), eight with 8-bit ones.  Every chunk has a
+// workgroup of its own, which the device gives out as others end (250 M elements,
+// 32-bit states: 2048 workgroups that walk over chunks of 32768 took 1427 us, a
+// workgroup for each 4096, 2048 and 1024 elements 1204, 1128 and 1080).
+constexpr int chunk_of(int bits) { return kThreads * (bits == 32 ? kE / 2 : kE); }
 
 template <int N>
 struct Table {
@@ -277,63 +279,54 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Table<N> t, Rates r)
         clip = clip > 1.0f ? 1.0f : clip;  // NaN stays
     }
     const int k = find(t, blockIdx.x);
+    constexpr uint32_t kChunk = chunk_of(BITS);
     const uint64_t count = t.count[k] >> 3, first = static_cast<uint64_t>(blockIdx.x - t.begin[k]) * kChunk;
     const uint32_t n = static_cast<uint32_t>(count - first < kChunk ? count - first : kChunk);
     const bool pb = t.count[k] & 1, gb = t.count[k] & 2, cb = t.count[k] & 4;
     if constexpr (BITS == 32) {
-        // Four elements a lane, whole lines a load, kU such groups in flight.
-        constexpr int E = 4, kU = 2;
-        for (uint32_t at = threadIdx.x * E; at < n; at += kThreads * E * kU) {
-            float p[kU][E], g[kU][E], m[kU][E], v[kU][E];
-            int have[kU];
+        constexpr int E = kE / 2;
+        const uint32_t at = threadIdx.x * E;
+        if (at >= n) return;
+        const int have = static_cast<int>(n - at < E ? n - at : E);
+        const uint64_t i = first + at;
+        float p[E], g[E], m[E], v[E];
+        load_e<E, STREAM>(t.p[k], pb, i, have, p);
+        load_e<E, STREAM>(t.g[k], gb, i, have, g);
+        load_e<E, STREAM>(t.m[k], false, i, have, m);
+        load_e<E, STREAM>(t.v[k], false, i, have, v);
 #pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                const uint32_t in = at + u * kThreads * E;
-                const uint64_t i = first + in;
-                have[u] = in < n ? static_cast<int>(n - in < E ? n - in : E) : 0;
-                load_e<E, STREAM>(t.p[k], pb, i, have[u], p[u]);
-                load_e<E, STREAM>(t.g[k], gb, i, have[u], g[u]);
-                load_e<E, STREAM>(t.m[k], false, i, have[u], m[u]);
-                load_e<E, STREAM>(t.v[k], false, i, have[u], v[u]);
-            }
-#pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                const uint64_t i = first + at + u * kThreads * E;
-#pragma unroll
-                for (int e = 0; e < E; ++e) update(p[u][e], g[u][e], m[u][e], v[u][e], clip, r);
-                store_e<E, STREAM>(t.p[k], pb, i, have[u], p[u]);
-                if (t.copy[k]) store_e<E, STREAM>(t.copy[k], cb, i, have[u], p[u]);
-                store_e<E, STREAM>(t.m[k], false, i, have[u], m[u]);
-                store_e<E, STREAM>(t.v[k], false, i, have[u], v[u]);
-            }
-        }
+        for (int e = 0; e < E; ++e) update(p[e], g[e], m[e], v[e], clip, r);
+        store_e<E, STREAM>(t.p[k], pb, i, have, p);
+        if (t.copy[k]) store_e<E, STREAM>(t.copy[k], cb, i, have, p);
+        store_e<E, STREAM>(t.m[k], false, i, have, m);
+        store_e<E, STREAM>(t.v[k], false, i, have, v);
     } else {
         // All lanes of a block of 128 go through its step together.
-        for (uint32_t at = threadIdx.x * kE; (at & ~static_cast<uint32_t>(kAdamBlock - 1)) < n; at += kThreads * kE) {
-            const int have = at < n ? static_cast<int>(n - at < kE ? n - at : kE) : 0;
-            const uint64_t i = first + at;
-            float p[kE], g[kE], m[kE], v[kE];
-            uint32_t qm[2], qv[2];
-            load_e<kE, STREAM>(t.p[k], pb, i, have, p);
-            load_e<kE, STREAM>(t.g[k], gb, i, have, g);
-            load_codes(t.m[k], i, have, qm);
-            load_codes(t.v[k], i, have, qv);
-            float km = t.ms[k][i / kAdamBlock], kv = t.vs[k][i / kAdamBlock];
-            decode(qm, qv, km, kv, m, v);
+        const uint32_t at = threadIdx.x * kE;
+        if ((at & ~static_cast<uint32_t>(kAdamBlock - 1)) >= n) return;
+        const int have = at < n ? static_cast<int>(n - at < kE ? n - at : kE) : 0;
+        const uint64_t i = first + at;
+        float p[kE], g[kE], m[kE], v[kE];
+        uint32_t qm[2], qv[2];
+        load_e<kE, STREAM>(t.p[k], pb, i, have, p);
+        load_e<kE, STREAM>(t.g[k], gb, i, have, g);
+        load_codes(t.m[k], i, have, qm);
+        load_codes(t.v[k], i, have, qv);
+        float km = t.ms[k][i / kAdamBlock], kv = t.vs[k][i / kAdamBlock];
+        decode(qm, qv, km, kv, m, v);
 #pragma unroll
-            for (int e = 0; e < kE; ++e) update(p[e], g[e], m[e], v[e], clip, r);
-            store_e<kE, STREAM>(t.p[k], pb, i, have, p);
-            if (t.copy[k]) store_e<kE, STREAM>(t.copy[k], cb, i, have, p);
+        for (int e = 0; e < kE; ++e) update(p[e], g[e], m[e], v[e], clip, r);
+        store_e<kE, STREAM>(t.p[k], pb, i, have, p);
+        if (t.copy[k]) store_e<kE, STREAM>(t.copy[k], cb, i, have, p);
 #pragma unroll
-            for (int e = 0; e < kE; ++e)
-                if (e >= have) m[e] = v[e] = 0.f;
-            encode(m, v, qm, qv, km, kv);
-            store_codes(t.m[k], i, have, qm);
-            store_codes(t.v[k], i, have, qv);
-            if ((threadIdx.x & 15) == 0) {
-                t.ms[k][i / kAdamBlock] = km;
-                t.vs[k][i / kAdamBlock] = kv;
-            }
+        for (int e = 0; e < kE; ++e)
+            if (e >= have) m[e] = v[e] = 0.f;
+        encode(m, v, qm, qv, km, kv);
+        store_codes(t.m[k], i, have, qm);
+        store_codes(t.v[k], i, have, qv);
+        if ((threadIdx.x & 15) == 0) {
+            t.ms[k][i / kAdamBlock] = km;
+            t.vs[k][i / kAdamBlock] = kv;
         }
     }
 }
@@ -343,19 +336,20 @@ template <int N, bool STREAM>
 __global__ __launch_bounds__(kThreads) void moments_kernel(Table<N> t)
 {
     const int k = find(t, blockIdx.x);
+    constexpr uint32_t kChunk = chunk_of(8);
     const uint64_t count = t.count[k] >> 3, first = static_cast<uint64_t>(blockIdx.x - t.begin[k]) * kChunk;
     const uint32_t n = static_cast<uint32_t>(count - first < kChunk ? count - first : kChunk);
-    for (uint32_t at = threadIdx.x * kE; at < n; at += kThreads * kE) {
-        const int have = static_cast<int>(n - at < kE ? n - at : kE);
-        const uint64_t i = first + at;
-        uint32_t qm[2], qv[2];
-        float m[kE], v[kE];
-        load_codes(t.m[k], i, have, qm);
-        load_codes(t.v[k], i, have, qv);
-        decode(qm, qv, t.ms[k][i / kAdamBlock], t.vs[k][i / kAdamBlock], m, v);
-        store_e<kE, STREAM>(t.p[k], false, i, have, m);
-        store_e<kE, STREAM>(t.copy[k], false, i, have, v);
-    }
+    const uint32_t at = threadIdx.x * kE;
+    if (at >= n) return;
+    const int have = static_cast<int>(n - at < kE ? n - at : kE);
+    const uint64_t i = first + at;
+    uint32_t qm[2], qv[2];
+    float m[kE], v[kE];
+    load_codes(t.m[k], i, have, qm);
+    load_codes(t.v[k], i, have, qv);
+    decode(qm, qv, t.ms[k][i / kAdamBlock], t.vs[k][i / kAdamBlock], m, v);
+    store_e<kE, STREAM>(t.p[k], false, i, have, m);
+    store_e<kE, STREAM>(t.copy[k], false, i, have, v);
 }
 
 // Lists whose step moves more than half of the memory-side cache go past it both
@@ -374,6 +368,7 @@ bool streams(const AdamList& l)
 template <int N, typename Go>
 hipError_t each_table(const AdamList& l, float* const* m_out, float* const* v_out, Go go)
 {
+    const uint64_t chunk = chunk_of(l.bits);
     int left = 0;
     for (int i = 0; i < l.n; ++i) left += l.counts[i] != 0;
     hipError_t e = hipSuccess;
@@ -384,7 +379,7 @@ hipError_t each_table(const AdamList& l, float* const* m_out, float* const* v_ou
         uint64_t chunks = 0;
         for (; i < l.n && t.n < N; ++i) {
             if (l.counts[i] == 0) continue;
-            const uint64_t more = (l.counts[i] + kChunk - 1) / kChunk;
+            const uint64_t more = (l.counts[i] + chunk - 1) / chunk;
             if (t.n > 0 && chunks + more > INT32_MAX) break;
             t.m[t.n] = l.m[i];
             t.v[t.n] = l.v[i];
