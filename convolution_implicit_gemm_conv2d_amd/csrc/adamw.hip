@@ -10,7 +10,7 @@
 // clip_gradients is a pass of its own.  One launch takes a table of up to 48
 // tensors as its argument and has a workgroup for each chunk of them.
 //
-// 8 bits: 128 elements, on 16 lanes, share a scale.  m is the scale times q |q|
+// 8 bits: 128 elements, on 32 lanes, share a scale.  m is the scale times q |q|
 // and the root of v the scale times q^2: steps next to the largest value are
 // 1.6 % and 3.1 % and values down to 6e-5 (of the root of v 1.5e-5) of it still have a code of
 // their own, without a table.  A value next to a border is compared with it
@@ -24,16 +24,16 @@
 namespace convmi {
 namespace {
 
-constexpr int kThreads = 256, kE = 8;  // elements of a lane at once
+constexpr int kThreads = 256, kE = 4;  // elements of a lane
 constexpr float kTiny = 0x1p-100f;     // blocks below it hold zeros
 constexpr int kMostM = 127, kMostV = 255;
 
-// Elements in a chunk: one vector for each lane of a workgroup, four elements
-// with 32-bit states (whole lines a load), eight with 8-bit ones.  Every chunk has a
-// workgroup of its own, which the device gives out as others end (250 M elements,
-// 32-bit states: 2048 workgroups that walk over chunks of 32768 took 1427 us, a
-// workgroup for each 4096, 2048 and 1024 elements 1204, 1128 and 1080).
-constexpr int chunk_of(int bits) { return kThreads * (bits == 32 ? kE / 2 : kE); }
+// Elements in a chunk: four a lane of a workgroup, so that fp32 arrays are read
+// and written in whole lines.  Every chunk has a workgroup of its own, which the device
+// gives out as others end (250 M elements, 32-bit states: 2048 workgroups that walk over
+// chunks of 32768 took 1427 us, a workgroup for each 4096, 2048 and 1024 elements
+// 1204, 1128 and 1032).
+constexpr uint32_t kChunk = kThreads * kE;
 
 template <int N>
 struct Table {
@@ -68,106 +68,93 @@ __device__ __forceinline__ int find(const Table<N>& t, uint32_t c)
     return lo;
 }
 
-template <int N>
-struct Words {
-    typedef uint32_t any __attribute__((ext_vector_type(N), aligned(2)));
-};
-
-// E elements from the i-th on; past the `have`-th zeros.
-template <int E, bool STREAM>
+// kE elements from the i-th on; past the `have`-th zeros.
+typedef uint32_t u2_any __attribute__((ext_vector_type(2), aligned(2)));
+template <bool STREAM, typename W>
+__device__ __forceinline__ W get(const W* p)
+{
+    if constexpr (STREAM) return __builtin_nontemporal_load(p);
+    else return *p;
+}
+template <bool STREAM, typename W>
+__device__ __forceinline__ void set(W* p, W w)
+{
+    if constexpr (STREAM) __builtin_nontemporal_store(w, p);
+    else *p = w;
+}
+template <bool STREAM>
 __device__ __forceinline__ void load_e(const void* at, bool bf16, uint64_t i, int have, float* v)
 {
-    if (have >= E) {
+    if (have >= kE) {
         if (bf16) {
-            typedef typename Words<E / 2>::any W;
-            const W* p = reinterpret_cast<const W*>(static_cast<const bf16_t*>(at) + i);
-            const W w = STREAM ? __builtin_nontemporal_load(p) : *p;
+            const u2_any w = get<STREAM>(reinterpret_cast<const u2_any*>(static_cast<const bf16_t*>(at) + i));
 #pragma unroll
-            for (int k = 0; k < E / 2; ++k) {
+            for (int k = 0; k < 2; ++k) {
                 v[2 * k] = __uint_as_float(w[k] << 16);
                 v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
             }
         } else {
-            typedef Words<4>::any W;
+            const uint32x4_any w = get<STREAM>(reinterpret_cast<const uint32x4_any*>(static_cast<const float*>(at) + i));
 #pragma unroll
-            for (int h = 0; h < E / 4; ++h) {
-                const W* p = reinterpret_cast<const W*>(static_cast<const float*>(at) + i + 4 * h);
-                const W w = STREAM ? __builtin_nontemporal_load(p) : *p;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) v[4 * h + k] = __uint_as_float(w[k]);
-            }
+            for (int k = 0; k < 4; ++k) v[k] = __uint_as_float(w[k]);
         }
         return;
     }
 #pragma unroll
-    for (int k = 0; k < E; ++k) {
+    for (int k = 0; k < kE; ++k) {
         v[k] = 0.f;
         if (k < have) v[k] = bf16 ? load_f(static_cast<const bf16_t*>(at) + i + k) : load_f(static_cast<const float*>(at) + i + k);
     }
 }
-template <int E, bool STREAM>
+template <bool STREAM>
 __device__ __forceinline__ void store_e(void* at, bool bf16, uint64_t i, int have, const float* v)
 {
-    if (have >= E) {
+    if (have >= kE) {
         if (bf16) {
-            typedef typename Words<E / 2>::any W;
-            W w;
+            u2_any w;
 #pragma unroll
-            for (int k = 0; k < E / 2; ++k) w[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
-            W* p = reinterpret_cast<W*>(static_cast<bf16_t*>(at) + i);
-            if (STREAM) __builtin_nontemporal_store(w, p); else *p = w;
+            for (int k = 0; k < 2; ++k) w[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+            set<STREAM>(reinterpret_cast<u2_any*>(static_cast<bf16_t*>(at) + i), w);
         } else {
-            typedef Words<4>::any W;
+            uint32x4_any w;
 #pragma unroll
-            for (int h = 0; h < E / 4; ++h) {
-                W w;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) w[k] = __float_as_uint(v[4 * h + k]);
-                W* p = reinterpret_cast<W*>(static_cast<float*>(at) + i + 4 * h);
-                if (STREAM) __builtin_nontemporal_store(w, p); else *p = w;
-            }
+            for (int k = 0; k < 4; ++k) w[k] = __float_as_uint(v[k]);
+            set<STREAM>(reinterpret_cast<uint32x4_any*>(static_cast<float*>(at) + i), w);
         }
         return;
     }
 #pragma unroll
-    for (int k = 0; k < E; ++k)
+    for (int k = 0; k < kE; ++k)
         if (k < have) {
             if (bf16) store_f(static_cast<bf16_t*>(at) + i + k, v[k]);
             else store_f(static_cast<float*>(at) + i + k, v[k]);
         }
 }
 
-typedef uint32_t u2_any __attribute__((ext_vector_type(2), aligned(1)));
-__device__ __forceinline__ void load_codes(const void* at, uint64_t i, int have, uint32_t* q)
+typedef uint32_t word_any __attribute__((aligned(1)));
+__device__ __forceinline__ uint32_t load_codes(const void* at, uint64_t i, int have)
 {
     const uint8_t* p = static_cast<const uint8_t*>(at) + i;
-    q[0] = q[1] = 0;
-    if (have >= kE) {
-        const u2_any w = *reinterpret_cast<const u2_any*>(p);
-        q[0] = w.x;
-        q[1] = w.y;
-    } else {
+    if (have >= kE) return *reinterpret_cast<const word_any*>(p);
+    uint32_t q = 0;
 #pragma unroll
-        for (int k = 0; k < kE; ++k)
-            if (k < have) q[k >> 2] |= static_cast<uint32_t>(p[k]) << (8 * (k & 3));
-    }
+    for (int k = 0; k < kE; ++k)
+        if (k < have) q |= static_cast<uint32_t>(p[k]) << (8 * k);
+    return q;
 }
-__device__ __forceinline__ void store_codes(void* at, uint64_t i, int have, const uint32_t* q)
+__device__ __forceinline__ void store_codes(void* at, uint64_t i, int have, uint32_t q)
 {
     uint8_t* p = static_cast<uint8_t*>(at) + i;
     if (have >= kE) {
-        u2_any w;
-        w.x = q[0];
-        w.y = q[1];
-        *reinterpret_cast<u2_any*>(p) = w;
+        *reinterpret_cast<word_any*>(p) = q;
     } else {
 #pragma unroll
         for (int k = 0; k < kE; ++k)
-            if (k < have) p[k] = static_cast<uint8_t>(q[k >> 2] >> (8 * (k & 3)));
+            if (k < have) p[k] = static_cast<uint8_t>(q >> (8 * k));
     }
 }
 
-// The 16 lanes of a block.
+// Over the 32 lanes of a block.
 __device__ __forceinline__ uint32_t block_max(uint32_t v)
 {
 #define CONVMI_MAX(CTRL) v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xf, 0xf, false)))
@@ -176,7 +163,8 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v)
     CONVMI_MAX(0x122);
     CONVMI_MAX(0x121);
 #undef CONVMI_MAX
-    return v;
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);  // the other row of 16
+    return max(static_cast<uint32_t>(r[0]), static_cast<uint32_t>(r[1]));
 }
 
 #pragma clang fp contract(off)
@@ -191,17 +179,17 @@ __device__ __forceinline__ float v_of(uint32_t byte, float scale)
     const float q = static_cast<float>(byte), r = q * q * scale;
     return r * r;
 }
-__device__ __forceinline__ void decode(const uint32_t* qm, const uint32_t* qv, float km, float kv, float* m, float* v)
+__device__ __forceinline__ void decode(uint32_t qm, uint32_t qv, float km, float kv, float* m, float* v)
 {
 #pragma unroll
     for (int k = 0; k < kE; ++k) {
-        m[k] = m_of((qm[k >> 2] >> (8 * (k & 3))) & 255u, km);
-        v[k] = v_of((qv[k >> 2] >> (8 * (k & 3))) & 255u, kv);
+        m[k] = m_of((qm >> (8 * k)) & 255u, km);
+        v[k] = v_of((qv >> (8 * k)) & 255u, kv);
     }
 }
 
 // Codes of a block's m and v, and its scales.
-__device__ __forceinline__ void encode(const float* m, const float* v, uint32_t* qm, uint32_t* qv, float& km, float& kv)
+__device__ __forceinline__ void encode(const float* m, const float* v, uint32_t& qm, uint32_t& qv, float& km, float& kv)
 {
     uint32_t top_m = 0, top_v = 0;  // as bits: a NaN is above everything
 #pragma unroll
@@ -218,7 +206,7 @@ __device__ __forceinline__ void encode(const float* m, const float* v, uint32_t*
     // No scale, or one that is no number: all codes are 0.
     const float im = km > 0.f ? __builtin_amdgcn_rcpf(km) : 0.f, iv = kv > 0.f ? __builtin_amdgcn_rcpf(kv) * (small ? 0x1p-32f : 1.0f) : 0.f;
     const float most_m = km > 0.f && km < __builtin_inff() ? kMostM : 0.f, most_v = kv > 0.f && kv < __builtin_inff() ? kMostV : 0.f;
-    qm[0] = qm[1] = qv[0] = qv[1] = 0;
+    qm = qv = 0;
 #pragma unroll
     for (int k = 0; k < kE; ++k) {
         // The guess is off by 2e-4 at most (two roundings of the reciprocal and
@@ -232,7 +220,7 @@ __device__ __forceinline__ void encode(const float* m, const float* v, uint32_t*
             else if (c > 0.f && !(a > down * down * km)) c -= 1.0f;
         }
         const int q = static_cast<int>(c);
-        qm[k >> 2] |= (static_cast<uint32_t>(m[k] < 0.f ? -q : q) & 255u) << (8 * (k & 3));
+        qm |= (static_cast<uint32_t>(m[k] < 0.f ? -q : q) & 255u) << (8 * k);
         const float tv = __builtin_amdgcn_sqrtf(__builtin_amdgcn_sqrtf(v[k] * lift) * iv), rv = __builtin_rintf(tv);
         float d = __builtin_fminf(rv, most_v);
         if (fabsf(tv - rv) > 0.499f) {
@@ -241,7 +229,7 @@ __device__ __forceinline__ void encode(const float* m, const float* v, uint32_t*
             else if (d > 0.f && !(v[k] > down * down)) d -= 1.0f;
         }
         const uint32_t w = static_cast<uint32_t>(d);
-        qv[k >> 2] |= (w == 0 && v[k] > 0.f && kv > 0.f ? 1u : w) << (8 * (k & 3));
+        qv |= (w == 0 && v[k] > 0.f && kv > 0.f ? 1u : w) << (8 * k);
     }
 }
 
@@ -279,55 +267,42 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Table<N> t, Rates r)
         clip = clip > 1.0f ? 1.0f : clip;  // NaN stays
     }
     const int k = find(t, blockIdx.x);
-    constexpr uint32_t kChunk = chunk_of(BITS);
     const uint64_t count = t.count[k] >> 3, first = static_cast<uint64_t>(blockIdx.x - t.begin[k]) * kChunk;
-    const uint32_t n = static_cast<uint32_t>(count - first < kChunk ? count - first : kChunk);
+    const uint32_t n = static_cast<uint32_t>(count - first < kChunk ? count - first : kChunk), at = threadIdx.x * kE;
+    // With 8 bits all lanes of a block of 128 go through its step together.
+    if ((BITS == 8 ? at & ~static_cast<uint32_t>(kAdamBlock - 1) : at) >= n) return;
     const bool pb = t.count[k] & 1, gb = t.count[k] & 2, cb = t.count[k] & 4;
-    if constexpr (BITS == 32) {
-        constexpr int E = kE / 2;
-        const uint32_t at = threadIdx.x * E;
-        if (at >= n) return;
-        const int have = static_cast<int>(n - at < E ? n - at : E);
-        const uint64_t i = first + at;
-        float p[E], g[E], m[E], v[E];
-        load_e<E, STREAM>(t.p[k], pb, i, have, p);
-        load_e<E, STREAM>(t.g[k], gb, i, have, g);
-        load_e<E, STREAM>(t.m[k], false, i, have, m);
-        load_e<E, STREAM>(t.v[k], false, i, have, v);
-#pragma unroll
-        for (int e = 0; e < E; ++e) update(p[e], g[e], m[e], v[e], clip, r);
-        store_e<E, STREAM>(t.p[k], pb, i, have, p);
-        if (t.copy[k]) store_e<E, STREAM>(t.copy[k], cb, i, have, p);
-        store_e<E, STREAM>(t.m[k], false, i, have, m);
-        store_e<E, STREAM>(t.v[k], false, i, have, v);
+    const int have = at < n ? static_cast<int>(n - at < kE ? n - at : kE) : 0;
+    const uint64_t i = first + at;
+    float p[kE], g[kE], m[kE], v[kE];
+    load_e<STREAM>(t.p[k], pb, i, have, p);
+    load_e<STREAM>(t.g[k], gb, i, have, g);
+    if constexpr (BITS == 8) {
+        decode(load_codes(t.m[k], i, have), load_codes(t.v[k], i, have), t.ms[k][i / kAdamBlock], t.vs[k][i / kAdamBlock], m, v);
     } else {
-        // All lanes of a block of 128 go through its step together.
-        const uint32_t at = threadIdx.x * kE;
-        if ((at & ~static_cast<uint32_t>(kAdamBlock - 1)) >= n) return;
-        const int have = at < n ? static_cast<int>(n - at < kE ? n - at : kE) : 0;
-        const uint64_t i = first + at;
-        float p[kE], g[kE], m[kE], v[kE];
-        uint32_t qm[2], qv[2];
-        load_e<kE, STREAM>(t.p[k], pb, i, have, p);
-        load_e<kE, STREAM>(t.g[k], gb, i, have, g);
-        load_codes(t.m[k], i, have, qm);
-        load_codes(t.v[k], i, have, qv);
-        float km = t.ms[k][i / kAdamBlock], kv = t.vs[k][i / kAdamBlock];
-        decode(qm, qv, km, kv, m, v);
+        load_e<STREAM>(t.m[k], false, i, have, m);
+        load_e<STREAM>(t.v[k], false, i, have, v);
+    }
 #pragma unroll
-        for (int e = 0; e < kE; ++e) update(p[e], g[e], m[e], v[e], clip, r);
-        store_e<kE, STREAM>(t.p[k], pb, i, have, p);
-        if (t.copy[k]) store_e<kE, STREAM>(t.copy[k], cb, i, have, p);
+    for (int e = 0; e < kE; ++e) update(p[e], g[e], m[e], v[e], clip, r);
+    store_e<STREAM>(t.p[k], pb, i, have, p);
+    if (t.copy[k]) store_e<STREAM>(t.copy[k], cb, i, have, p);
+    if constexpr (BITS == 8) {
 #pragma unroll
         for (int e = 0; e < kE; ++e)
             if (e >= have) m[e] = v[e] = 0.f;
+        uint32_t qm, qv;
+        float km, kv;
         encode(m, v, qm, qv, km, kv);
         store_codes(t.m[k], i, have, qm);
         store_codes(t.v[k], i, have, qv);
-        if ((threadIdx.x & 15) == 0) {
+        if ((threadIdx.x & (kAdamBlock / kE - 1)) == 0) {
             t.ms[k][i / kAdamBlock] = km;
             t.vs[k][i / kAdamBlock] = kv;
         }
+    } else {
+        store_e<STREAM>(t.m[k], false, i, have, m);
+        store_e<STREAM>(t.v[k], false, i, have, v);
     }
 }
 
@@ -336,20 +311,15 @@ template <int N, bool STREAM>
 __global__ __launch_bounds__(kThreads) void moments_kernel(Table<N> t)
 {
     const int k = find(t, blockIdx.x);
-    constexpr uint32_t kChunk = chunk_of(8);
     const uint64_t count = t.count[k] >> 3, first = static_cast<uint64_t>(blockIdx.x - t.begin[k]) * kChunk;
-    const uint32_t n = static_cast<uint32_t>(count - first < kChunk ? count - first : kChunk);
-    const uint32_t at = threadIdx.x * kE;
+    const uint32_t n = static_cast<uint32_t>(count - first < kChunk ? count - first : kChunk), at = threadIdx.x * kE;
     if (at >= n) return;
     const int have = static_cast<int>(n - at < kE ? n - at : kE);
     const uint64_t i = first + at;
-    uint32_t qm[2], qv[2];
     float m[kE], v[kE];
-    load_codes(t.m[k], i, have, qm);
-    load_codes(t.v[k], i, have, qv);
-    decode(qm, qv, t.ms[k][i / kAdamBlock], t.vs[k][i / kAdamBlock], m, v);
-    store_e<kE, STREAM>(t.p[k], false, i, have, m);
-    store_e<kE, STREAM>(t.copy[k], false, i, have, v);
+    decode(load_codes(t.m[k], i, have), load_codes(t.v[k], i, have), t.ms[k][i / kAdamBlock], t.vs[k][i / kAdamBlock], m, v);
+    store_e<STREAM>(t.p[k], false, i, have, m);
+    store_e<STREAM>(t.copy[k], false, i, have, v);
 }
 
 // Lists whose step moves more than half of the memory-side cache go past it both
@@ -368,7 +338,6 @@ bool streams(const AdamList& l)
 template <int N, typename Go>
 hipError_t each_table(const AdamList& l, float* const* m_out, float* const* v_out, Go go)
 {
-    const uint64_t chunk = chunk_of(l.bits);
     int left = 0;
     for (int i = 0; i < l.n; ++i) left += l.counts[i] != 0;
     hipError_t e = hipSuccess;
@@ -379,7 +348,7 @@ hipError_t each_table(const AdamList& l, float* const* m_out, float* const* v_ou
         uint64_t chunks = 0;
         for (; i < l.n && t.n < N; ++i) {
             if (l.counts[i] == 0) continue;
-            const uint64_t more = (l.counts[i] + chunk - 1) / chunk;
+            const uint64_t more = (l.counts[i] + kChunk - 1) / kChunk;
             if (t.n > 0 && chunks + more > INT32_MAX) break;
             t.m[t.n] = l.m[i];
             t.v[t.n] = l.v[i];
