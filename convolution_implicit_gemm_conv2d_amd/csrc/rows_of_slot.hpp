@@ -5,33 +5,37 @@
 
 namespace convmi {
 
-// Calls f(row, slot) for the rows that the workgroup of `row` has to do: `row`
-// itself, and the later ones of the same slot after it, in order; none if an
-// earlier row has that slot, since that row's workgroup does them all.  A slot
-// outside the pool is a row without a state: f(row, -1).  Without slots a row's
-// slot is its number.  All threads of the workgroup call it.
-template <typename F>
-__device__ __forceinline__ void each_row_of_slot(const int* slots, int rows, int count, int row, F f)
+// Does the rows that the workgroup of `row` has to do: `row` itself, and the
+// later ones of the same slot after it, in order; none if an earlier row has that
+// slot, since that row's workgroup does them all.  read(row, slot) loads what a row
+// needs, finish(row, slot) computes and stores it; absent(row) is called for a row
+// whose slot lies outside the pool.  Without slots a row's slot is its number.  All threads
+// of the workgroup call it.  The rows' own loads are out while the slots are
+// compared.
+template <typename R, typename F, typename A>
+__device__ __forceinline__ void each_row_of_slot(const int* slots, int rows, int count, int row, R read, F finish, A absent)
 {
-    if (!slots) {
-        f(row, row);
-        return;
-    }
-    const int slot = slots[row];
+    const int slot = slots ? slots[row] : row;
     if (slot < 0 || slot >= count) {
-        f(row, -1);
+        absent(row);
         return;
     }
-    bool other = false;
-    for (int i = threadIdx.x; i < rows; i += blockDim.x) other |= i != row && slots[i] == slot;
-    if (!__syncthreads_or(other)) {
-        f(row, slot);
-        return;
+    read(row, slot);
+    if (slots) {
+        bool other = false;
+        for (int i = threadIdx.x; i < rows; i += blockDim.x) other |= i != row && slots[i] == slot;
+        if (__syncthreads_or(other)) {
+            for (int i = 0; i < row; ++i)
+                if (slots[i] == slot) return;
+            for (int i = row; i < rows; ++i)
+                if (slots[i] == slot) {  // each thread reads back only what it wrote itself
+                    read(i, slot);
+                    finish(i, slot);
+                }
+            return;
+        }
     }
-    for (int i = 0; i < row; ++i)
-        if (slots[i] == slot) return;
-    for (int i = row; i < rows; ++i)
-        if (slots[i] == slot) f(i, slot);  // each thread reads back only what it wrote itself
+    finish(row, slot);
 }
 
 }  // namespace convmi

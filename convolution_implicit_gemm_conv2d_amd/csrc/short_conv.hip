@@ -402,31 +402,41 @@ template <typename T>
 __global__ __launch_bounds__(kThreads) void causal_step_kernel(CausalArgs a, int count, int blocks)
 {
     const int row = static_cast<int>(blockIdx.x / blocks), c = static_cast<int>(blockIdx.x % blocks) * kThreads + threadIdx.x;
-    each_row_of_slot(a.slots, static_cast<int>(a.rows), count, row, [&](int r, int slot) {
-        if (c >= a.C) return;
-        T* y = static_cast<T*>(a.y) + static_cast<int64_t>(r) * a.C + c;
-        if (slot < 0) {
-            if (a.clear) store_f(y, 0.f);
-            return;
-        }
-        const T* w = static_cast<const T*>(a.w) + static_cast<int64_t>(c) * a.K;
-        T* state = static_cast<T*>(a.state) + static_cast<int64_t>(slot) * (a.K - 1) * a.C + c;
-        const T x = static_cast<const T*>(a.x)[r * a.xs + c];
-        T old[kCausalTaps - 1];
+    const bool on = c < a.C;
+    const int K = a.K, cc = on ? c : 0;  // lanes behind the last channel read the first one
+    T x = T(0), old[kCausalTaps - 1], w[kCausalTaps], b = T(0);
+    auto at = [&](int slot) { return static_cast<T*>(a.state) + static_cast<int64_t>(slot) * (K - 1) * a.C + cc; };
+    each_row_of_slot(
+        a.slots, static_cast<int>(a.rows), count, row,
+        [&](int r, int slot) {
+            const T* state = at(slot);
+            x = static_cast<const T*>(a.x)[r * a.xs + cc];
 #pragma unroll
-        for (int k = 0; k < kCausalTaps - 1; ++k)
-            if (k < a.K - 1) old[k] = state[static_cast<int64_t>(k) * a.C];
-        float p = a.bias ? load_f(static_cast<const T*>(a.bias) + c) : 0.f;
+            for (int k = 0; k < kCausalTaps - 1; ++k)
+                if (k < K - 1) old[k] = state[static_cast<int64_t>(k) * a.C];
 #pragma unroll
-        for (int k = 0; k < kCausalTaps - 1; ++k)
-            if (k < a.K - 1) {
-                p = __builtin_fmaf(load_f(w + k), load_f(&old[k]), p);
-                if (k > 0) state[static_cast<int64_t>(k - 1) * a.C] = old[k];
-            }
-        p = __builtin_fmaf(load_f(w + a.K - 1), load_f(&x), p);
-        state[static_cast<int64_t>(a.K - 2) * a.C] = x;
-        store_f(y, act_value(a.act, p));
-    });
+            for (int k = 0; k < kCausalTaps; ++k)
+                if (k < K) w[k] = static_cast<const T*>(a.w)[static_cast<int64_t>(cc) * K + k];
+            if (a.bias) b = static_cast<const T*>(a.bias)[cc];
+        },
+        [&](int r, int slot) {
+            if (!on) return;
+            T* state = at(slot);
+            float p = load_f(&b), last = 0.f;
+#pragma unroll
+            for (int k = 0; k < kCausalTaps; ++k)
+                if (k < K) {
+                    if (k < K - 1) p = __builtin_fmaf(load_f(&w[k]), load_f(&old[k < kCausalTaps - 1 ? k : 0]), p);
+                    else last = load_f(&w[k]);
+                    if (k > 0 && k < K - 1) state[static_cast<int64_t>(k - 1) * a.C] = old[k < kCausalTaps - 1 ? k : 0];
+                }
+            p = __builtin_fmaf(last, load_f(&x), p);
+            state[static_cast<int64_t>(K - 2) * a.C] = x;
+            store_f(static_cast<T*>(a.y) + static_cast<int64_t>(r) * a.C + c, act_value(a.act, p));
+        },
+        [&](int r) {
+            if (on && a.clear) store_f(static_cast<T*>(a.y) + static_cast<int64_t>(r) * a.C + c, 0.f);
+        });
 }
 
 // Channels of a lane: four, or one where there are fewer.  Two would leave room
