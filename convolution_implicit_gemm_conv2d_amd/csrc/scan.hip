@@ -36,11 +36,13 @@ int64_t waves_of(const ScanArgs& a, int gr) { return static_cast<int64_t>(a.grou
 
 Plan plan(ScanArgs& a, bool packed, bool gradient)
 {
-    const int few = a.n <= 16 ? 4 : a.n <= 32 ? 8 : 16, many = few == 4 ? 8 : few;
+    const int few = a.n <= 16 ? 4 : a.n <= 32 ? 8 : 16, many = a.n <= 4 ? 4 : a.n <= 32 ? 8 : 16;
     const bool whole = a.rows == 0 || (!packed && a.seqs * waves_of(a, many) >= kSimds);
     Plan p;
     p.gr = gradient || (whole && a.seqs * waves_of(a, few) < 2 * kSimds) ? many : few;
     p.ns = (a.n + p.gr - 1) / p.gr;
+    // three states of a lane cost the gradient more registers than four
+    if (gradient && p.ns == 3) p.ns = 4;
     a.blocks = static_cast<int>(blocks_of(a, p.gr));
     a.pieces = 0;
     a.piece_rows = 0;

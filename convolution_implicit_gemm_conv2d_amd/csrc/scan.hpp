@@ -113,6 +113,7 @@ struct Lanes {
     static constexpr int CH = 64 / GR;        // channels of a wave
     static constexpr int R = kTile / GR;      // rows of a tile that a lane prepares and finishes
     static constexpr int NP = GR * NS;        // states, padded
+    static constexpr int SP = NS == 3 ? 4 : NS, LP = GR * SP;  // a group's and a row's place in LDS: aligned reads
     static constexpr int ROWS = 64 / NP;      // whole rows of B that a wave loads at once
     static constexpr int LOADS = (kTile + ROWS - 1) / ROWS;
     int lane, wave, ch, grp, row;  // row: of each GR rows the one that is this lane's
@@ -241,7 +242,7 @@ struct Shared {
           cs(static_cast<uint32_t>(a.cs) * sizeof(T))
     {
         const int r = l.lane / L::NP, n = l.lane % L::NP;
-        at = r < L::ROWS ? r * L::NP + n : -1;
+        at = r < L::ROWS ? r * L::LP + n / NS * L::SP + n % NS : -1;
         const bool on = at >= 0 && n < a.n;
         ob = on ? r * bs + n * static_cast<uint32_t>(sizeof(T)) : kOutside;
         oc = on ? r * cs + n * static_cast<uint32_t>(sizeof(T)) : kOutside;
@@ -264,9 +265,9 @@ struct Shared {
         if (at < 0) return;
 #pragma unroll
         for (int i = 0; i < L::LOADS; ++i)
-            if ((i + 1) * L::ROWS <= kTile || at + i * L::ROWS * L::NP < kTile * L::NP) {
-                to_b[at + i * L::ROWS * L::NP] = load_f(&b[i]);
-                to_c[at + i * L::ROWS * L::NP] = load_f(&c[i]);
+            if ((i + 1) * L::ROWS <= kTile || at + i * L::ROWS * L::LP < kTile * L::LP) {
+                to_b[at + i * L::ROWS * L::LP] = load_f(&b[i]);
+                to_c[at + i * L::ROWS * L::LP] = load_f(&c[i]);
             }
     }
 };

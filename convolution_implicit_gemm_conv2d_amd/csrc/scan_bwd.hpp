@@ -52,9 +52,9 @@ template <typename T, int GR, int NS>
 __global__ __launch_bounds__(kThreads) void back_kernel(ScanArgs a)
 {
     typedef Lanes<GR, NS> L;
-    constexpr int CH = L::CH, R = L::R, NP = L::NP;
+    constexpr int CH = L::CH, R = L::R, LP = L::LP;
     __shared__ float2 lds_d[kWaves][kTile][CH];
-    __shared__ float lds_b[kWaves][kTile * NP], lds_c[kWaves][kTile * NP];
+    __shared__ float lds_b[kWaves][kTile * LP], lds_c[kWaves][kTile * LP];
     const uint32_t cb = static_cast<uint32_t>(a.groups) * a.blocks;
     const int item = static_cast<int>(blockIdx.x / cb);
     const L l(a, blockIdx.x % cb);
@@ -114,7 +114,7 @@ __global__ __launch_bounds__(kThreads) void back_kernel(ScanArgs a)
 #pragma unroll
         for (int r = kTile - 1; r >= 0; --r) {
             const float2 v = dd[r][l.ch];
-            const float* c = sc + r * NP + l.n0;
+            const float* c = sc + r * LP + l.grp * L::SP;
             total += v.x;
 #pragma unroll
             for (int j = 0; j < NS; ++j) g[j] = __builtin_fmaf(c[j], v.y, g[j]) * exp2_hw(v.x * A[j]);
@@ -125,15 +125,15 @@ __global__ __launch_bounds__(kThreads) void back_kernel(ScanArgs a)
 }
 
 template <typename T, int GR, int NS>
-__global__ __launch_bounds__(kThreads) void bwd_kernel(ScanArgs a)
+__global__ __launch_bounds__(kThreads, 2) void bwd_kernel(ScanArgs a)
 {
     typedef Lanes<GR, NS> L;
-    constexpr int CH = L::CH, R = L::R, NP = L::NP;
+    constexpr int CH = L::CH, R = L::R, NP = L::NP, LP = L::LP;
     constexpr int V = pow2_of(2 * NS);                                   // values of dB and dC a row, padded
     constexpr int RB = CH / V < 1 ? 1 : CH / V > GR ? GR : CH / V;       // rows merged at once
     constexpr int K = V * RB, KEPT = K > CH ? K / CH : 1;
     __shared__ float4 lds_d[kWaves][kTile][CH];
-    __shared__ float lds_b[kWaves][kTile * NP], lds_c[kWaves][kTile * NP];
+    __shared__ float lds_b[kWaves][kTile * LP], lds_c[kWaves][kTile * LP];
     __shared__ float lds_part[2][kWaves][kTile * 2 * NP];
 
     const uint32_t cb = static_cast<uint32_t>(a.groups) * a.blocks, block = blockIdx.x % cb;
@@ -226,7 +226,7 @@ __global__ __launch_bounds__(kThreads) void bwd_kernel(ScanArgs a)
             to -= rows;
             load(to);
             // ------------------------------------------- states again --
-            constexpr int G = NS <= 2 ? kGroup : kGroup / 2, NG = kTile / G;  // rows whose operands are read at once
+            constexpr int G = NS <= 2 ? kGroup : 1, NG = kTile / G;  // rows whose operands are read at once
             static_assert(NG % 2 == 0, "operands alternate");
             typedef Operands<NS, G, float4> Ops;
             Ops ops[2];
@@ -236,12 +236,13 @@ __global__ __launch_bounds__(kThreads) void bwd_kernel(ScanArgs a)
                     o.d[r] = dd[group * G + r][l.ch];
 #pragma unroll
                     for (int j = 0; j < NS; ++j) {
-                        o.b[r][j] = sb[(group * G + r) * NP + l.n0 + j];
-                        o.c[r][j] = sc[(group * G + r) * NP + l.n0 + j];
+                        o.b[r][j] = sb[(group * G + r) * LP + l.grp * L::SP + j];
+                        o.c[r][j] = sc[(group * G + r) * LP + l.grp * L::SP + j];
                     }
                 }
             };
-            float hs[kTile][NS], as[kTile][NS], v[kTile];
+            constexpr bool kKeep = NS <= 2;
+            float hs[kTile][NS], as[kKeep ? kTile : 1][NS], v[kTile];
             fetch(ops[0], 0);
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
@@ -254,8 +255,9 @@ __global__ __launch_bounds__(kThreads) void bwd_kernel(ScanArgs a)
                     v[k] = 0.f;
 #pragma unroll
                     for (int j = 0; j < NS; ++j) {
-                        as[k][j] = exp2_hw(o.d[r].x * A[j]);
-                        hs[k][j] = __builtin_fmaf(as[k][j], k ? hs[k ? k - 1 : 0][j] : first[j], o.d[r].y * o.b[r][j]);
+                        const float f = exp2_hw(o.d[r].x * A[j]);
+                        if (kKeep) as[kKeep ? k : 0][j] = f;
+                        hs[k][j] = __builtin_fmaf(f, k ? hs[k ? k - 1 : 0][j] : first[j], o.d[r].y * o.b[r][j]);
                         v[k] = __builtin_fmaf(hs[k][j], o.c[r][j], v[k]);
                     }
                 }
@@ -285,7 +287,7 @@ __global__ __launch_bounds__(kThreads) void bwd_kernel(ScanArgs a)
                         m[in * V + j] = e * o.d[r].y;
                         m[in * V + NS + j] = o.d[r].z * hs[k][j];
                         w[k] = __builtin_fmaf(e, o.b[r][j], w[k]);
-                        g[j] = e * as[k][j];
+                        g[j] = e * (kKeep ? as[kKeep ? k : 0][j] : exp2_hw(o.d[r].x * A[j]));
                         const float q = g[j] * (k ? hs[k ? k - 1 : 0][j] : first[j]);
                         u[k] = __builtin_fmaf(A[j], q, u[k]);
                         da[j] = __builtin_fmaf(o.d[r].x, q, da[j]);

@@ -39,10 +39,10 @@ template <typename T, int GR, int NS, int WANT>
 __global__ __launch_bounds__(kThreads) void fwd_kernel(ScanArgs a)
 {
     typedef Lanes<GR, NS> L;
-    constexpr int CH = L::CH, R = L::R, NP = L::NP;
+    constexpr int CH = L::CH, R = L::R, LP = L::LP;
     // two tiles: while one is worked on, the next one is prepared
     __shared__ float2 lds_d[kWaves][2][kTile][CH];
-    __shared__ float lds_b[kWaves][2][kTile * NP], lds_c[kWaves][2][kTile * NP];
+    __shared__ float lds_b[kWaves][2][kTile * LP], lds_c[kWaves][2][kTile * LP];
 
     const uint32_t cb = static_cast<uint32_t>(a.groups) * a.blocks;
     const int item = static_cast<int>(blockIdx.x / cb);
@@ -115,8 +115,8 @@ __global__ __launch_bounds__(kThreads) void fwd_kernel(ScanArgs a)
                 o.d[r] = lds_d[l.wave][turn][row + r][l.ch];
 #pragma unroll
                 for (int j = 0; j < NS; ++j) {
-                    o.b[r][j] = lds_b[l.wave][turn][(row + r) * NP + l.n0 + j];
-                    if (WANT == kOutputs) o.c[r][j] = lds_c[l.wave][turn][(row + r) * NP + l.n0 + j];
+                    o.b[r][j] = lds_b[l.wave][turn][(row + r) * LP + l.grp * L::SP + j];
+                    if (WANT == kOutputs) o.c[r][j] = lds_c[l.wave][turn][(row + r) * LP + l.grp * L::SP + j];
                 }
             }
         };

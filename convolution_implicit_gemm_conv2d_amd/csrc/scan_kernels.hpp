@@ -11,6 +11,7 @@ namespace scan {
 template <typename T, int GR, int NS>
 hipError_t run_one(int run, const ScanArgs& a, int items, hipStream_t s)
 {
+    constexpr bool kGradient = NS != 3 && (GR > 4 || NS == 1);  // what the plan takes for it
     const int64_t blocks = static_cast<int64_t>(a.groups) * a.blocks * items;
     if (run == kRunSums) {
         const int64_t n = (a.rows * 2 * a.n + 255) / 256;
@@ -24,10 +25,10 @@ hipError_t run_one(int run, const ScanArgs& a, int items, hipStream_t s)
     case kRunStates: return launch(fwd_kernel<T, GR, NS, kStates>, grid, threads, 0, s, a);
     case kRunEnds: return launch(fwd_kernel<T, GR, NS, kEnds>, grid, threads, 0, s, a);
     case kRunBack:
-        if constexpr (GR > 4) return launch(back_kernel<T, GR, NS>, grid, threads, 0, s, a);
-        else return hipErrorInvalidConfiguration;  // the gradient has eight groups at least
+        if constexpr (kGradient) return launch(back_kernel<T, GR, NS>, grid, threads, 0, s, a);
+        else return hipErrorInvalidConfiguration;
     default:
-        if constexpr (GR > 4) return launch(bwd_kernel<T, GR, NS>, grid, threads, 0, s, a);
+        if constexpr (kGradient) return launch(bwd_kernel<T, GR, NS>, grid, threads, 0, s, a);
         else return hipErrorInvalidConfiguration;
     }
 }
