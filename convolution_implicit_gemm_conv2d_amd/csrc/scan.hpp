@@ -228,6 +228,32 @@ struct Rows {
     }
 };
 
+// This lane's states of a [channels, n] array of fp32, through a buffer: whole
+// groups of NS states in one access where n is a multiple of NS.
+template <int GR, int NS>
+struct States {
+    uint32_t off;  // bytes
+    int have;      // states of this lane
+    bool whole;
+    __device__ States(const ScanArgs& a, const Lanes<GR, NS>& l)
+    {
+        have = l.on ? a.n - l.n0 : 0;
+        whole = a.n % NS == 0;
+        off = have > 0 ? (static_cast<uint32_t>(l.c) * a.n + l.n0) * 4 : kOutside;
+    }
+    __device__ void put(rsrc_t r, const float* v) const
+    {
+        if (NS == 2 && whole) {
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(decltype(__builtin_amdgcn_raw_buffer_load_b64(r, 0, 0, 0)), make_uint2(__float_as_uint(v[0]), __float_as_uint(v[NS > 1 ? 1 : 0]))), r, off, 0, 0);
+        } else if (NS == 4 && whole) {
+            buffer_store16(r, off, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[NS > 1 ? 1 : 0]), __float_as_uint(v[NS > 2 ? 2 : 0]), __float_as_uint(v[NS > 3 ? 3 : 0])));
+        } else {
+#pragma unroll
+            for (int j = 0; j < NS; ++j) scan::put(r, j < have ? off + 4 * j : kOutside, v[j], 0.f);
+        }
+    }
+};
+
 // B and C of a tile, in flight to the wave's LDS.
 template <typename T, int GR, int NS>
 struct Shared {

@@ -56,6 +56,7 @@ __global__ __launch_bounds__(kThreads) void fwd_kernel(ScanArgs a)
     const float bias = a.bias ? a.bias[l.c] : 0.f, skip = a.D ? a.D[l.c] : 0.f;
     const int64_t states = static_cast<int64_t>(a.channels) * a.n;
     const bool gate = WANT == kOutputs && a.z;
+    const States<GR, NS> kept(a, l);
 
     for (int s = share.first; s < share.last; ++s) {
         const Span span = span_of(a, s);
@@ -137,7 +138,8 @@ __global__ __launch_bounds__(kThreads) void fwd_kernel(ScanArgs a)
         // dependent chains that cost little time of their own there.
         auto work = [&](Raw& w, int turn) __attribute__((always_inline)) {
             const int here = rows;
-            if (WANT != kEnds && a.saved && at > span.begin) l.write(a, a.saved + static_cast<int64_t>(at / kTile) * states, h);
+            if (WANT != kEnds && a.saved && at > span.begin)
+                kept.put(make_rsrc(a.saved + static_cast<int64_t>(at / kTile) * states, static_cast<uint32_t>(states) * 4), h);
             at += rows;
             rows = rows_from(at, end);
             prepare(w, rows, next);
