@@ -4,6 +4,7 @@
 #include "scan_launch.hpp"
 
 #include <algorithm>
+#include <cmath>
 
 namespace convmi {
 namespace scan {
@@ -51,7 +52,9 @@ Plan plan(ScanArgs& a, bool packed, bool gradient)
     // 2048 channels, a prompt's call (and forward with gradient): 256 rows take 15.5 us (46.7) in
     // pieces of 32, 19.6 (55.9) in pieces of 64, 28.5 (93.6) in whole; 128 rows 14.3 (42.0)
     // and 16.5 (56.8) in whole; 64 rows 13.8 (40.1) and 10.5 (38.2) in whole.
-    const int64_t most = a.rows < 128 ? 1 : a.rows / 32;
+    // A piece reads the ends of all before it, so at most as many pieces as a piece has rows
+    // (16384 rows of 64 channels: 128 pieces 57 us, 256 74 us, 512 163 us; 64 were 66 us).
+    const int64_t most = a.rows < 128 ? 1 : std::min(a.rows / 32, static_cast<int64_t>(std::sqrt(static_cast<double>(a.rows))));
     const int64_t want = std::min((2 * kSimds + waves_of(a, p.gr) - 1) / waves_of(a, p.gr), most);
     if (!packed && want <= a.seqs) return p;
     const int64_t rows = (a.rows + want - 1) / want;

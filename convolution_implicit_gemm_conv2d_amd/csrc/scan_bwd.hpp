@@ -29,23 +29,6 @@ constexpr int pow2_of(int v)
 }
 constexpr float kLn2 = 0.69314718055994531f;
 
-// What the pieces behind a share give to the gradient of its last state.
-template <int GR, int NS>
-__device__ __forceinline__ void inherit_back(const ScanArgs& a, const Lanes<GR, NS>& l, const float* A, int item, int end, float* g)
-{
-    const int64_t states = static_cast<int64_t>(a.channels) * a.n;
-    float passed = 0.f;
-    for (int q = item + 1; q < a.pieces; ++q) {
-        float e[NS];
-        l.read(a, a.ends + q * states, e);
-        const float sum = a.sums[static_cast<int64_t>(q) * a.channels + l.c];
-#pragma unroll
-        for (int j = 0; j < NS; ++j) g[j] = __builtin_fmaf(exp2_hw(A[j] * passed), e[j], g[j]);
-        passed += sum;
-        if (end <= (q + 1) * a.piece_rows) break;  // the sequence ends in that piece
-    }
-}
-
 // The gradient that a piece passes on to the row before it, from nothing behind
 // it, for the pieces in front.
 template <typename T, int GR, int NS>
@@ -165,7 +148,7 @@ __global__ __launch_bounds__(kThreads, 2) void bwd_kernel(ScanArgs a)
         if (span.end <= share.end) {
             if (a.dlast) l.read(a, a.dlast + s * states, g);
         } else {
-            inherit_back(a, l, A, item, span.end, g);
+            inherit<1>(a, l, A, item, (span.end - 1) / a.piece_rows - item, g);
         }
         const int begin = span.begin > share.begin ? span.begin : share.begin;
         const int end = span.end < share.end ? span.end : share.end;

@@ -12,24 +12,6 @@
 namespace convmi {
 namespace scan {
 
-// The state that the pieces before a share leave to its first sequence: what
-// each of them ends with, faded by the pieces between.
-template <int GR, int NS>
-__device__ __forceinline__ void inherit(const ScanArgs& a, const Lanes<GR, NS>& l, const float* A, int item, int begin, float* h)
-{
-    const int64_t states = static_cast<int64_t>(a.channels) * a.n;
-    float passed = 0.f;
-    for (int q = item - 1; q >= 0; --q) {
-        float e[NS];
-        l.read(a, a.ends + q * states, e);
-        const float sum = a.sums[static_cast<int64_t>(q) * a.channels + l.c];
-#pragma unroll
-        for (int j = 0; j < NS; ++j) h[j] = __builtin_fmaf(exp2_hw(A[j] * passed), e[j], h[j]);
-        passed += sum;
-        if (begin >= static_cast<int64_t>(q) * a.piece_rows) break;  // the sequence begins in that piece
-    }
-}
-
 // kStates: states for the gradient's tiles alone; kEnds: the state at the end of
 // a piece from nothing before it, for the pieces behind it.
 enum Want { kOutputs, kStates, kEnds };
@@ -66,7 +48,7 @@ __global__ __launch_bounds__(kThreads) void fwd_kernel(ScanArgs a)
         if (span.begin >= share.begin) {
             if (a.initial) l.read(a, a.initial + s * states, h);
         } else if (WANT != kEnds) {
-            inherit(a, l, A, item, span.begin, h);
+            inherit<-1>(a, l, A, item, item - span.begin / a.piece_rows, h);
         }
         const int begin = span.begin > share.begin ? span.begin : share.begin, end = span.end < share.end ? span.end : share.end;
         float total = 0.f;  // sum of d
