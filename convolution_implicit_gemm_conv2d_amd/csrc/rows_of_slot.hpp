@@ -11,7 +11,9 @@ namespace convmi {
 // needs, finish(row, slot) computes and stores it; absent(row) is called for a row
 // whose slot lies outside the pool.  Without slots a row's slot is its number.  All threads
 // of the workgroup call it.  The rows' own loads are out while the slots are
-// compared.
+// compared, four at a time: every workgroup reads all slots, which costs from about a thousand
+// rows on (4096 rows of 1024 channels: convolution 49 us one by one, 35 so, 19 without
+// slots; scan 247, 193 and 147).
 template <typename R, typename F, typename A>
 __device__ __forceinline__ void each_row_of_slot(const int* slots, int rows, int count, int row, R read, F finish, A absent)
 {
@@ -22,8 +24,16 @@ __device__ __forceinline__ void each_row_of_slot(const int* slots, int rows, int
     }
     read(row, slot);
     if (slots) {
-        bool other = false;
-        for (int i = threadIdx.x; i < rows; i += blockDim.x) other |= i != row && slots[i] == slot;
+        typedef int four __attribute__((ext_vector_type(4), aligned(4)));
+        int same = 0;  // rows of this slot
+        const int whole = rows & ~3;
+        for (int i = threadIdx.x * 4; i < whole; i += blockDim.x * 4) {
+            const four t = *reinterpret_cast<const four*>(slots + i);
+            same += (t.x == slot) + (t.y == slot) + (t.z == slot) + (t.w == slot);
+        }
+        if (threadIdx.x < rows - whole) same += slots[whole + threadIdx.x] == slot;
+        // its own row is one of them, found by one thread
+        const bool other = same > (row < whole ? row / 4 % blockDim.x == threadIdx.x : row - whole == threadIdx.x);
         if (__syncthreads_or(other)) {
             for (int i = 0; i < row; ++i)
                 if (slots[i] == slot) return;

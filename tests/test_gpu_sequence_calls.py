@@ -114,3 +114,24 @@ def test_a_padded_batch_of_tokens_and_many_rows():
     assert not y[9::100].any() and torch.equal(state[5], x[mine][-3:])
     alone = [r for r in range(rows) if slots[r] == r and r != 5]
     assert torch.equal(y[alone], x[alone])
+
+
+@pytest.mark.parametrize("rows", [2, 3, 4, 5, 7, 255, 1023, 1025, 2051])
+def test_the_same_slot_twice_wherever_it_stands(rows):
+    """Slots are compared four at a time, the last ones one by one, from any address."""
+    x = torch.randn(rows, 6, generator=torch.Generator().manual_seed(rows)).to(DEV)
+    b, w, A = torch.ones(rows, 2, device=DEV), torch.ones(6, 4, device=DEV), t(6, 2) - 1
+    far = {1, min(2, rows - 1), rows // 2, rows - 2, rows - 1}
+    for pair in ((i, j) for i in (0, rows // 3) for j in far if j > i):
+        i, j = pair
+        slots = torch.arange(-1, rows, dtype=torch.int32, device=DEV)[1:]
+        slots[j] = i
+        state, h = t(rows, 3, 6), t(rows, 6, 2)
+        y = cm.causal_conv_step(x, w, state, slots=slots)
+        z = cm.selective_step(x, x, A, b, b, h, slots=slots)
+        both, of = x[[i, j]], (b[[i, j]], b[[i, j]])
+        assert torch.allclose(y[[i, j]], cm.causal_conv(both, w), rtol=1e-6, atol=1e-6)
+        # a state and its two products are rounded a few times in 32 bits
+        assert torch.allclose(z[[i, j]], cm.selective_scan(both, both, A, *of), rtol=1e-5, atol=1e-5)
+        rest = [r for r in range(rows) if r not in pair]
+        assert torch.equal(y[rest], x[rest]) and not state[j].any() and not h[j].any()
