@@ -148,7 +148,7 @@ __global__ __launch_bounds__(kThreads, 2) void bwd_kernel(ScanArgs a)
         if (span.end <= share.end) {
             if (a.dlast) l.read(a, a.dlast + s * states, g);
         } else {
-            inherit<1>(a, l, A, item, (span.end - 1) / a.piece_rows - item, g);
+            inherit<1>(a, l, A, item, piece_of(a, span.end - 1) - item, g);
         }
         const int begin = span.begin > share.begin ? span.begin : share.begin;
         const int end = span.end < share.end ? span.end : share.end;

@@ -48,7 +48,7 @@ __global__ __launch_bounds__(kThreads) void fwd_kernel(ScanArgs a)
         if (span.begin >= share.begin) {
             if (a.initial) l.read(a, a.initial + s * states, h);
         } else if (WANT != kEnds) {
-            inherit<-1>(a, l, A, item, item - span.begin / a.piece_rows, h);
+            inherit<-1>(a, l, A, item, item - piece_of(a, span.begin), h);
         }
         const int begin = span.begin > share.begin ? span.begin : share.begin, end = span.end < share.end ? span.end : share.end;
         float total = 0.f;  // sum of d
