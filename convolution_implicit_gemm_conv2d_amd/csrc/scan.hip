@@ -23,10 +23,10 @@ int64_t blocks_of(const ScanArgs& a, int gr) { return (a.per_group + kWaves * (6
 // with four multiply-adds takes 31 cycles there, 23 with two waves, 20 with eight), so with
 // less than two waves for each SIMD twice the groups are better (4 x 4096 rows of 4096
 // channels, 16 states: 395 us with 4 groups, 376 with 8), and the gradient, whose
-// 256 registers leave room for two waves in any case, always takes them (8 x 2048 rows of
+// 244 registers leave room for two waves in any case, always takes them (8 x 2048 rows of
 // 2048 channels, forward and gradient: 832 us and 788).  With less than one wave for each SIMD
 // the rows are cut into pieces, which cost a pass more over them (16384 rows of 1024
-// channels: 146 us in pieces, 280 in whole).  So are packed rows always: their
+// channels: 141 us in pieces, 280 in whole).  So are packed rows always: their
 // lengths are the device's own knowledge, and one long sequence among short ones
 // would otherwise keep a few waves busy alone.
 struct Plan {

@@ -9,11 +9,14 @@
 //
 // A tile's states come again from the state in front of it (the forward pass
 // keeps one every 16 rows, 4 bytes a state of a row; going back by dividing by a
-// would not be stable) and stay in registers, factors too, so a tile costs one
-// exp2 a state and row.  Then the tile goes backwards.  About 20 issue slots a
-// state and row, four of them the sums over channels of dB and dC, which are
+// would not be stable) and stay in registers, up to two states of a lane factors
+// too.  Then the tile goes backwards.  The sums over channels of dB and dC are
 // merged over a wave's lanes in pairs, over the workgroup's waves in LDS and
 // over workgroups by a kernel of their own: no atomics, so a fixed order.
+//
+// 8 x 2048 rows of 2048 channels, 16 states, bf16: 540 to 580 us, with 835 vector
+// instructions of a wave for a tile, which keep the vector units busy 88 % of the
+// time; about a third of them are the merges.  Two waves a SIMD (244 registers).
 #pragma once
 
 #include "scan.hpp"

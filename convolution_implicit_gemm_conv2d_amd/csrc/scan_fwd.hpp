@@ -1,10 +1,12 @@
 // Forward pass of the selective scan, for one type: included by the sources
 // that build it for bf16 and for fp32.
 //
-// What a state of a row costs are its instructions: d A, exp2 (a quarter of the
-// rate), d x B, and the two multiply-adds of h and y are 8 issue slots; the
-// rows' softplus, gate and conversions add about a third at 16 states.  Memory
-// (x, delta, z, y once) takes a third of that time.
+// What a state of a row costs are its instructions: d A, exp2, d x B, and the two
+// multiply-adds of h and y take 20 cycles of a SIMD with eight waves, 22.6 with two (exp2
+// alone 8.6); the row's softplus, gate, conversions and merges come on top.  4 x 4096 rows
+// of 4096 channels, 16 states, bf16: 378 to 399 us, where the states alone are 137 at
+// eight waves and memory (x, delta, z, y once) 104.  16384 rows of 1024 channels in 32
+// pieces: 62 us for their ends and 95 for the outputs.
 #pragma once
 
 #include "scan.hpp"

@@ -10,7 +10,8 @@
 // range of rows with the last K - 1 rows (in the gradient also the last K - 1
 // dp) in registers, so every value is loaded once but for the K - 1 rows around
 // a range.  The next four rows' loads are out while four are worked on (72 -> 58
-// us for 4 x 4096 rows of 4096 channels, bf16: 4.7 TB/s).  Sequences may begin anywhere in a range.  The rows' ragged end
+// us for 4 x 4096 rows of 4096 channels, bf16: 4.7 TB/s; training step of 20011 packed rows of
+// 1544 channels: 31 us forward, 64 the gradient at two waves a SIMD, 6 the sums).  Sequences may begin anywhere in a range.  The rows' ragged end
 // repeats channels of the lane before it.
 #include "act.hpp"
 #include "kernels.hpp"

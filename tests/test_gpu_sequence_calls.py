@@ -135,3 +135,79 @@ def test_the_same_slot_twice_wherever_it_stands(rows):
         assert torch.allclose(z[[i, j]], cm.selective_scan(both, both, A, *of), rtol=1e-5, atol=1e-5)
         rest = [r for r in range(rows) if r not in pair]
         assert torch.equal(y[rest], x[rest]) and not state[j].any() and not h[j].any()
+
+
+def test_rate_or_step_alone_on_the_device():
+    p0, g = torch.linspace(-1, 1, 500, device=DEV), torch.linspace(2, -1, 500, device=DEV)
+    got = []
+    for lr, step in ((3e-3, 7), (torch.tensor(3e-3, device=DEV), 7), (3e-3, torch.tensor([7], device=DEV))):
+        p = p0.clone()
+        state = cm.adamw_state([p])
+        cm.adamw_step([p], [g], state, step, lr, weight_decay=0.2)
+        got.append(p)
+    for p in got[1:]:  # the scalars of both ways are rounded from 64 bits
+        assert torch.allclose(p, got[0], rtol=2 ** -21, atol=2 ** -30)
+
+
+def test_calls_at_once_and_graphs_in_turn():
+    """Pieces and partial sums lie in each call's own workspace."""
+    gen = torch.Generator().manual_seed(4)
+    r = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    sets, want = [], []
+    for n, L in ((1, 1500), (2, 1100), (3, 700)):
+        x, d, b, w = (r(L, 40), r(L, 40), r(L, 16), r(40, 4))
+        sets.append([v.to(DEV) for v in (x, d, -torch.rand(40, 16, generator=gen), b, b.flip(0).contiguous())] + [w.to(DEV)])
+
+    def go(x, d, A, b, c, w):
+        y = cm.causal_conv(x, w, activation="silu")
+        s = cm.selective_scan_saved(x, A)
+        z = cm.selective_scan(y, d, A, b, c, saved=s)
+        g = cm.selective_scan_grad(z, y, d, A, b, c, saved=s)
+        return [y, z, g["x"], g["A"], g["B"], *(cm.causal_conv_grad(g["x"], x, w, activation="silu")[k] for k in ("x", "weight"))]
+
+    want = [go(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = []
+    for _ in range(4):
+        for s, ins in zip(streams, sets):
+            with torch.cuda.stream(s):
+                got.append(go(*ins))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(g, want[i % len(sets)]))
+    graphs, outs, pool = [], [], None
+    for ins in sets:  # one pool of memory, as graphs that run in turn may share
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], pool=pool):
+            outs.append(go(*ins))
+        pool = pool or graphs[-1].pool()
+    for _ in range(3):
+        for graph, out, w in zip(graphs, outs, want):
+            for t_ in out:
+                t_.zero_()
+            graph.replay()
+            go(*sets[0])
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(out, w))
+
+
+def test_many_short_sequences():
+    """Packed rows of thousands of sequences come to what a batch of them does."""
+    S, L = 3000, 3
+    gen = torch.Generator().manual_seed(8)
+    x, d, b = (torch.randn(S, L, n, generator=gen).to(DEV) for n in (20, 20, 4))
+    A = -torch.rand(20, 4, generator=gen).to(DEV)
+    st = torch.arange(0, S * L + 1, L, dtype=torch.int32, device=DEV)
+    flat = [v.reshape(S * L, -1) for v in (x, d, b)]
+    w = torch.randn(20, 4, generator=gen).to(DEV)
+    assert torch.equal(cm.causal_conv(x, w).view(S * L, 20), cm.causal_conv(flat[0], w, starts=st))
+    y = cm.selective_scan(x, d, A, b, b).view(S * L, 20)
+    z = cm.selective_scan(flat[0], flat[1], A, flat[2], flat[2], starts=st)
+    # the groups of lanes that a sum goes over may differ: four states, fp32
+    assert torch.allclose(y, z, rtol=1e-5, atol=1e-5)
+    a = cm.selective_scan_grad(y.view(S, L, 20), x, d, A, b, b)
+    c = cm.selective_scan_grad(y, flat[0], flat[1], A, flat[2], flat[2], starts=st)
+    # fp32 sums over 4 states and 20 channels in another order
+    for k in ("x", "delta", "B", "C"):
+        assert torch.allclose(a[k].view(S * L, -1), c[k], rtol=1e-4, atol=1e-4 * a[k].abs().max().item())
