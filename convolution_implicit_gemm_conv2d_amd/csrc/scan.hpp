@@ -392,6 +392,17 @@ __device__ __forceinline__ int piece_of(const ScanArgs& a, int row)
     return static_cast<int>(static_cast<uint32_t>(row) / static_cast<uint32_t>(a.piece_rows));
 }
 
+// h + 2^t e.  The power alone may leave fp32's range where the product does not:
+// a state that grows over many pieces (A > 0, or steps below 0) and was 0, or
+// tiny, before them; 0 times an overflow would be no number.  There t goes into
+// the exponent of e: 2^512 and 2^-512 take any e out of range.
+__device__ __forceinline__ float faded(float t, float e, float h)
+{
+    if (fabsf(t) <= 126.0f) return __builtin_fmaf(exp2_hw(t), e, h);
+    const float c = __builtin_fminf(__builtin_fmaxf(t, -512.0f), 512.0f), k = __builtin_ceilf(c);
+    return h + __builtin_ldexpf(e * exp2_hw(c - k), static_cast<int>(k));
+}
+
 // The state that the `count` pieces before a share (DIR -1) leave to its first
 // sequence, or the gradient that those behind it (DIR 1) give to its last one:
 // what each of them ends with, faded by the pieces between.  Their ends are
@@ -415,7 +426,7 @@ __device__ __forceinline__ void inherit(const ScanArgs& a, const Lanes<GR, NS>& 
         for (int u = 0; u < U; ++u) {
             if (k + u >= count) break;
 #pragma unroll
-            for (int j = 0; j < NS; ++j) h[j] = __builtin_fmaf(exp2_hw(A[j] * passed), e[u][j], h[j]);
+            for (int j = 0; j < NS; ++j) h[j] = faded(A[j] * passed, e[u][j], h[j]);
             passed += sum[u];
         }
     }
