@@ -392,15 +392,15 @@ __device__ __forceinline__ int piece_of(const ScanArgs& a, int row)
     return static_cast<int>(static_cast<uint32_t>(row) / static_cast<uint32_t>(a.piece_rows));
 }
 
-// h + 2^t e.  The power alone may leave fp32's range where the product does not:
-// a state that grows over many pieces (A > 0, or steps below 0) and was 0, or
-// tiny, before them; 0 times an overflow would be no number.  There t goes into
-// the exponent of e: 2^512 and 2^-512 take any e out of range.
+// h + 2^(2 t) e.  The whole power leaves fp32's range where the product does not:
+// for a state that grows over many pieces (A > 0, or steps below 0) and was 0, or
+// tiny, before them, where 0 times an overflow would be no number, or that fades
+// from a large one.  Half of it does not: e is multiplied by 2^t twice, by 2^127 at
+// most, which takes any normal e there that 2^(2 t) would.
 __device__ __forceinline__ float faded(float t, float e, float h)
 {
-    if (fabsf(t) <= 126.0f) return __builtin_fmaf(exp2_hw(t), e, h);
-    const float c = __builtin_fminf(__builtin_fmaxf(t, -512.0f), 512.0f), k = __builtin_ceilf(c);
-    return h + __builtin_ldexpf(e * exp2_hw(c - k), static_cast<int>(k));
+    const float f = exp2_hw(__builtin_fminf(t, 127.0f));
+    return __builtin_fmaf(f, f * e, h);
 }
 
 // The state that the `count` pieces before a share (DIR -1) leave to its first
@@ -413,7 +413,7 @@ __device__ __forceinline__ void inherit(const ScanArgs& a, const Lanes<GR, NS>& 
 {
     constexpr int U = 4;
     const int64_t states = static_cast<int64_t>(a.channels) * a.n;
-    float passed = 0.f;
+    float passed = 0.f;  // half of the sum
     for (int k = 0; k < count; k += U) {
         float e[U][NS], sum[U];
 #pragma unroll
@@ -427,7 +427,7 @@ __device__ __forceinline__ void inherit(const ScanArgs& a, const Lanes<GR, NS>& 
             if (k + u >= count) break;
 #pragma unroll
             for (int j = 0; j < NS; ++j) h[j] = faded(A[j] * passed, e[u][j], h[j]);
-            passed += sum[u];
+            passed = __builtin_fmaf(0.5f, sum[u], passed);
         }
     }
 }
