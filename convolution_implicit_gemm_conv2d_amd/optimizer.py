@@ -45,11 +45,11 @@ def adamw_state(params, bits=32):
     and v = (scale q^2)^2 (q uint8)."""
     import torch
 
+    params = list(params)
     if bits == 32:
         return {k: [torch.zeros_like(p, dtype=torch.float32) for p in params] for k in ("m", "v")}
     if bits != 8:
         raise ValueError(f"bits must be 8 or 32; got {bits!r}")
-    params = list(params)
     zeros = lambda per, t: [torch.zeros(-(-p.numel() // per), dtype=t, device=p.device) for p in params]  # noqa: E731
     return {"m": zeros(1, torch.int8), "v": zeros(1, torch.uint8), "m_scale": zeros(BLOCK, torch.float32),
             "v_scale": zeros(BLOCK, torch.float32)}
