@@ -376,18 +376,20 @@ struct List {
     std::vector<int> dtypes;
     const at::Tensor* first = nullptr;
 
-    explicit List(PyObject* o)
+    // `one`: what an entry is.
+    List(PyObject* o, const char* one)
     {
-        if (!PyList_Check(o)) throw Refused("the gradients must be a list of tensors");
+        if (!PyList_Check(o)) throw Refused(std::string("the ") + one + "s must be a list of tensors");
         const Py_ssize_t n = PyList_GET_SIZE(o);
-        if (n == 0) throw Refused("the list of gradients is empty");
+        if (n == 0) throw Refused(std::string("the list of ") + one + "s is empty");
         narrow(n, "the number of tensors");
+        const std::string entry = std::string("an entry of the ") + one + "s";
         tensors.reserve(n);
         at.reserve(n);
         counts.reserve(n);
         dtypes.reserve(n);
         for (Py_ssize_t i = 0; i < n; ++i) {
-            const at::Tensor& t = needed(PyList_GET_ITEM(o, i), "a gradient");
+            const at::Tensor& t = needed(PyList_GET_ITEM(o, i), entry.c_str());
             if (!first) first = &t;
             dtypes.push_back(Call::code(t));
             if (!t.is_cuda() || t.device() != first->device()) throw Refused("tensors passed to convmi must be on one GPU device");
@@ -406,7 +408,7 @@ PyObject* clip(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     return guarded(n, 5, [&]() -> PyObject* {
         const bool only_norm = a[1] == Py_None;
-        List g(a[0]);
+        List g(a[0], "gradient");
         const float max_norm = static_cast<float>(PyFloat_AsDouble(a[2])), eps = static_cast<float>(PyFloat_AsDouble(a[3]));
         if (PyErr_Occurred()) return nullptr;
         std::vector<void*> out;
@@ -414,7 +416,7 @@ PyObject* clip(PyObject*, PyObject* const* a, Py_ssize_t n)
         if (!only_norm && a[1] != a[0]) {
             if (PyList_Check(a[1]) && PyList_GET_SIZE(a[1]) != PyList_GET_SIZE(a[0]))
                 throw Refused("out has " + std::to_string(PyList_GET_SIZE(a[1])) + " tensors for " + std::to_string(g.n()) + " gradients");
-            List o(a[1]);
+            List o(a[1], "output");
             if (o.counts != g.counts || o.dtypes != g.dtypes || o.first->device() != g.first->device())
                 throw Refused("the tensors of out must have the sizes, dtypes and device of the gradients");
             for (int i = 0; i < g.n(); ++i) {
@@ -820,7 +822,7 @@ int64_t blocks_of(const at::Tensor& p) { return (p.numel() + 127) / 128; }
 PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     return guarded(n, 19, [&]() -> PyObject* {
-        List p(a[0]);
+        List p(a[0], "parameter");
         const int count = p.n();
         Beside g(a[1], "grads", count, false), m(a[2], "the states' m", count, false), v(a[3], "the states' v", count, false);
         Beside ms(a[4], "the states' m_scale", count, false), vs(a[5], "the states' v_scale", count, false), copies(a[6], "copies", count, true);
@@ -877,7 +879,8 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n)
 PyObject* moments(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     return guarded(n, 7, [&]() -> PyObject* {
-        if (!PyList_Check(a[0]) || PyList_GET_SIZE(a[0]) == 0) throw Refused("the states' m must be a list of tensors");
+        if (!PyList_Check(a[0])) throw Refused("the states' m must be a list of tensors");
+        if (PyList_GET_SIZE(a[0]) == 0) throw Refused("the list of states is empty");
         const int count = narrow(PyList_GET_SIZE(a[0]), "the number of tensors");
         Beside m(a[0], "m", count, false), v(a[1], "v", count, false), ms(a[2], "m_scale", count, false), vs(a[3], "v_scale", count, false);
         Beside mo(a[4], "out's m", count, false), vo(a[5], "out's v", count, false);

@@ -57,7 +57,7 @@ def adamw_state(params, bits=32):
 
 def adamw_step(params, grads, state, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, norm=None, max_norm=1.0,
                norm_eps=1e-6, copies=None, stream=None):
-    """One AdamW step over a list of float32 and bfloat16 parameters, in place:
+    """One AdamW step over a non-empty list of float32 and bfloat16 parameters, in place:
 
         g' = g min(1, max_norm / (norm + norm_eps))     without ``norm``: g
         m = b1 m + (1 - b1) g',   v = b2 v + (1 - b2) g'^2
