@@ -369,6 +369,17 @@ PyObject* norm_grad(PyObject*, PyObject* const* a, Py_ssize_t n)
 
 // --------------------------------------------------------------- lists --
 
+// Two dense tensors whose elements lie in memory in the same order.  A dimension
+// of one entry has no say, whatever its stride is.
+bool lie_alike(const at::Tensor& a, const at::Tensor& b)
+{
+    if (a.is_contiguous() && b.is_contiguous()) return true;
+    if (a.sizes() != b.sizes()) return false;
+    for (int64_t i = 0; i < a.dim(); ++i)
+        if (a.size(i) != 1 && a.stride(i) != b.stride(i)) return false;
+    return true;
+}
+
 struct List {
     std::vector<const at::Tensor*> tensors;
     std::vector<void*> at;
@@ -420,8 +431,7 @@ PyObject* clip(PyObject*, PyObject* const* a, Py_ssize_t n)
             if (o.counts != g.counts || o.dtypes != g.dtypes || o.first->device() != g.first->device())
                 throw Refused("the tensors of out must have the sizes, dtypes and device of the gradients");
             for (int i = 0; i < g.n(); ++i) {
-                const at::Tensor &from = *g.tensors[i], &to = *o.tensors[i];
-                if (!(from.is_contiguous() && to.is_contiguous()) && (from.sizes() != to.sizes() || from.strides() != to.strides()))
+                if (!lie_alike(*g.tensors[i], *o.tensors[i]))
                     throw Refused("the tensors of out must lie in memory as the gradients do");
             }
             out = std::move(o.at);
@@ -799,8 +809,7 @@ struct Beside {
     void lies_as(const at::Tensor& p, int i, const char* name) const
     {
         const at::Tensor& t = *tensors[i];
-        const bool alike = t.sizes() == p.sizes() && t.strides() == p.strides();
-        if (t.device() != p.device() || t.numel() != p.numel() || !(alike || (t.is_contiguous() && p.is_contiguous())))
+        if (t.device() != p.device() || t.numel() != p.numel() || !lie_alike(t, p))
             throw Refused(std::string(name) + " must have the size, device and order in memory of their parameters; found " + text(t.sizes()) + " with strides " +
                           text(t.strides()) + " for " + text(p.sizes()) + " with strides " + text(p.strides()));
     }
