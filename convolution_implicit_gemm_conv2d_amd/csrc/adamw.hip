@@ -19,6 +19,7 @@
 // exactly, so codes do not depend on the roundings of the hardware's root and
 // reciprocal, and the arithmetic up to them has a fixed order of roundings, no
 // multiply-add contracted.
+#include "adamw_tables.hpp"
 #include "kernels.hpp"
 
 #include <cmath>
@@ -26,16 +27,11 @@
 namespace convmi {
 namespace {
 
-constexpr int kThreads = 256, kE = 4;  // elements of a lane
+constexpr int kThreads = kAdamThreads, kE = kAdamElements;
 constexpr float kTiny = 0x1p-100f;     // blocks below it hold zeros
 constexpr int kMostM = 127, kMostV = 255;
 
-// Elements in a chunk: four a lane of a workgroup, so that fp32 arrays are read
-// and written in whole lines.  Every chunk has a workgroup of its own, which the device
-// gives out as others end (250 M elements, 32-bit states: 2048 workgroups that walk over
-// chunks of 32768 took 1427 us, a workgroup for each 4096, 2048 and 1024 elements
-// 1204, 1128 and 1032).
-constexpr uint32_t kChunk = kThreads * kE;
+constexpr uint32_t kChunk = kAdamChunk;
 
 template <int N>
 struct Table {
@@ -336,44 +332,41 @@ bool streams(const AdamList& l)
     return bytes > kStreamBytes;
 }
 
-// One list, N tensors a launch: `go` launches one table.
+// One list, tables of N tensors: `go` launches one.
 template <int N, typename Go>
 hipError_t each_table(const AdamList& l, float* const* m_out, float* const* v_out, Go go)
 {
-    int left = 0;
-    for (int i = 0; i < l.n; ++i) left += l.counts[i] != 0;
     hipError_t e = hipSuccess;
     CallEvents events;
-    for (int i = 0; left > 0 && e == hipSuccess;) {
+    ListPlace at;
+    while (e == hipSuccess && more_chunks(l.counts, l.n, at)) {
         Table<N> t;
         t.n = 0;
-        uint64_t chunks = 0;
-        for (; i < l.n && t.n < N; ++i) {
-            if (l.counts[i] == 0) continue;
-            const uint64_t more = (l.counts[i] + kChunk - 1) / kChunk;
-            if (t.n > 0 && chunks + more > INT32_MAX) break;
-            t.m[t.n] = l.m[i];
-            t.v[t.n] = l.v[i];
-            t.ms[t.n] = l.m_scales ? l.m_scales[i] : nullptr;
-            t.vs[t.n] = l.v_scales ? l.v_scales[i] : nullptr;
-            t.count[t.n] = static_cast<uint64_t>(l.counts[i]) * 8;
+        const int sb = l.bits == 8 ? 1 : 4;  // bytes of a state
+        auto plus = [](void* p, uint64_t bytes) { return p ? static_cast<void*>(static_cast<char*>(p) + bytes) : nullptr; };
+        const uint32_t chunks = fill_table(l.counts, l.n, N, kMostChunks, at, [&](int k, int i, uint64_t first, uint64_t count, uint32_t begin) {
+            t.m[k] = plus(l.m[i], first * sb);
+            t.v[k] = plus(l.v[i], first * sb);
+            t.ms[k] = l.m_scales ? l.m_scales[i] + first / kAdamBlock : nullptr;
+            t.vs[k] = l.v_scales ? l.v_scales[i] + first / kAdamBlock : nullptr;
+            t.count[k] = count * 8;
             if (m_out) {
-                t.p[t.n] = m_out[i];
-                t.copy[t.n] = v_out[i];
-                t.g[t.n] = nullptr;
+                t.p[k] = m_out[i] + first;
+                t.copy[k] = v_out[i] + first;
+                t.g[k] = nullptr;
             } else {
-                t.p[t.n] = l.params[i];
-                t.g[t.n] = l.grads[i];
-                t.copy[t.n] = l.copies ? l.copies[i] : nullptr;
-                t.count[t.n] += (l.param_dtypes[i] == 1 ? 1 : 0) + (l.grad_dtypes[i] == 1 ? 2 : 0) + (t.copy[t.n] && l.copy_dtypes[i] == 1 ? 4 : 0);
+                const bool pb = l.param_dtypes[i] == 1, gb = l.grad_dtypes[i] == 1, cb = l.copies && l.copies[i] && l.copy_dtypes[i] == 1;
+                t.p[k] = plus(l.params[i], first * (pb ? 2 : 4));
+                t.g[k] = plus(const_cast<void*>(l.grads[i]), first * (gb ? 2 : 4));
+                t.copy[k] = l.copies ? plus(l.copies[i], first * (cb ? 2 : 4)) : nullptr;
+                t.count[k] += (pb ? 1 : 0) + (gb ? 2 : 0) + (cb ? 4 : 0);
             }
-            t.begin[t.n++] = static_cast<uint32_t>(chunks);
-            chunks += more;
-            --left;
-        }
-        t.begin[t.n] = static_cast<uint32_t>(chunks);
-        events.next(left == 0);
-        e = go(t, dim3(static_cast<unsigned>(chunks)));
+            t.begin[k] = begin;
+            t.n = k + 1;
+        });
+        t.begin[t.n] = chunks;
+        events.next(!more_chunks(l.counts, l.n, at));
+        e = go(t, dim3(chunks));
     }
     return e;
 }
