@@ -241,6 +241,23 @@ private:
     bool any_ = false;
 };
 
+// Host: a call's `blocks` workgroups of `threads` lanes in launches that a grid can
+// hold (fewer than 2^32 lanes): go(first, grid) launches those from the first on,
+// a multiple of `unit`.
+template <typename Go>
+hipError_t in_grids(int64_t blocks, int threads, int64_t unit, Go go)
+{
+    const int64_t most = ((int64_t(1) << 32) - 1) / threads / unit * unit;
+    hipError_t e = hipSuccess;
+    CallEvents events;
+    for (int64_t first = 0; first < blocks && e == hipSuccess; first += most) {
+        const int64_t n = blocks - first < most ? blocks - first : most;
+        events.next(first + n == blocks);
+        e = go(first, dim3(static_cast<unsigned>(n)));
+    }
+    return e;
+}
+
 // Host: launches `kernel` on stream `s`.  If events are armed, the launch goes
 // through hipExtLaunchKernel so that the runtime stamps the kernel's own start
 // and end into them (no extra packets on the stream), and the events are

@@ -98,9 +98,9 @@ struct Step {
 };
 
 template <typename T, int U, bool WHOLE>
-__global__ __launch_bounds__(256) void step_kernel(ScanArgs a, float* state, int count, int lanes, int blocks)
+__global__ __launch_bounds__(256) void step_kernel(ScanArgs a, float* state, int count, int lanes, int blocks, int row0)
 {
-    const int row = static_cast<int>(blockIdx.x / blocks);
+    const int row = row0 + static_cast<int>(blockIdx.x / blocks);
     const int at = static_cast<int>(blockIdx.x % blocks) * (256 * U) + threadIdx.x;
     const int c = at / lanes, apart = 256 / lanes, first = (at & (lanes - 1)) * kPer;
     Step<T, U, WHOLE> step;
@@ -134,9 +134,10 @@ hipError_t launch_scan_step(const ScanArgs& a, float* state, int count, int dtyp
     const int64_t all = static_cast<int64_t>(a.channels) * lanes, half = (all + 511) / 512;
     const bool two = half * a.rows >= 1024;
     const int64_t blocks = two ? half : (all + 255) / 256;
-    if (blocks * a.rows >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
     auto kernel = dtype ? scan::kernel_of<bf16_t>(two, a.n % scan::kPer == 0) : scan::kernel_of<float>(two, a.n % scan::kPer == 0);
-    return launch(kernel, dim3(static_cast<unsigned>(blocks * a.rows)), dim3(256), 0, s, a, state, count, lanes, static_cast<int>(blocks));
+    return in_grids(blocks * a.rows, 256, blocks, [&](int64_t first, dim3 grid) {
+        return launch(kernel, grid, dim3(256), 0, s, a, state, count, lanes, static_cast<int>(blocks), static_cast<int>(first / blocks));
+    });
 }
 
 }  // namespace convmi

@@ -400,9 +400,9 @@ __global__ __launch_bounds__(kThreads) void causal_bwd_kernel(CausalArgs a, int6
 
 // A row each of many sequences; the K - 1 rows before it in a slot of a pool.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void causal_step_kernel(CausalArgs a, int count, int blocks)
+__global__ __launch_bounds__(kThreads) void causal_step_kernel(CausalArgs a, int count, int blocks, int row0)
 {
-    const int row = static_cast<int>(blockIdx.x / blocks), c = static_cast<int>(blockIdx.x % blocks) * kThreads + threadIdx.x;
+    const int row = row0 + static_cast<int>(blockIdx.x / blocks), c = static_cast<int>(blockIdx.x % blocks) * kThreads + threadIdx.x;
     const bool on = c < a.C;
     const int K = a.K, cc = on ? c : 0;  // lanes behind the last channel read the first one
     T x = T(0), old[kCausalTaps - 1], w[kCausalTaps], b = T(0);
@@ -487,25 +487,43 @@ size_t causal_bwd_workspace(int64_t rows, int C, int K)
         if (vector_of(a) == 4) { CONVMI_TAPS(float, 4, KERNEL, GO) } else { CONVMI_TAPS(float, 1, KERNEL, GO) }   \
     }
 
+// The launches of `ranges` ranges and then `states` sequences' states, `vecs` lanes
+// each, as a grid holds them (fewer than 2^32 lanes; the ranges alone have 2^18, or
+// rows * channels / 512).  A later launch is given the ranges less what is behind
+// it, a negative number, and so goes on at a sequence.
+template <typename Go>
+hipError_t each_grid(int64_t ranges, int64_t states, int64_t vecs, CallEvents& events, bool last, Go go)
+{
+    constexpr int64_t kMost = (int64_t(1) << 32) - kThreads;
+    if (ranges > kMost / vecs) return hipErrorInvalidConfiguration;
+    hipError_t e = hipSuccess;
+    for (int64_t lanes; ranges + states > 0 && e == hipSuccess; ranges -= lanes / vecs) {
+        const int64_t all = (ranges + states) * vecs;
+        lanes = all < kMost ? all : kMost;
+        events.next(last && lanes == all);
+        e = go(ranges, dim3(static_cast<unsigned>((lanes + kThreads - 1) / kThreads)));
+    }
+    return e;
+}
+
 hipError_t launch_causal_fwd(CausalArgs a, int dtype, hipStream_t s)
 {
     plan(a);
     const int64_t ranges = (a.rows + a.per - 1) / a.per, vecs = (a.C + vector_of(a) - 1) / vector_of(a);
-    const int64_t blocks = ((ranges + (a.last ? a.seqs : 0)) * vecs + kThreads - 1) / kThreads;
-    if (blocks == 0) return hipSuccess;
-    if (blocks >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
-    hipError_t e = hipSuccess;
-#define GO(k) launch(k, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, s, a, ranges, static_cast<int>(vecs))
-    CONVMI_CAUSAL(causal_fwd_kernel, GO)
-    return e;
+    CallEvents events;
+    return each_grid(ranges, a.last ? a.seqs : 0, vecs, events, true, [&](int64_t at, dim3 grid) {
+        hipError_t e = hipSuccess;
+#define GO(k) launch(k, grid, dim3(kThreads), 0, s, a, at, static_cast<int>(vecs))
+        CONVMI_CAUSAL(causal_fwd_kernel, GO)
+        return e;
+    });
 }
 
 hipError_t launch_causal_bwd(CausalArgs a, void* dw, void* db, int dtype, void* workspace, hipStream_t s)
 {
     plan(a);
     const int64_t ranges = (a.rows + a.per - 1) / a.per, vecs = (a.C + vector_of(a) - 1) / vector_of(a);
-    const int64_t blocks = ((ranges + (a.dinitial ? a.seqs : 0)) * vecs + kThreads - 1) / kThreads;
-    if (blocks >= (int64_t(1) << 31) || ranges >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
+    if (ranges >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
     a.part_w = static_cast<float*>(workspace);
     a.part_b = reinterpret_cast<float*>(static_cast<char*>(workspace) + up(static_cast<size_t>(ranges) * a.C * a.K * 4));
     SumArgs sums{};
@@ -513,13 +531,12 @@ hipError_t launch_causal_bwd(CausalArgs a, void* dw, void* db, int dtype, void* 
     if (dw) add_sum(sums, a.part_w, wn, wn, static_cast<int>(ranges), dw);
     if (db) add_sum(sums, a.part_b, a.C, a.C, static_cast<int>(ranges), db);
     CallEvents events;
-    hipError_t e = hipSuccess;
-    if (blocks > 0) {
-        events.next(!sums.jobs);
+    const hipError_t rc = each_grid(ranges, a.dinitial ? a.seqs : 0, vecs, events, !sums.jobs, [&](int64_t at, dim3 grid) {
+        hipError_t e = hipSuccess;
         CONVMI_CAUSAL(causal_bwd_kernel, GO)
-        if (e != hipSuccess) return e;
-    }
-    if (!sums.jobs) return e;
+        return e;
+    });
+    if (rc != hipSuccess || !sums.jobs) return rc;
     events.next(true);
     return launch_sums(sums, dtype, s);
 }
@@ -529,9 +546,10 @@ hipError_t launch_causal_step(const CausalArgs& a, int count, int dtype, hipStre
 {
     if (a.rows == 0) return hipSuccess;
     const int64_t blocks = (a.C + kThreads - 1) / kThreads;
-    if (blocks * a.rows >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
-    return launch(dtype ? causal_step_kernel<bf16_t> : causal_step_kernel<float>, dim3(static_cast<unsigned>(blocks * a.rows)), dim3(kThreads), 0, s,
-                  a, count, static_cast<int>(blocks));
+    return in_grids(blocks * a.rows, kThreads, blocks, [&](int64_t first, dim3 grid) {
+        return launch(dtype ? causal_step_kernel<bf16_t> : causal_step_kernel<float>, grid, dim3(kThreads), 0, s, a, count, static_cast<int>(blocks),
+                      static_cast<int>(first / blocks));
+    });
 }
 
 }  // namespace convmi
