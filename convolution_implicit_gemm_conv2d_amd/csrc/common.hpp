@@ -261,11 +261,14 @@ hipError_t in_grids(int64_t blocks, int threads, int64_t unit, Go go)
 // Host: launches `kernel` on stream `s`.  If events are armed, the launch goes
 // through hipExtLaunchKernel so that the runtime stamps the kernel's own start
 // and end into them (no extra packets on the stream), and the events are
-// disarmed.  Returns the launch status.
+// disarmed.  Returns the launch status.  A grid of 2^32 lanes or more in one
+// dimension is refused here: the runtime reports nothing and leaves lanes out.
 template <typename... Params, typename... Args>
 hipError_t launch(void (*kernel)(Params...), dim3 grid, dim3 block, size_t lds, hipStream_t s,
                   Args... args)
 {
+    for (const uint64_t lanes : {uint64_t(grid.x) * block.x, uint64_t(grid.y) * block.y, uint64_t(grid.z) * block.z})
+        if (lanes >> 32) return hipErrorInvalidConfiguration;
     clear_stale_error();
     ArmedEvents& ev = armed_events();
     if (ev.start || ev.stop) {
