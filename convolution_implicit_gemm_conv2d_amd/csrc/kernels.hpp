@@ -181,9 +181,13 @@ struct ScanArgs {
     int64_t rows, len;                 // len: rows of each sequence, without starts
     int64_t xs, ds, zs, bs, cs;        // elements from one row to the next
     int64_t piece_rows;
+    int64_t part_rows;                 // rows of part_bc
+    int64_t sum_rows, row0;            // rows that a launch of the sums of dB and dC adds up, and the first of them
     int seqs, channels, n, groups, per_group;
     int blocks;                        // workgroups of a group's channels
-    int pieces;                        // 0: a workgroup a sequence
+    int pieces;                        // 0: whole sequences, `walk` of them a workgroup
+    int walk, seq0;                    // seq0: the first sequence of a launch
+    int launch_seqs;                   // sequences of a launch of the gradient
     int softplus, act, clear;          // clear: rows of no sequence become zeros
 };
 struct ScanGrads {

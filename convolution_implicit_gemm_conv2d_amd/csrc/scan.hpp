@@ -357,7 +357,7 @@ __device__ __forceinline__ int first_of(const ScanArgs& a, int row)
     return lo;
 }
 
-// A workgroup's share of the rows: one sequence, or a piece of all rows with
+// A workgroup's share of the rows: some whole sequences, or a piece of all rows with
 // the sequences [first, last) that have rows in it (empty ones count where they lie).
 struct Share {
     int begin, end, first, last;
@@ -366,12 +366,11 @@ struct Share {
     __device__ Share(const ScanArgs& a, int item) : pieces(a.pieces > 0)
     {
         if (!pieces) {
-            const Span s = span_of(a, item);
-            begin = s.begin;
-            end = s.end;
-            first = item;
-            last = item + 1;
-            end_of_all = item + 1 == a.seqs;
+            first = a.seq0 + item * a.walk;
+            last = a.seqs - first > a.walk ? first + a.walk : a.seqs;
+            begin = span_of(a, first).begin;
+            end = span_of(a, last - 1).end;
+            end_of_all = last == a.seqs;
             return;
         }
         const int64_t from = static_cast<int64_t>(item) * a.piece_rows, to = from + a.piece_rows;

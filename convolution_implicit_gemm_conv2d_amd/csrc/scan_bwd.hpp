@@ -310,7 +310,7 @@ __global__ __launch_bounds__(kThreads, 2) void bwd_kernel(ScanArgs a)
             // The workgroup's sum of dB and dC; the other half of the buffer
             // is the next tile's, so one barrier a tile is enough.
             lds_barrier();
-            float* out = a.part_bc + (static_cast<int64_t>(block) * a.rows + to) * 2 * a.n;
+            float* out = a.part_bc + (static_cast<int64_t>(block) * a.part_rows + to) * 2 * a.n;
 #pragma unroll
             for (int q = 0; q < (kTile * 2 * NP + kThreads - 1) / kThreads; ++q) {
                 const int e = threadIdx.x + q * kThreads, row = e / (2 * NP), in = e % (2 * NP), n = in % NP;
@@ -323,15 +323,25 @@ __global__ __launch_bounds__(kThreads, 2) void bwd_kernel(ScanArgs a)
         }
         if (a.dinitial && span.begin >= share.begin) l.write(a, a.dinitial + s * states, g);
     }
-    l.write(a, a.part_a + item * states, dA);
 #pragma unroll
     for (int dist = 32; dist >= CH; dist >>= 1) {
         dskip += __shfl_xor(dskip, dist);
         dbias += __shfl_xor(dbias, dist);
     }
+    float* part_a = a.part_a + item * states;
+    const int64_t at_c = static_cast<int64_t>(item) * a.channels + l.c;
+    if (a.seq0 > 0) {  // what the launch before has left there
+        float before[NS];
+        l.read(a, part_a, before);
+#pragma unroll
+        for (int j = 0; j < NS; ++j) dA[j] += before[j];
+        dskip += a.part_d[at_c];
+        dbias += a.part_bias[at_c];
+    }
+    l.write(a, part_a, dA);
     if (l.grp == 0 && l.on) {
-        a.part_d[static_cast<int64_t>(item) * a.channels + l.c] = dskip;
-        a.part_bias[static_cast<int64_t>(item) * a.channels + l.c] = dbias;
+        a.part_d[at_c] = dskip;
+        a.part_bias[at_c] = dbias;
     }
     if (a.clear && a.starts) {  // rows of no sequence
         auto clear = [&](int64_t from, int64_t to) {
@@ -348,11 +358,11 @@ __global__ __launch_bounds__(kThreads, 2) void bwd_kernel(ScanArgs a)
 template <typename T>
 __global__ __launch_bounds__(256) void sum_bc_kernel(ScanArgs a)
 {
-    const int64_t one = a.rows * 2 * a.n, at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    const int64_t one = a.part_rows * 2 * a.n, at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     const int group = blockIdx.y;
-    if (at >= one) return;
-    const int64_t row = at / (2 * a.n);
-    const int in = static_cast<int>(at - row * 2 * a.n), n = in % a.n;
+    if (at >= a.sum_rows * 2 * a.n) return;
+    const int64_t in_launch = at / (2 * a.n), row = a.row0 + in_launch;
+    const int in = static_cast<int>(at - in_launch * 2 * a.n), n = in % a.n;
     void* to = in < a.n ? a.dB : a.dC;
     if (!to) return;
     bool there = true;

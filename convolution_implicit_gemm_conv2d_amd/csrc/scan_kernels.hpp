@@ -14,11 +14,11 @@ hipError_t run_one(int run, const ScanArgs& a, int items, hipStream_t s)
     constexpr bool kGradient = NS != 3 && (GR > 4 || NS == 1);  // what the plan takes for it
     const int64_t blocks = static_cast<int64_t>(a.groups) * a.blocks * items;
     if (run == kRunSums) {
-        const int64_t n = (a.rows * 2 * a.n + 255) / 256;
-        if (n >= (int64_t(1) << 31) || a.groups > 65535) return hipErrorInvalidConfiguration;
+        const int64_t n = (a.sum_rows * 2 * a.n + 255) / 256;
+        if (a.groups > 65535) return hipErrorInvalidConfiguration;
         return launch(sum_bc_kernel<T>, dim3(static_cast<unsigned>(n), a.groups), dim3(256), 0, s, a);
     }
-    if (blocks >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
+    if (blocks > kMostBlocks) return hipErrorInvalidConfiguration;
     const dim3 grid(static_cast<unsigned>(blocks)), threads(kThreads);
     switch (run) {
     case kRunOutputs: return launch(fwd_kernel<T, GR, NS, kOutputs>, grid, threads, 0, s, a);

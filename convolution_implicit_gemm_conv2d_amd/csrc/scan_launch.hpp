@@ -6,6 +6,8 @@
 namespace convmi {
 namespace scan {
 
+constexpr int64_t kMostBlocks = (int64_t(1) << 24) - 1;  // of 256 lanes: a grid holds fewer than 2^32
+
 enum Run { kRunOutputs, kRunStates, kRunEnds, kRunBack, kRunGradient, kRunSums };
 
 // One launch over `items` shares of the rows with `gr` groups of `ns` states.
