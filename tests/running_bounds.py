@@ -75,6 +75,8 @@ def act(a, kind):
         return a, B(torch.ones_like(x))
     if kind == "relu":
         return B(x.clamp(min=0), a.e * (x > 0)), B((x > 0).double())
+    if kind in ("gelu", "gelu_tanh"):
+        return gelu(a, kind)
     p = torch.sigmoid(x)
     if kind == "sigmoid":
         v, d, dd = p, p * (1 - p), p
@@ -87,6 +89,44 @@ def act(a, kind):
         raise ValueError(kind)
     n = 2 * x.abs() + 12
     return B(v, a.e * d.abs() + n * v.abs()), B(d, a.e * dd + n * (d.abs() + dd))
+
+
+def gelu(a, kind):
+    """Both forms of it, and their derivatives.
+
+    The normal distribution's tail is exp(-t^2 / 2) times a fitted polynomial in a
+    reciprocal: the exponent's three roundings move the exponential by 3 t^2 / 2 units
+    relative, itself two more; fit (2), reciprocal (2), eight multiply-adds (their terms
+    cancel to a third at worst) and products: 40 in all.  t Phi(t) is max(t, 0) less |t|
+    times the tail.
+
+    The tanh form is t times the logistic function of w = 2 k (t + c t^3): six
+    roundings of w, the exponential's two |w| / 2 and two more, sum and reciprocal
+    come to (1 - p) 8 |w| + 4 units relative.
+
+    Exponentials and reciprocals below 2^-126 are zeros: off by that much, times what
+    they are multiplied by."""
+    t = a.v
+    least = 2.0 ** -126 / U32 * (1 + t.abs())
+    if kind == "gelu":
+        tail = torch.erfc(t.abs() * math.sqrt(0.5)) / 2
+        p, dense = torch.where(t < 0, tail, 1 - tail), torch.exp(-t * t / 2) / math.sqrt(2 * math.pi)
+        n = 1.5 * t * t + 40
+        v, d = t * p, p + t * dense
+        ev = t.abs() * tail * n + v.abs() + t.abs() * tail + least
+        ed = tail * n + (t * dense).abs() * n + 2 * (p + (t * dense).abs()) + least
+    else:
+        k, c = math.sqrt(2 / math.pi), 0.044715
+        w = 2 * k * (t + c * t ** 3)
+        p, slope = torch.sigmoid(w), 2 * k * (1 + 3 * c * t * t)
+        n = torch.sigmoid(-w) * 8 * w.abs() + 4
+        second = t * p * torch.sigmoid(-w) * slope
+        v, d = t * p, p + second
+        ev = v.abs() * (n + 2) + least
+        # 1 - p is off by what p is, and a rounding
+        ed = p * n + (t * p * slope).abs() * (p * n + 1) * (w.abs() < 25) + second.abs() * (n + 8) + p + second.abs() + least * (1 + slope)
+    # both second derivatives stay below 1
+    return B(v, a.e * d.abs() + ev), B(d, a.e + ed)
 
 
 def within(name, got, want, also=0.0):
