@@ -201,7 +201,9 @@ __device__ __forceinline__ void encode(const float* m, const float* v, uint32_t&
     // The hardware's root takes denormal values for 0: small blocks' v are lifted.
     const bool small = sv < 0x1p-40f;
     const float lift = small ? 0x1p64f : 1.0f;
-    // No scale, or one that is no number: all codes are 0.
+    // No scale, or one that is no number: all codes are 0, but for a positive v under an
+    // infinite scale, which keeps its 1.  Either way a block whose scale is not finite
+    // stands for no finite value: 0 times it is NaN.
     const float im = km > 0.f ? __builtin_amdgcn_rcpf(km) : 0.f, iv = kv > 0.f ? __builtin_amdgcn_rcpf(kv) * (small ? 0x1p-32f : 1.0f) : 0.f;
     const float most_m = km > 0.f && km < __builtin_inff() ? kMostM : 0.f, most_v = kv > 0.f && kv < __builtin_inff() ? kMostV : 0.f;
     qm = qv = 0;
