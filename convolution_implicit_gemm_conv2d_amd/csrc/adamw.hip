@@ -44,6 +44,11 @@ struct Table {
 };
 constexpr int kTensors = 48;
 static_assert(sizeof(Table<kTensors>) + 128 <= 4096, "the table is a kernel argument");
+// Lists that fit a table of a KiB take one: a launch hands its whole argument to the
+// device, whatever is in it (a tensor of 1000 elements 5.2 us so and 5.9 with the large
+// table, 12 of them 6.5 and 6.9).
+constexpr int kFewTensors = 14;
+static_assert(sizeof(Table<kFewTensors>) <= 1024 && sizeof(Table<kFewTensors + 1>) > 1024, "as many as a KiB holds");
 
 struct Rates {
     double lr, log_b1, log_b2;         // for device values
@@ -403,7 +408,7 @@ hipError_t launch_adamw(const AdamList& l, const AdamRates& a, hipStream_t s)
         auto kernel = l.bits == 8 ? (stream ? adamw_kernel<8, N, true> : adamw_kernel<8, N, false>) : stream ? adamw_kernel<32, N, true> : adamw_kernel<32, N, false>;
         return each_table<N>(l, nullptr, nullptr, [&](const Table<N>& t, dim3 grid) { return launch(kernel, grid, dim3(kThreads), 0, s, t, r); });
     };
-    return l.n <= 12 ? run(std::integral_constant<int, 12>{}) : run(std::integral_constant<int, kTensors>{});
+    return l.n <= kFewTensors ? run(std::integral_constant<int, kFewTensors>{}) : run(std::integral_constant<int, kTensors>{});
 }
 
 hipError_t launch_adamw_moments(const AdamList& l, float* const* m_out, float* const* v_out, hipStream_t s)
@@ -413,7 +418,7 @@ hipError_t launch_adamw_moments(const AdamList& l, float* const* m_out, float* c
         constexpr int N = decltype(small)::value;
         return each_table<N>(l, m_out, v_out, [&](const Table<N>& t, dim3 grid) { return launch(stream ? moments_kernel<N, true> : moments_kernel<N, false>, grid, dim3(kThreads), 0, s, t); });
     };
-    return l.n <= 12 ? run(std::integral_constant<int, 12>{}) : run(std::integral_constant<int, kTensors>{});
+    return l.n <= kFewTensors ? run(std::integral_constant<int, kFewTensors>{}) : run(std::integral_constant<int, kTensors>{});
 }
 
 }  // namespace convmi
