@@ -350,7 +350,7 @@ __device__ __forceinline__ int first_of(const ScanArgs& a, int row)
 {
     int lo = 0, hi = a.seqs;
     while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
+        const int mid = lo + ((hi - lo) >> 1);  // lo + hi may pass 2^31
         const Span s = span_of(a, mid);
         if (s.end > row || s.begin >= row) hi = mid; else lo = mid + 1;
     }

@@ -110,7 +110,7 @@ __device__ __forceinline__ int first_of(const CausalArgs& a, int64_t row)
     if (!a.starts) return static_cast<int>(row / a.len);
     int lo = 0, hi = a.seqs;
     while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
+        const int mid = lo + ((hi - lo) >> 1);  // lo + hi may pass 2^31
         if (span_of(a, mid).end > row) hi = mid; else lo = mid + 1;
     }
     return lo;

@@ -58,3 +58,13 @@ def test_tokens():
     small = cut(h)
     y = cm.selective_step(x, delta, A, b, b, h)
     ends("scan", (y, cm.selective_step(cut(x), cut(delta), A, cut(b), cut(b), small)), (h, small))
+
+
+def test_more_packed_sequences_than_half_of_all():
+    S = (1 << 30) + 100_000  # sequences of a row each: their number doubled passes 2^31
+    x, w, b = rand(S, 1, seed=1), torch.tensor([[3.0, 0.5]], device=DEV, dtype=BF16), torch.ones(1, device=DEV, dtype=BF16)
+    starts = torch.arange(S + 1, dtype=torch.int32, device=DEV)
+    last = torch.empty(S, 1, 1, device=DEV, dtype=BF16)
+    y = cm.causal_conv(x, w, b, starts=starts, last=last)
+    for cut in (slice(0, END), slice(S // 2, S // 2 + END), slice(S - END, S)):
+        assert torch.equal(y[cut], (x[cut].float() * 0.5 + 1).to(BF16)) and torch.equal(last[cut, 0], x[cut])
