@@ -9,8 +9,8 @@
 // 8-bit states: 10).  Clipping by a norm in hand costs a factor here, where
 // clip_gradients is a pass of its own.  One launch takes a table of up to 48
 // tensors as its argument and has a workgroup for each chunk of them.  250 M elements
-// of mixed types: 1077 us with 32-bit states (6.0 TB/s); 827 with 8-bit ones, which their
-// roots and borders bound, and 520 to read those out.
+// of mixed types: 1075 to 1100 us with 32-bit states (5.9 TB/s); 795 to 825 with 8-bit ones,
+// which their roots and borders bound, and 505 to 520 to read those out.
 //
 // 8 bits: 128 elements, on 32 lanes, share a scale.  m is the scale times q |q|
 // and the root of v the scale times q^2: steps next to the largest value are

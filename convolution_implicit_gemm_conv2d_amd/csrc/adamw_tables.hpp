@@ -13,9 +13,9 @@ namespace convmi {
 
 // Elements in a chunk: four a lane of a workgroup, so that fp32 arrays are read
 // and written in whole lines.  Every chunk has a workgroup of its own, which the device
-// gives out as others end (250 M elements, 32-bit states: 2048 workgroups that walk over
-// chunks of 32768 took 1427 us, a workgroup for each 4096, 2048 and 1024 elements
-// 1204, 1128 and 1032).
+// gives out as others end (250 M elements, 32-bit states, in one comparison: 2048
+// workgroups that walk over chunks of 32768 took 1427 us, a workgroup for each 4096,
+// 2048 and 1024 elements 1204, 1128 and 1032; cards and runs differ by 5 %).
 constexpr int kAdamThreads = 256, kAdamElements = 4;  // of a lane
 constexpr uint32_t kAdamChunk = kAdamThreads * kAdamElements;
 constexpr uint32_t kMostChunks = (uint32_t(1) << 24) - 1;

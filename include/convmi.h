@@ -596,7 +596,9 @@ int conv_causal_step(const void *x, const void *w, const void *bias,
  *   x, delta, z, y [rows, channels]; z NULL: no gate (act unused).
  *   B, C [rows, groups, N]: `groups` divides channels, consecutive
  *   channels / groups channels share a group.
- *   A [channels, N], D, delta_bias [channels] (or NULL): fp32, finite.
+ *   A [channels, N], D, delta_bias [channels] (or NULL): fp32, finite.  Each
+ *   row's factor exp(d A) is an fp32 value: where it overflows (d A past 88),
+ *   so does what it is multiplied by, a state of 0 included.
  *   initial, last : fp32 [seqs, channels, N], the state before each sequence
  *   and the one behind it; either may be NULL.
  *   saved : receives states for conv_scan_bwd, conv_scan_saved_size bytes; NULL
@@ -623,7 +625,9 @@ int conv_scan_fwd(const void *x, const void *delta, const float *A,
  *   saved : as conv_scan_fwd wrote it for the same inputs, or NULL: the states
  *   are computed again.
  *   workspace : 16-byte aligned, at least conv_scan_bwd_workspace_size bytes
- *   for this call's choice of `saved`.
+ *   for this call's choice of `saved` (many sequences: about a GiB; a few long
+ *   ones and packed rows: N / 4 bytes a value of x up to 32 states, N / 2 beyond;
+ *   without `saved` the bytes of conv_scan_saved_size more).
  */
 int conv_scan_bwd(const void *dy, const float *dlast, const void *x,
                   const void *delta, const float *A, const void *B,
@@ -682,7 +686,9 @@ int conv_scan_step(const void *x, const void *delta, const float *A,
  *   A block's scale fits its largest value to the largest byte, values go to
  *   the nearest byte on the line of q (borders at (q + 1/2)^2 times the scale;
  *   a positive v to 1 at least), and blocks whose largest value is below
- *   2^-100 hold zeros.  p' is computed before m' and v' are rounded.
+ *   2^-100 hold zeros.  What a block with an infinity or NaN in its new m (or v)
+ *   stands for is not finite, all of it.  p' is computed before m' and v' are
+ *   rounded.
  *   norm : one fp32 value on the device (conv_grad_norm's), or NULL.
  *   lr_dev, step_dev : one fp32 and one int64 value on the device that replace
  *   lr and step where not NULL (for a captured graph); step counts from 1.
