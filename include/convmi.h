@@ -626,8 +626,9 @@ int conv_scan_fwd(const void *x, const void *delta, const float *A,
  *   are computed again.
  *   workspace : 16-byte aligned, at least conv_scan_bwd_workspace_size bytes
  *   for this call's choice of `saved` (many sequences: about a GiB; a few long
- *   ones and packed rows: N / 4 bytes a value of x up to 32 states, N / 2 beyond;
- *   without `saved` the bytes of conv_scan_saved_size more).
+ *   ones and packed rows, for 32 channels a group or more: N / 4 bytes a value
+ *   of x up to 32 states, N / 2 beyond; without `saved` the bytes of
+ *   conv_scan_saved_size more).
  */
 int conv_scan_bwd(const void *dy, const float *dlast, const void *x,
                   const void *delta, const float *A, const void *B,
