@@ -579,7 +579,9 @@ int conv_causal_bwd_workspace_size(long long rows, int C, int K, int dtype,
  *   slots : rows int32 values on the device, or NULL for slots[r] = r.
  *   A slot outside [0, count) marks a row without a sequence: its output is
  *   left as it was (zeros with `clear`).  Rows of the same slot are taken in
- *   their order, as consecutive rows of one sequence.
+ *   their order, as consecutive rows of one sequence.  Every row's slot is
+ *   compared with all others: with slots, a call's time grows with the square
+ *   of its rows, noticeably from about a thousand on.
  */
 int conv_causal_step(const void *x, const void *w, const void *bias,
                      void *state, const int *slots, void *y, long long rows,
